@@ -295,6 +295,125 @@ ar_result_t ar_comm_set_streaming(ar_comm_t comm, int enable);
  * timed yet. */
 ar_result_t ar_last_step_times_ms(ar_comm_t comm, float* out, int cap, int* nsteps);
 
+/* ---- language-model operators around the gradient all-reduce -------------
+ *
+ * What a training step does next to the all-reduce: the global norm of the
+ * gradients and their clip, the embedding at one end of the model and the
+ * softmax cross entropy of the linear head at the other, whose gradients are
+ * the largest tensors of a data-parallel bucket.
+ *
+ * The clip calls carry every rank's buffers, as ar_all_reduce_multi; the
+ * embedding and cross-entropy calls work on one rank's data (a rank's forward
+ * or backward pass) and take the comm for its device and workspace. Types are
+ * fp32, fp16 and bf16 (int32: UNSUPPORTED). All calls are stream-ordered,
+ * deterministic and capture-safe, and allocate no device memory. Calls that
+ * need a workspace take the comm's (ar_comm_set_workspace), of at least the
+ * size that the operator's ..._workspace_bytes gives, else INVALID_ARGUMENT;
+ * what they leave in it is of no further use. Row pitches (ld_...) are in
+ * elements, 0 meaning the row length. Buffers that a call writes may overlap
+ * none that it reads or writes (and not the workspace) except where a call
+ * says so; anything else is INVALID_ARGUMENT. */
+
+/* Type of token and target numbers. */
+typedef enum { AR_INDEX_INT32 = 0, AR_INDEX_INT64 = 1 } ar_index_t;
+
+/* Norm over all elements: sqrt(sum x^2), or max |x|. */
+typedef enum { AR_NORM_L2 = 0, AR_NORM_INF = 1 } ar_norm_t;
+
+/* How the ranks hold the gradients. REPLICATED: every rank the same values,
+ * as after an all-reduce; the norm is rank 0's, only rank 0's send buffers are
+ * read, and every rank's recv buffers get its clipped values. SHARDED: every
+ * rank its own part, as after a reduce-scatter; the norm goes over all ranks'
+ * elements. */
+typedef enum { AR_GRADS_REPLICATED = 0, AR_GRADS_SHARDED = 1 } ar_grads_t;
+
+/* Workspace of the three calls below; the same for every size. */
+size_t ar_clip_workspace_bytes(void);
+
+/* *norm_out (device) = the norm of all gradients, rounded from fp64 sums of
+ * fp64 squares, so that neither squares beyond fp32's range nor small
+ * gradients beside large ones are lost. Tensor t of rank r is
+ * grads[t*nranks + r] with counts[t] elements. NaN where an element is NaN; 0
+ * over no elements. */
+ar_result_t ar_grad_norm(ar_comm_t comm, int ntensors, const void* const grads[], const size_t counts[],
+                         ar_dtype_t dtype, ar_grads_t layout, ar_norm_t norm, float* norm_out, hipStream_t stream);
+
+/* Clips gradients to a global norm: recv = send * min(1, max_norm / (norm +
+ * 1e-6)), the factor rounded once to fp32 and the product once to dtype. An
+ * infinite norm gives the factor 0 (finite elements become 0, infinite ones
+ * NaN), a NaN norm makes every element NaN; norm_out (device, may be NULL)
+ * tells. max_norm: at least 0, may be infinite. In place per tensor and rank
+ * (send == recv) is allowed. */
+ar_result_t ar_clip_grads(ar_comm_t comm, int ntensors, const void* const sendbufs[], void* const recvbufs[],
+                          const size_t counts[], ar_dtype_t dtype, ar_grads_t layout, ar_norm_t norm, double max_norm,
+                          float* norm_out, hipStream_t stream);
+
+/* ar_all_reduce_multi (SUM or AVG; other ops UNSUPPORTED) and ar_clip_grads of
+ * its replicated result as one call, bit for bit, in fewer passes: the
+ * reduction writes one copy and its norm, the clip reads that copy and writes
+ * every rank's: 2(N+1)S bytes where the two calls move (3N+2)S. In place per
+ * tensor and rank is allowed. */
+ar_result_t ar_all_reduce_clip(ar_comm_t comm, int ntensors, const void* const sendbufs[], void* const recvbufs[],
+                               const size_t counts[], ar_dtype_t dtype, ar_op_t op, ar_norm_t norm, double max_norm,
+                               float* norm_out, hipStream_t stream);
+
+/* Embedding lookup: out[t] = weight[tokens[t] - first_row] * scale, the product
+ * in fp32 and rounded once; a row of zeros where tokens[t] - first_row is not
+ * in [0, rows). weight holds rows first_row .. first_row + rows - 1 of the
+ * vocabulary: where ranks share one, an all-reduce (SUM) of their outputs is
+ * the whole lookup. No workspace. */
+ar_result_t ar_embedding(ar_comm_t comm, const void* weight, const void* tokens, ar_index_t index, void* out,
+                         size_t ntokens, size_t rows, size_t width, size_t ld_weight, size_t ld_out,
+                         long long first_row, float scale, ar_dtype_t dtype, hipStream_t stream);
+
+/* Workspace of ar_embedding_backward; (size_t)-1 for sizes it does not take. */
+size_t ar_embedding_workspace_bytes(size_t ntokens, size_t rows, size_t width);
+
+/* Its gradient: grad_weight[v] = scale * sum of grad_out[t] over the tokens t
+ * with tokens[t] - first_row = v, summed in fp32 in a fixed order and rounded
+ * once to grad_dtype (dtype or fp32). Every row is written, zeros where no
+ * token falls; with accumulate != 0 the sum is added to what the row holds
+ * (e.g. the head's gradient of a shared weight), and other rows are left
+ * alone. Tokens outside [first_row, first_row + rows) add nothing. */
+ar_result_t ar_embedding_backward(ar_comm_t comm, const void* grad_out, const void* tokens, ar_index_t index,
+                                  void* grad_weight, size_t ntokens, size_t rows, size_t width, size_t ld_grad_out,
+                                  size_t ld_grad_weight, long long first_row, float scale, ar_dtype_t dtype,
+                                  ar_dtype_t grad_dtype, int accumulate, hipStream_t stream);
+
+/* Workspace of ar_linear_cross_entropy (backward = 0) or its gradient
+ * (backward != 0); (size_t)-1 for sizes they do not take. */
+size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, size_t width, ar_dtype_t dtype,
+                                               int backward);
+
+/* Softmax cross entropy of the linear head weight [vocab][width] on hidden
+ * [ntokens][width], in pieces of the vocabulary, without keeping the logits:
+ *   z[t][v] = hidden[t] . weight[v],  lse[t] = log sum_v exp(z[t][v]),
+ *   losses[t] = lse[t] - z[t][targets[t]].
+ * A token whose target is ignore_index or outside [0, vocab) is ignored: its
+ * loss is 0 (its lse is still given). Products of fp16 and bf16 are summed in
+ * fp32; fp32 products are made of bf16 pieces that hold all 24 bits. losses
+ * and lse are fp32. */
+ar_result_t ar_linear_cross_entropy(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
+                                    ar_index_t index, float* losses, float* lse, size_t ntokens, size_t vocab,
+                                    size_t width, size_t ld_hidden, size_t ld_weight, long long ignore_index,
+                                    ar_dtype_t dtype, hipStream_t stream);
+
+/* Its gradients, given lse of the forward call and the gradient of each loss
+ * (e.g. 1 / number of tokens that count, for their mean):
+ *   d[t][v] = grad_losses[t] * (exp(z[t][v] - lse[t]) - [v = targets[t]]),
+ *   grad_hidden = d weight,  grad_weight = d^T hidden,
+ * both of dtype and either may be NULL. Ignored tokens have zero grad_hidden
+ * and add nothing to grad_weight, whatever their hidden row holds. For fp16
+ * and bf16, d is rounded to that type once (scaled by a power of two and, for
+ * grad_weight, by the largest |grad_losses|, so that small probabilities do
+ * not underflow); sums are fp32. */
+ar_result_t ar_linear_cross_entropy_backward(ar_comm_t comm, const void* hidden, const void* weight,
+                                             const void* targets, ar_index_t index, const float* lse,
+                                             const float* grad_losses, void* grad_hidden, void* grad_weight,
+                                             size_t ntokens, size_t vocab, size_t width, size_t ld_hidden,
+                                             size_t ld_weight, size_t ld_grad_hidden, size_t ld_grad_weight,
+                                             long long ignore_index, ar_dtype_t dtype, hipStream_t stream);
+
 /* Static description of a result code. */
 const char* ar_result_string(ar_result_t result);
 

@@ -45,6 +45,13 @@ AR_MODE_FUSED, AR_MODE_RING_STEPWISE, AR_MODE_RING_GRAPH, AR_MODE_TREE, AR_MODE_
 # ar_access_t
 AR_ACCESS_AUTO, AR_ACCESS_STREAMING, AR_ACCESS_CACHED = range(3)
 ACCESS_NAMES = {"auto": AR_ACCESS_AUTO, "streaming": AR_ACCESS_STREAMING, "cached": AR_ACCESS_CACHED}
+# ar_index_t, ar_norm_t, ar_grads_t
+AR_INDEX_INT32, AR_INDEX_INT64 = range(2)
+AR_NORM_L2, AR_NORM_INF = range(2)
+AR_GRADS_REPLICATED, AR_GRADS_SHARDED = range(2)
+INDEX_NAMES = {"i32": AR_INDEX_INT32, "i64": AR_INDEX_INT64}
+NORM_NAMES = {"l2": AR_NORM_L2, "inf": AR_NORM_INF}
+GRADS_NAMES = {"replicated": AR_GRADS_REPLICATED, "sharded": AR_GRADS_SHARDED}
 # ar_collective_t
 AR_COLL_ALL_REDUCE, AR_COLL_REDUCE_SCATTER, AR_COLL_ALL_GATHER, AR_COLL_ALL_TO_ALL = range(4)
 
@@ -57,6 +64,9 @@ EXPORTED_SYMBOLS = (
     "ar_comm_create", "ar_comm_destroy", "ar_comm_nranks", "ar_workspace_bytes", "ar_comm_set_workspace",
     "ar_all_reduce", "ar_all_reduce_noalloc", "ar_reduce_scatter", "ar_all_gather", "ar_all_to_all", "ar_all_reduce_multi",
     "ar_comm_set_step_timing", "ar_comm_set_access", "ar_comm_set_streaming", "ar_last_step_times_ms",
+    "ar_clip_workspace_bytes", "ar_grad_norm", "ar_clip_grads", "ar_all_reduce_clip",
+    "ar_embedding", "ar_embedding_workspace_bytes", "ar_embedding_backward",
+    "ar_linear_cross_entropy_workspace_bytes", "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward",
     "ar_result_string", "ar_last_error",
 )
 
@@ -81,6 +91,23 @@ _lib.ar_comm_set_step_timing.argtypes = [_vp, _c_int]
 _lib.ar_comm_set_streaming.argtypes = [_vp, _c_int]
 _lib.ar_comm_set_access.argtypes = [_vp, _c_int]
 _lib.ar_last_step_times_ms.argtypes = [_vp, ctypes.POINTER(ctypes.c_float), _c_int, ctypes.POINTER(_c_int)]
+_size_array, _c_i64 = ctypes.POINTER(_c_size), ctypes.c_longlong
+_lib.ar_clip_workspace_bytes.argtypes = []
+_lib.ar_clip_workspace_bytes.restype = _c_size
+_lib.ar_grad_norm.argtypes = [_vp, _c_int, _ptr_array, _size_array, _c_int, _c_int, _c_int, _vp, _vp]
+_lib.ar_clip_grads.argtypes = [_vp, _c_int, _ptr_array, _ptr_array, _size_array, _c_int, _c_int, _c_int,
+                               ctypes.c_double, _vp, _vp]
+_lib.ar_all_reduce_clip.argtypes = _lib.ar_clip_grads.argtypes
+_lib.ar_embedding.argtypes = [_vp, _vp, _vp, _c_int, _vp] + [_c_size] * 5 + [_c_i64, ctypes.c_float, _c_int, _vp]
+_lib.ar_embedding_workspace_bytes.argtypes = [_c_size] * 3
+_lib.ar_embedding_workspace_bytes.restype = _c_size
+_lib.ar_embedding_backward.argtypes = [_vp, _vp, _vp, _c_int, _vp] + [_c_size] * 5 + [_c_i64, ctypes.c_float, _c_int,
+                                                                                   _c_int, _c_int, _vp]
+_lib.ar_linear_cross_entropy_workspace_bytes.argtypes = [_c_size] * 3 + [_c_int, _c_int]
+_lib.ar_linear_cross_entropy_workspace_bytes.restype = _c_size
+_lib.ar_linear_cross_entropy.argtypes = [_vp, _vp, _vp, _vp, _c_int, _vp, _vp] + [_c_size] * 5 + [_c_i64, _c_int, _vp]
+_lib.ar_linear_cross_entropy_backward.argtypes = ([_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _vp] + [_c_size] * 7 +
+                                                  [_c_i64, _c_int, _vp])
 _lib.ar_result_string.argtypes = [_c_int]
 _lib.ar_result_string.restype = ctypes.c_char_p
 _lib.ar_last_error.argtypes = []
@@ -88,7 +115,9 @@ _lib.ar_last_error.restype = ctypes.c_char_p
 for _name in ("ar_comm_create", "ar_comm_destroy", "ar_comm_set_workspace", "ar_all_reduce", "ar_all_reduce_noalloc",
               "ar_reduce_scatter",
               "ar_all_gather", "ar_all_to_all", "ar_all_reduce_multi", "ar_comm_set_step_timing",
-              "ar_comm_set_streaming", "ar_comm_set_access", "ar_last_step_times_ms"):
+              "ar_comm_set_streaming", "ar_comm_set_access", "ar_last_step_times_ms",
+              "ar_grad_norm", "ar_clip_grads", "ar_all_reduce_clip", "ar_embedding", "ar_embedding_backward",
+              "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward"):
     getattr(_lib, _name).restype = _c_int
 
 
@@ -293,3 +322,153 @@ def ar_last_step_times_ms(comm, cap: int = 2 * MAX_RANKS + 1):
     n = ctypes.c_int()
     _check(_lib.ar_last_step_times_ms(_h(comm), out, cap, ctypes.byref(n)), "ar_last_step_times_ms")
     return [out[i] for i in range(min(n.value, cap))]
+
+
+# Language-model operators ----------------------------------------------------
+def _flat(bufs):
+    """A tensor-major list of buffers from one list of per-rank buffers per
+    tensor, or as it is."""
+    return [b for row in bufs for b in row] if len(bufs) and isinstance(bufs[0], (list, tuple)) else bufs
+
+
+def _counts(counts):
+    return (ctypes.c_size_t * max(len(counts), 1))(*counts)
+
+
+def _device(comm) -> int:
+    return comm.device if isinstance(comm, Comm) else 0
+
+
+def _check_size(value: int, where: str) -> int:
+    if value == ctypes.c_size_t(-1).value:
+        raise ValueError(f"{where}: invalid arguments or overflow")
+    return value
+
+
+def ar_clip_workspace_bytes() -> int:
+    return _lib.ar_clip_workspace_bytes()
+
+
+def ar_grad_norm(comm, grads, counts, norm_out, dtype, layout="replicated", norm="l2", stream=None):
+    """The global norm of many gradient tensors into the device float
+    ``norm_out``. ``grads``: one list of per-rank buffers per tensor
+    (``grads[t][r]``), or a flat tensor-major list; counts[t] elements."""
+    _check(_lib.ar_grad_norm(_h(comm), len(counts), _ptrs(_flat(grads)), _counts(counts),
+                             _enum(dtype, DTYPE_NAMES, "dtype"), _enum(layout, GRADS_NAMES, "layout"),
+                             _enum(norm, NORM_NAMES, "norm"), _addr(norm_out), _stream(stream, _device(comm))),
+           "ar_grad_norm")
+
+
+def ar_clip_grads(comm, sendbufs, recvbufs, counts, max_norm: float, norm_out, dtype, layout="replicated", norm="l2",
+                  stream=None):
+    """recv = send * min(1, max_norm / (norm + 1e-6)) over all tensors.
+    Buffers as in ar_all_reduce_multi; norm_out: a device float or None."""
+    s = _flat(sendbufs)
+    r = s if recvbufs is sendbufs else _flat(recvbufs)
+    _check(_lib.ar_clip_grads(_h(comm), len(counts), *_ptr_pair(s, r), _counts(counts),
+                              _enum(dtype, DTYPE_NAMES, "dtype"), _enum(layout, GRADS_NAMES, "layout"),
+                              _enum(norm, NORM_NAMES, "norm"), max_norm,
+                              None if norm_out is None else _addr(norm_out), _stream(stream, _device(comm))),
+           "ar_clip_grads")
+
+
+def ar_all_reduce_clip(comm, sendbufs, recvbufs, counts, max_norm: float, norm_out, dtype, op="avg", norm="l2",
+                       stream=None):
+    """ar_all_reduce_multi (sum or avg) and ar_clip_grads of its result in one call."""
+    s = _flat(sendbufs)
+    r = s if recvbufs is sendbufs else _flat(recvbufs)
+    _check(_lib.ar_all_reduce_clip(_h(comm), len(counts), *_ptr_pair(s, r), _counts(counts),
+                                   _enum(dtype, DTYPE_NAMES, "dtype"), _enum(op, OP_NAMES, "op"),
+                                   _enum(norm, NORM_NAMES, "norm"), max_norm,
+                                   None if norm_out is None else _addr(norm_out), _stream(stream, _device(comm))),
+           "ar_all_reduce_clip")
+
+
+def _index(index, buf) -> int:
+    """The index type: as named, or the tensor's own."""
+    if index is not None:
+        return _enum(index, INDEX_NAMES, "index")
+    if isinstance(buf, int):
+        raise TypeError("index numbers passed as an address need their type: index='i32' or 'i64'")
+    if buf.dtype == torch.int64:
+        return AR_INDEX_INT64
+    if buf.dtype == torch.int32:
+        return AR_INDEX_INT32
+    raise TypeError(f"unsupported index dtype {buf.dtype}")
+
+
+def _rows(buf, ld: int):
+    """(address, row pitch) of a matrix: a tensor's own pitch where none is
+    given, its rows being contiguous."""
+    if isinstance(buf, int):
+        return buf, ld
+    if buf is None:
+        return None, ld
+    if ld == 0 and buf.dim() == 2:
+        if buf.shape[1] > 1 and buf.stride(1) != 1:
+            raise ValueError("the rows of a matrix must be contiguous")
+        return buf.data_ptr(), buf.stride(0) if buf.shape[0] > 1 else 0
+    return buf.data_ptr() if ld else _addr(buf), ld
+
+
+def ar_embedding(comm, weight, tokens, out, ntokens: int, rows: int, width: int, dtype, scale: float = 1.0,
+                 first_row: int = 0, ld_weight: int = 0, ld_out: int = 0, index=None, stream=None):
+    """out[t] = weight[tokens[t] - first_row] * scale, zeros where that row is
+    not in [0, rows)."""
+    w, ld_weight = _rows(weight, ld_weight)
+    o, ld_out = _rows(out, ld_out)
+    _check(_lib.ar_embedding(_h(comm), w, _addr(tokens), _index(index, tokens), o, ntokens, rows, width, ld_weight,
+                             ld_out, first_row, scale, _enum(dtype, DTYPE_NAMES, "dtype"),
+                             _stream(stream, _device(comm))), "ar_embedding")
+
+
+def ar_embedding_workspace_bytes(ntokens: int, rows: int, width: int) -> int:
+    return _check_size(_lib.ar_embedding_workspace_bytes(ntokens, rows, width), "ar_embedding_workspace_bytes")
+
+
+def ar_embedding_backward(comm, grad_out, tokens, grad_weight, ntokens: int, rows: int, width: int, dtype,
+                          grad_dtype=None, scale: float = 1.0, first_row: int = 0, ld_grad_out: int = 0,
+                          ld_grad_weight: int = 0, accumulate: bool = False, index=None, stream=None):
+    """grad_weight[v] (+)= scale * the sum of grad_out[t] over the tokens of row v."""
+    d = _enum(dtype, DTYPE_NAMES, "dtype")
+    g, ld_grad_out = _rows(grad_out, ld_grad_out)
+    w, ld_grad_weight = _rows(grad_weight, ld_grad_weight)
+    _check(_lib.ar_embedding_backward(_h(comm), g, _addr(tokens), _index(index, tokens), w, ntokens, rows, width,
+                                      ld_grad_out, ld_grad_weight, first_row, scale, d,
+                                      d if grad_dtype is None else _enum(grad_dtype, DTYPE_NAMES, "grad_dtype"),
+                                      1 if accumulate else 0, _stream(stream, _device(comm))), "ar_embedding_backward")
+
+
+def ar_linear_cross_entropy_workspace_bytes(ntokens: int, vocab: int, width: int, dtype, backward: bool = False) -> int:
+    return _check_size(_lib.ar_linear_cross_entropy_workspace_bytes(ntokens, vocab, width,
+                                                                    _enum(dtype, DTYPE_NAMES, "dtype"),
+                                                                    1 if backward else 0),
+                       "ar_linear_cross_entropy_workspace_bytes")
+
+
+def ar_linear_cross_entropy(comm, hidden, weight, targets, losses, lse, ntokens: int, vocab: int, width: int, dtype,
+                            ignore_index: int = -100, ld_hidden: int = 0, ld_weight: int = 0, index=None, stream=None):
+    """losses[t] = lse[t] - z[t][targets[t]] with z = hidden weight^T and lse its
+    logsumexp, without keeping z."""
+    x, ld_hidden = _rows(hidden, ld_hidden)
+    w, ld_weight = _rows(weight, ld_weight)
+    _check(_lib.ar_linear_cross_entropy(_h(comm), x, w, _addr(targets), _index(index, targets), _addr(losses),
+                                        _addr(lse), ntokens, vocab, width, ld_hidden, ld_weight, ignore_index,
+                                        _enum(dtype, DTYPE_NAMES, "dtype"), _stream(stream, _device(comm))),
+           "ar_linear_cross_entropy")
+
+
+def ar_linear_cross_entropy_backward(comm, hidden, weight, targets, lse, grad_losses, grad_hidden, grad_weight,
+                                     ntokens: int, vocab: int, width: int, dtype, ignore_index: int = -100,
+                                     ld_hidden: int = 0, ld_weight: int = 0, ld_grad_hidden: int = 0,
+                                     ld_grad_weight: int = 0, index=None, stream=None):
+    """grad_hidden and grad_weight (either may be None) from lse and the gradient of each loss."""
+    x, ld_hidden = _rows(hidden, ld_hidden)
+    w, ld_weight = _rows(weight, ld_weight)
+    gx, ld_grad_hidden = _rows(grad_hidden, ld_grad_hidden)
+    gw, ld_grad_weight = _rows(grad_weight, ld_grad_weight)
+    _check(_lib.ar_linear_cross_entropy_backward(_h(comm), x, w, _addr(targets), _index(index, targets), _addr(lse),
+                                                 _addr(grad_losses), gx, gw, ntokens, vocab, width, ld_hidden,
+                                                 ld_weight, ld_grad_hidden, ld_grad_weight, ignore_index,
+                                                 _enum(dtype, DTYPE_NAMES, "dtype"), _stream(stream, _device(comm))),
+           "ar_linear_cross_entropy_backward")

@@ -23,11 +23,13 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liballreduce.so")
 OBJDIR = os.path.join(PKG, "_build")
 # Two translation units per dtype (ring kernels, tree kernels: the heavy
-# template instantiations), the dtype switch / copy kernels and the C ABI;
+# template instantiations), the dtype switch / copy kernels, the C ABI, and the
+# language-model operators (lm/);
 # compiled in parallel, then linked.
 SOURCES = [os.path.join(CSRC, f) for f in
            ("dtype_f32.hip", "dtype_f16.hip", "dtype_bf16.hip", "dtype_i32.hip", "tree_f32.hip", "tree_f16.hip",
-            "tree_bf16.hip", "tree_i32.hip", "kernels.hip", "noalloc.hip", "api.cpp")]
+            "tree_bf16.hip", "tree_i32.hip", "kernels.hip", "noalloc.hip", "api.cpp",
+            "lm/clip.hip", "lm/embedding.hip", "lm/cross_entropy.hip", "lm/lm_api.cpp")]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -47,7 +49,8 @@ def hipcc_link(objs, out: str):
 def _stale(src: str, obj: str) -> bool:
     if not os.path.exists(obj):
         return True
-    deps = [src] + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith(".h")] + \
+    deps = [src] + [os.path.join(d, h) for d in (CSRC, os.path.join(CSRC, "lm")) for h in os.listdir(d)
+                    if h.endswith(".h")] + \
            [os.path.join(INCLUDE, h) for h in os.listdir(INCLUDE)]
     return max(os.path.getmtime(d) for d in deps) > os.path.getmtime(obj)
 
