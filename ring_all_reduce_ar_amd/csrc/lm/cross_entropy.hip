@@ -26,7 +26,7 @@ namespace {
 
 // d is held times 2^14: a probability of 1e-8 is still a normal fp16, and
 // |p - 1| 2^14 is far below its largest.
-constexpr float kDScale = 16384.0f;
+constexpr float kDBits = 14.0f, kDScale = 16384.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPartA[kF32Parts] = {0, 0, 1, 0, 1, 2};
 constexpr int kPartB[kF32Parts] = {0, 1, 0, 2, 1, 0};
@@ -35,6 +35,15 @@ __device__ __forceinline__ int64_t load_target(const Indices& x, uint64_t t, int
 {
     const int64_t y = x.is64 ? gptr<int64_t>(x.p)[t] : static_cast<int64_t>(gptr<int32_t>(x.p)[t]);
     return y == ignore || static_cast<uint64_t>(y) >= vocab ? -1 : y;
+}
+
+// Where target y lies among a lane's rows v, v + 1 .. of MT groups of 16.
+constexpr uint32_t kNoTarget = UINT32_MAX;
+template <int MT>
+__device__ __forceinline__ uint32_t target_at(int64_t y, uint64_t v)
+{
+    const uint64_t at = static_cast<uint64_t>(y) - v;
+    return y >= 0 && at < MT * 16 ? static_cast<uint32_t>(at) : kNoTarget;
 }
 
 // The three bf16 pieces of a float; a value that is no number stays in the first.
@@ -123,9 +132,19 @@ struct StatsEpilogue {
     uint64_t v0;          // the piece's first vocabulary row
     uint64_t row0;        // the piece's first row of `stats`
 
-    template <int MT, int NT>
+    template <int MT, int NT, class S>
     __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const GemmArgs& g,
-                                               uint32_t mrow, uint32_t) const
+                                               uint32_t mrow, uint32_t, const S&) const
+    {
+        if (m0 + MT * 16 <= g.m) parts<true>(acc, m0, n0, g, mrow);
+        else parts<false>(acc, m0, n0, g, mrow);
+    }
+
+private:
+    // FULL: all of the wave's rows are rows of the vocabulary.
+    template <bool FULL, int MT, int NT>
+    __device__ __forceinline__ void parts(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const GemmArgs& g,
+                                          uint32_t mrow) const
     {
         const int lane = threadIdx.x & 63, quad = lane >> 4;
         const uint32_t mine = m0 + quad * 4;  // vocabulary rows of the piece: mine + 16 i + r
@@ -138,7 +157,7 @@ struct StatsEpilogue {
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (mine + 16 * i + r < g.m) top = fmaxf(top, acc.v[i][j][r]);
+                    if (FULL || mine + 16 * i + r < g.m) top = fmaxf(top, acc.v[i][j][r]);
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             const float base = top == -INFINITY ? 0.0f : top;
@@ -147,17 +166,18 @@ struct StatsEpilogue {
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (mine + 16 * i + r < g.m) sum += __builtin_amdgcn_exp2f((acc.v[i][j][r] - base) * kLog2e);
+                    if (FULL || mine + 16 * i + r < g.m)
+                        sum += __builtin_amdgcn_exp2f((acc.v[i][j][r] - base) * kLog2e);
             sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
             if (ok && quad == 0) stats[(row0 + mrow) * g.n + t] = Stats{top, sum};
-            const int64_t y = ok ? load_target(targets, t, ignore, vocab) : -1;
-            const int64_t at = y - static_cast<int64_t>(v0) - mine;
+            const uint32_t at = ok ? target_at<MT>(load_target(targets, t, ignore, vocab), v0 + mine) : kNoTarget;
+            if (!__any(at != kNoTarget)) continue;  // few tiles hold a target
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (y >= 0 && at == 16 * i + r) target_logit[t] = acc.v[i][j][r];
+                    if (at == 16 * i + r) target_logit[t] = acc.v[i][j][r];
         }
     }
 };
@@ -229,7 +249,7 @@ __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices target
 // d of one piece, in both orders: d[t][part * piece_pad + v] = 2^14 (p - [v =
 // y]) for the hidden gradient (whose rows take g[t] at the end) and
 // dt[v][part * t_pad + t] the same times g[t] / max |g| for the weight's.
-template <class F, int PARTS>
+template <class T, int PARTS>
 struct DEpilogue {
     uint16_t* d;
     uint16_t* dt;
@@ -240,33 +260,79 @@ struct DEpilogue {
     int64_t ignore;
     uint64_t vocab, v0, piece_pad, t_pad;
 
-    template <int MT, int NT>
-    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const GemmArgs& g,
-                                               uint32_t, uint32_t) const
+    template <int MT, int NT, class S>
+    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const GemmArgs& g, uint32_t,
+                                               uint32_t, const S& stage) const
     {
-        const int lane = threadIdx.x & 63, quad = lane >> 4;
+        const int lane = threadIdx.x & 63;
+        float factor[NT];  // of a token's column of dt
+        bool all = m0 + MT * 16 <= g.m;
         const float inv = 1.0f / scale->top;
+        uint32_t at[NT];
+        bool on[NT];
+        float l[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const uint32_t t = n0 + j * 16 + (lane & 15);
-            const bool ok = t < g.n;
-            const int64_t y = ok ? load_target(targets, t, ignore, vocab) : -1;
-            const float l = ok ? lse[t] : 0.0f;
-            const float gt = ok ? g_losses[t] * inv : 0.0f;
+            const int64_t y = t < g.n ? load_target(targets, t, ignore, vocab) : -1;
+            at[j] = target_at<MT>(y, v0 + m0 + (lane >> 4) * 4);
+            on[j] = y >= 0;
+            l[j] = on[j] ? lse[t] : 0.0f;
+            factor[j] = on[j] ? g_losses[t] * inv : 0.0f;
+            all = all && on[j];
+        }
+        if (__all(all)) differences<true>(acc, at, on, l, m0, g);
+        else differences<false>(acc, at, on, l, m0, g);
+        if constexpr (S::kOn && PARTS == 1) {
+            if (d) stage.template store_by_column<T>(acc, d, piece_pad, g.n, static_cast<uint32_t>(piece_pad));
+            if (dt) stage.template store_by_row<T>(acc, factor, dt, t_pad, g.m, static_cast<uint32_t>(t_pad));
+        } else {
+            store(acc, factor, m0, n0, g);
+        }
+    }
+
+private:
+    // acc = 2^14 (exp(acc - lse) - [v = y]). FULL: every row is one of the
+    // vocabulary and every token counts; else zeros where not.
+    template <bool FULL, int MT, int NT>
+    __device__ __forceinline__ void differences(Tile<MT, NT>& acc, const uint32_t (&at)[NT], const bool (&on)[NT],
+                                                const float (&l)[NT], uint32_t m0, const GemmArgs& g) const
+    {
+        const uint32_t mine = m0 + ((threadIdx.x & 63) >> 4) * 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][r] - l[j], kLog2e, kDBits));
+                    acc.v[i][j][r] = FULL || (on[j] && mine + 16 * i + r < g.m) ? p : 0.0f;
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            if (!__any(at[j] != kNoTarget)) continue;  // few tiles hold a target
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc.v[i][j][r] -= at[j] == 16 * i + r ? kDScale : 0.0f;
+        }
+    }
+
+    template <int MT, int NT>
+    __device__ __forceinline__ void store(const Tile<MT, NT>& acc, const float (&factor)[NT], uint32_t m0, uint32_t n0,
+                                          const GemmArgs& g) const
+    {
+        const int lane = threadIdx.x & 63, quad = lane >> 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint32_t t = n0 + j * 16 + (lane & 15);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const uint32_t v = m0 + quad * 4 + 16 * i;
-                float x[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float p = __builtin_amdgcn_exp2f((acc.v[i][j][r] - l) * kLog2e);
-                    const bool hit = y == static_cast<int64_t>(v0 + v + r);
-                    // rows beyond the vocabulary and ignored tokens are zeros
-                    x[r] = y >= 0 && v + r < g.m ? (p - (hit ? 1.0f : 0.0f)) * kDScale : 0.0f;
-                }
-                if (d && ok && v < piece_pad) {
+                const f32x4 x = acc.v[i][j];
+                if (d && t < g.n && v < piece_pad) {
                     if constexpr (PARTS == 1) {
-                        *reinterpret_cast<u32x2*>(d + static_cast<uint64_t>(t) * piece_pad + v) = F::pack4(x);
+                        *reinterpret_cast<u32x2*>(d + static_cast<uint64_t>(t) * piece_pad + v) =
+                            u32x2{T::pack2(x[0], x[1]), T::pack2(x[2], x[3])};
                     } else {
                         uint32_t p[4][3];
 #pragma unroll
@@ -283,9 +349,9 @@ struct DEpilogue {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         if (v + r >= g.m) continue;
-                        const float s = y >= 0 ? x[r] * gt : 0.0f;
+                        const float s = x[r] * factor[j];
                         if constexpr (PARTS == 1) {
-                            F::st(dt, static_cast<uint64_t>(v + r) * t_pad + t, s);
+                            T::Format::st(dt, static_cast<uint64_t>(v + r) * t_pad + t, s);
                         } else {
                             uint32_t p[3];
                             split3(s, p);
@@ -307,9 +373,9 @@ struct HiddenEpilogue {
     uint64_t width;
     int add;
 
-    template <int MT, int NT>
+    template <int MT, int NT, class S>
     __device__ __forceinline__ void operator()(Tile<MT, NT>& c, uint32_t m0, uint32_t n0, const GemmArgs& g, uint32_t,
-                                               uint32_t split) const
+                                               uint32_t split, const S&) const
     {
         const int lane = threadIdx.x & 63, quad = lane >> 4;
 #pragma unroll
@@ -360,9 +426,9 @@ struct WeightEpilogue {
     const RowScale* scale;
     int vec;  // 4 elements at a time: the pitch and the address allow it
 
-    template <int MT, int NT>
+    template <int MT, int NT, class S>
     __device__ __forceinline__ void operator()(Tile<MT, NT>& c, uint32_t m0, uint32_t n0, const GemmArgs& g, uint32_t,
-                                               uint32_t) const
+                                               uint32_t, const S&) const
     {
         const int lane = threadIdx.x & 63, quad = lane >> 4;
         const float s = scale->top * (1.0f / kDScale);
@@ -513,7 +579,7 @@ struct Call {
             const uint64_t pad = (rows + kTileK - 1) / kTileK * kTileK;
             if (a.ntokens) {  // no token: the weight's gradient is the empty sum
                 if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
-                const DEpilogue<typename T::Format, PARTS> epi{d, dt, a.lse, a.grad_losses, scale, a.targets,
+                const DEpilogue<T, PARTS> epi{d, dt, a.lse, a.grad_losses, scale, a.targets,
                                                                a.ignore_index, a.vocab, v0, pad, p.t_pad};
                 if ((e = logits<T>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
             }

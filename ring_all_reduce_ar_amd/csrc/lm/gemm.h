@@ -19,9 +19,14 @@
 
 namespace ar {
 namespace lm {
+using detail::u32x2;
+using detail::u32x4;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct MmaBF16 {
@@ -31,6 +36,11 @@ struct MmaBF16 {
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
+    // Two floats, rounded to nearest even, the first in the low half.
+    static __device__ __forceinline__ uint32_t pack2(float x, float y)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+    }
 };
 struct MmaF16 {
     using Frag = f16x8;
@@ -38,6 +48,10 @@ struct MmaF16 {
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t pack2(float x, float y)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, f16x2));
     }
 };
 
@@ -78,6 +92,90 @@ __device__ __forceinline__ void tile_of_workgroup(const GemmArgs& g, uint32_t* t
     *tm = first + in % high;
     *tn = in / high;
 }
+
+// ---------------------------------------------------------------------------
+// storing a tile of 16-bit results in rows, through LDS
+// ---------------------------------------------------------------------------
+// A lane's results are four rows of one column; stored as they lie they make
+// pieces of 32 bytes. A 256 x 256 tile of 16-bit values fills the 128 KiB that
+// the product's stages held, and leaves in whole rows of 512 bytes.
+struct NoStaging {
+    static constexpr bool kOn = false;
+};
+struct Staging {
+    static constexpr bool kOn = true;
+    char* lds;
+    uint32_t m, n;            // the wave's first row and column within the tile
+    uint32_t m_base, n_base;  // the tile's
+
+    // Rows of 32 16-byte columns, permuted by the row within groups of eight
+    // so that the lanes of one write spread over the banks.
+    static __device__ __forceinline__ uint32_t at(uint32_t row, uint32_t byte, uint32_t key)
+    {
+        return row * 512 + (byte ^ ((key & 7) * 16));
+    }
+
+    // out[n][m], `ld` apart, for the first `rows` n and `cols` m (a multiple of 8).
+    template <class T, int MT, int NT>
+    __device__ __forceinline__ void store_by_column(const Tile<MT, NT>& x, uint16_t* out, uint64_t ld, uint32_t rows,
+                                                    uint32_t cols) const
+    {
+        const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const uint32_t row = n + j * 16 + (lane & 15), col = m + i * 16 + quad * 4;
+                const f32x4 v = x.v[i][j];
+                *reinterpret_cast<u32x2*>(lds + at(row, col * 2, row)) = u32x2{T::pack2(v[0], v[1]), T::pack2(v[2], v[3])};
+            }
+        }
+        __syncthreads();
+        copy_rows(out, ld, n_base, rows, m_base, cols, 0);
+    }
+
+    // out[m][n]: neighbouring columns lie in neighbouring lanes, which
+    // exchange halves, so that each has two columns of two rows.
+    template <class T, int MT, int NT>
+    __device__ __forceinline__ void store_by_row(const Tile<MT, NT>& x, const float (&factor)[NT], uint16_t* out,
+                                                 uint64_t ld, uint32_t rows, uint32_t cols) const
+    {
+        const uint32_t lane = threadIdx.x & 63, quad = lane >> 4, odd = lane & 1;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const f32x4 v = x.v[i][j] * factor[j];
+                const uint32_t p01 = T::pack2(v[0], v[1]), p23 = T::pack2(v[2], v[3]);
+                const uint32_t give = odd ? p01 : p23, keep = odd ? p23 : p01;
+                const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+                const uint32_t lo = odd ? got : keep, hi = odd ? keep : got;
+                const uint32_t row = m + i * 16 + quad * 4 + odd * 2, byte = (n + j * 16 + (lane & 14)) * 2;
+                *reinterpret_cast<uint32_t*>(lds + at(row, byte, row >> 1)) = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+                *reinterpret_cast<uint32_t*>(lds + at(row + 1, byte, row >> 1)) = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+            }
+        }
+        __syncthreads();
+        copy_rows(out, ld, m_base, rows, n_base, cols, 1);
+    }
+
+private:
+    __device__ __forceinline__ void copy_rows(uint16_t* out, uint64_t ld, uint32_t row0, uint32_t rows, uint32_t col0,
+                                              uint32_t cols, int key_shift) const
+    {
+        const uint32_t c = threadIdx.x & 31;
+#pragma unroll 4
+        for (uint32_t r = threadIdx.x >> 5; r < 256; r += 16) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(lds + at(r, c * 16, r >> key_shift));
+            if (row0 + r < rows && col0 + c * 8 < cols)
+                *reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(row0 + r) * ld + col0 + c * 8) = v;
+        }
+    }
+};
 
 template <class T, int BN, int WM, int WN, class Epilogue>
 __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epilogue epi)
@@ -162,7 +260,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
                 for (int j = 0; j < NT; ++j) acc.v[i][j] = T::mma(fa[i], fb[j], acc.v[i][j]);
         }
     }
-    epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * WM + wm, split);
+    epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * WM + wm, split, NoStaging{});
 }
 
 // ---------------------------------------------------------------------------
@@ -334,9 +432,11 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
             stage ^= kStage;
         }
         if (wave < 4) meet();
+        // the loads past the end have arrived too: LDS is the epilogue's
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
     }
-    epi(acc, m_base + wm * 128, n_base + wn * 64, g, tm * 2 + wm, split);
+    epi(acc, m_base + wm * 128, n_base + wn * 64, g, tm * 2 + wm, split, Staging{lds, wm * 128u, wn * 64u, m_base, n_base});
 }
 
 template <class T, int BN, int WM, int WN, class Epilogue>
