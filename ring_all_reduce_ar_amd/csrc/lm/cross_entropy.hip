@@ -11,9 +11,9 @@
 // are gemm.h's, with both operands contiguous along the summed axis, so W and
 // X are also laid out transposed, and d is written in both orders.
 //
-// fp32 operands are laid out as three bf16 pieces each (kF32Parts): six bf16
-// products give the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the fp32
-// matrix instructions end at 0.16.
+// fp32 operands are laid out as three bf16 pieces each: six bf16 products give
+// the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the fp32 matrix
+// instructions end at 0.16.
 #include <type_traits>
 
 #include "gemm.h"
@@ -28,8 +28,6 @@ namespace {
 // |p - 1| 2^14 is far below its largest.
 constexpr float kDBits = 14.0f, kDScale = 16384.0f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kPartA[kF32Parts] = {0, 0, 1, 0, 1, 2};
-constexpr int kPartB[kF32Parts] = {0, 1, 0, 2, 1, 0};
 
 __device__ __forceinline__ int64_t load_target(const Indices& x, uint64_t t, int64_t ignore, uint64_t vocab)
 {
@@ -49,68 +47,109 @@ __device__ __forceinline__ uint32_t target_at(int64_t y, uint64_t v)
 // The three bf16 pieces of a float; a value that is no number stays in the first.
 __device__ __forceinline__ void split3(float x, uint32_t (&p)[3])
 {
-    p[0] = f32_to_bf16(x);
-    const float r1 = x - bf16_to_f32(p[0]);
-    const bool finite = __builtin_isfinite(bf16_to_f32(p[0]));
-    p[1] = finite ? f32_to_bf16(r1) : 0;
-    const float r2 = r1 - bf16_to_f32(p[1]);
-    p[2] = finite ? f32_to_bf16(r2) : 0;
+    auto round = [](float v) { return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v))); };
+    p[0] = round(x);
+    const float top = bf16_to_f32(p[0]);
+    const float r1 = __builtin_isfinite(top) ? x - top : 0.0f;
+    p[1] = round(r1);
+    p[2] = round(r1 - bf16_to_f32(p[1]));
 }
 
 // ---------------------------------------------------------------------------
 // laying out operands
 // ---------------------------------------------------------------------------
-// out[r][part * pad + c] = in[r][c], zeros up to `pad`.
-template <class F, int PARTS, bool IS_A>
-__global__ __launch_bounds__(kBlock) void pack_rows(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
-                                                    uint64_t pad, uint16_t* out)
+// Stores eight depths k..k+7 (k a multiple of 8) of a row: as they are, or in pieces.
+template <int PARTS, class Raw>
+__device__ __forceinline__ void put8(uint16_t* row, uint64_t k, const Raw (&x)[8])
 {
-    const uint64_t n = rows * pad;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x; i < n;
-         i += static_cast<uint64_t>(gridDim.x) * kBlock) {
-        const uint64_t r = i / pad, c = i - r * pad;
-        if constexpr (PARTS == 1) {
-            out[i] = c < width ? gptr<uint16_t>(in)[r * ld + c] : 0;
-        } else {
-            uint32_t p[3];
-            split3(c < width ? F::ld(in, r * ld + c) : 0.0f, p);
+    if constexpr (PARTS == 1) {
+        u32x4 v;
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k)
-                out[(r * PARTS + k) * pad + c] = static_cast<uint16_t>(p[IS_A ? kPartA[k] : kPartB[k]]);
+        for (int i = 0; i < 4; ++i) v[i] = x[2 * i] | (static_cast<uint32_t>(x[2 * i + 1]) << 16);
+        *reinterpret_cast<u32x4*>(row + k) = v;
+    } else {
+        uint32_t p[8][3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split3(x[i], p[i]);
+        uint16_t* at = row + (k / kPieceDepth) * (kPieceDepth * kPieces) + k % kPieceDepth;
+#pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            u32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = p[2 * i][q] | (p[2 * i + 1][q] << 16);
+            *reinterpret_cast<u32x4*>(at + q * kPieceDepth) = v;
         }
     }
 }
 
-// out[c][part * pad + r] = in[r][c] for r < rows, zeros up to `pad` and in
-// rows whose target is ignored (whatever they hold). 64x64 tiles through LDS.
-template <class F, int PARTS>
+template <int PARTS>
+using RawOf = typename std::conditional<PARTS == 1, uint16_t, float>::type;
+
+// Eight elements from a 16-byte boundary, or one by one as far as they go.
+template <class Raw, bool VEC>
+__device__ __forceinline__ void get8(const void* in, uint64_t at, uint64_t left, Raw (&x)[8])
+{
+    if constexpr (VEC) {
+        if (left >= 8) {
+            constexpr int N = sizeof(Raw) / 2;
+            u32x4 v[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = ldv_at<false>(in, at * sizeof(Raw) + i * 16);
+            __builtin_memcpy(x, v, sizeof(x));
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = static_cast<uint64_t>(i) < left ? gptr<Raw>(in)[at + i] : Raw(0);
+}
+
+// out[r] = in[r] in pieces (or as it is, on a 16-byte boundary), zeros from
+// `width` up to `pad`. `lanes` (a power of two) threads a row.
+template <int PARTS, bool VEC>
+__global__ __launch_bounds__(kBlock) void pack_rows(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
+                                                    uint64_t pad, uint16_t* out, int lanes)
+{
+    const uint64_t r = static_cast<uint64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
+    if (r >= rows) return;
+    for (uint64_t c = (threadIdx.x & (lanes - 1)) * 8ull; c < pad; c += lanes * 8ull) {
+        RawOf<PARTS> x[8];
+        get8<RawOf<PARTS>, VEC>(in, r * ld + c, c < width ? width - c : 0, x);
+        put8<PARTS>(out + r * pad * PARTS, c, x);
+    }
+}
+
+// out[c] = the column c of `in` for rows below `rows`, zeros up to `pad` (a
+// multiple of 64) and in rows whose target is ignored (whatever they hold).
+// 64 x 64 tiles through LDS; a lane takes eight rows of one column, eight
+// lanes 128 bytes (or three times 64, twice).
+template <int PARTS, bool VEC>
 __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
                                                           uint64_t pad, uint16_t* out, Indices targets, int masked,
                                                           int64_t ignore, uint64_t vocab)
 {
-    using Raw = typename std::conditional<PARTS == 1, uint16_t, float>::type;
-    __shared__ Raw tile[64][65];
+    using Raw = RawOf<PARTS>;
+    __shared__ Raw tile[64][PARTS == 1 ? 66 : 65];
     const uint64_t r0 = static_cast<uint64_t>(blockIdx.x) * 64, c0 = static_cast<uint64_t>(blockIdx.y) * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    for (int i = y; i < 64; i += 4) {
-        const uint64_t r = r0 + i, c = c0 + x;
-        Raw v = 0;
+    const int slot = threadIdx.x & 7;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = i * 32 + (threadIdx.x >> 3);
+        const uint64_t r = r0 + row, c = c0 + slot * 8;
+        Raw x[8] = {};
         if (r < rows && c < width && (!masked || load_target(targets, r, ignore, vocab) >= 0))
-            v = gptr<Raw>(in)[r * ld + c];
-        tile[i][x] = v;
+            get8<Raw, VEC>(in, r * ld + c, width - c, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tile[row][slot * 8 + k] = x[k];
     }
     __syncthreads();
-    for (int i = y; i < 64; i += 4) {
-        const uint64_t r = r0 + x, c = c0 + i;
-        if (r >= pad || c >= width) continue;
-        if constexpr (PARTS == 1) {
-            out[c * pad + r] = tile[x][i];
-        } else {
-            uint32_t p[3];
-            split3(tile[x][i], p);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) out[(c * PARTS + k) * pad + r] = static_cast<uint16_t>(p[kPartA[k]]);
-        }
+    for (int i = 0; i < 2; ++i) {
+        const int c = i * 32 + (threadIdx.x >> 3);
+        if (c0 + c >= width) continue;
+        Raw x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = tile[slot * 8 + k][c];
+        put8<PARTS>(out + (c0 + c) * pad * PARTS, r0 + slot * 8, x);
     }
 }
 
@@ -182,41 +221,45 @@ private:
     }
 };
 
-// Joins the parts of each token's row: 16 tokens a workgroup, 16 parts at a time.
-__global__ __launch_bounds__(kBlock) void join_stats(const Stats* stats, uint64_t stat_rows, const float* target_logit,
-                                                     Indices targets, int64_t ignore, uint64_t vocab, uint64_t ntokens,
-                                                     float* losses, float* lse)
+// Two parts of one row's sum. A part of nothing has the top -infinity; a NaN
+// stays in the sum.
+__device__ __forceinline__ Stats join_parts(Stats a, Stats b)
 {
-    __shared__ Stats part[16][17];
-    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * 16 + x;
-    float top = -INFINITY, sum = 0.0f;
+    const float m = fmaxf(a.top, b.top);
+    const float sum = m == -INFINITY ? a.sum + b.sum
+                                     : a.sum * __builtin_amdgcn_exp2f((a.top - m) * kLog2e) +
+                                           b.sum * __builtin_amdgcn_exp2f((b.top - m) * kLog2e);
+    return Stats{m, sum};
+}
+
+// Joins the parts of each token's row: X tokens a workgroup, kJoinBlock / X
+// threads for each. Neighbouring tokens lie side by side, so many tokens take
+// 16 (128 bytes) and few tokens as few as there are, for more threads to a
+// row: 3 tokens with 2048 parts in 5 us rather than 38.
+constexpr int kJoinBlock = 512;
+template <int X>
+__global__ __launch_bounds__(kJoinBlock) void join_stats(const Stats* stats, uint64_t stat_rows,
+                                                         const float* target_logit, Indices targets, int64_t ignore,
+                                                         uint64_t vocab, uint64_t ntokens, float* losses, float* lse)
+{
+    constexpr int Y = kJoinBlock / X;
+    __shared__ Stats part[Y][X];
+    const int x = threadIdx.x % X, y = threadIdx.x / X;
+    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * X + x;
+    Stats s{-INFINITY, 0.0f};
     if (t < ntokens) {
-        for (uint64_t r = y; r < stat_rows; r += 16) {
-            const Stats s = stats[r * ntokens + t];
-            const float m = fmaxf(top, s.top);
-            if (m == -INFINITY) {
-                sum += s.sum;  // nothing yet, or a NaN
-            } else {
-                sum = sum * __builtin_amdgcn_exp2f((top - m) * kLog2e) + s.sum * __builtin_amdgcn_exp2f((s.top - m) * kLog2e);
-            }
-            top = m;
-        }
+#pragma unroll 4
+        for (uint64_t r = y; r < stat_rows; r += Y) s = join_parts(s, stats[r * ntokens + t]);
     }
-    part[y][x] = Stats{top, sum};
-    __syncthreads();
+    part[y][x] = s;
+#pragma unroll
+    for (int h = Y / 2; h >= 1; h /= 2) {
+        __syncthreads();
+        if (y < h) part[y][x] = join_parts(part[y][x], part[y + h][x]);
+    }
     if (y == 0 && t < ntokens) {
-        for (int k = 1; k < 16; ++k) {
-            const Stats s = part[k][x];
-            const float m = fmaxf(top, s.top);
-            if (m == -INFINITY) {
-                sum += s.sum;
-            } else {
-                sum = sum * __builtin_amdgcn_exp2f((top - m) * kLog2e) + s.sum * __builtin_amdgcn_exp2f((s.top - m) * kLog2e);
-            }
-            top = m;
-        }
-        const float l = top + logf(sum);
+        s = part[0][x];
+        const float l = s.top + logf(s.sum);
         lse[t] = l;
         losses[t] = load_target(targets, t, ignore, vocab) >= 0 ? l - target_logit[t] : 0.0f;
     }
@@ -246,10 +289,10 @@ __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices target
     }
 }
 
-// d of one piece, in both orders: d[t][part * piece_pad + v] = 2^14 (p - [v =
-// y]) for the hidden gradient (whose rows take g[t] at the end) and
-// dt[v][part * t_pad + t] the same times g[t] / max |g| for the weight's.
-template <class T, int PARTS>
+// d of one piece of the vocabulary, in both orders: d[t][v] = 2^14 (p - [v =
+// y]) for the hidden gradient (whose rows take g[t] at the end) and dt[v][t]
+// the same times g[t] / max |g| for the weight's.
+template <class T>
 struct DEpilogue {
     uint16_t* d;
     uint16_t* dt;
@@ -283,9 +326,14 @@ struct DEpilogue {
         }
         if (__all(all)) differences<true>(acc, at, on, l, m0, g);
         else differences<false>(acc, at, on, l, m0, g);
-        if constexpr (S::kOn && PARTS == 1) {
-            if (d) stage.template store_by_column<T>(acc, d, piece_pad, g.n, static_cast<uint32_t>(piece_pad));
-            if (dt) stage.template store_by_row<T>(acc, factor, dt, t_pad, g.m, static_cast<uint32_t>(t_pad));
+        const uint32_t cols = static_cast<uint32_t>(piece_pad), tcols = static_cast<uint32_t>(t_pad);
+        if constexpr (std::is_same<S, PieceStaging>::value) {
+            auto split = [](float x, uint32_t (&p)[3]) { split3(x, p); };
+            if (d) stage.store_by_column(acc, d, piece_pad * kPieces, g.n, cols, split);
+            if (dt) stage.store_by_row(acc, factor, dt, t_pad * kPieces, g.m, tcols, split);
+        } else if constexpr (S::kOn) {
+            if (d) stage.template store_by_column<T>(acc, d, piece_pad, g.n, cols);
+            if (dt) stage.template store_by_row<T>(acc, factor, dt, t_pad, g.m, tcols);
         } else {
             store(acc, factor, m0, n0, g);
         }
@@ -329,38 +377,13 @@ private:
             for (int i = 0; i < MT; ++i) {
                 const uint32_t v = m0 + quad * 4 + 16 * i;
                 const f32x4 x = acc.v[i][j];
-                if (d && t < g.n && v < piece_pad) {
-                    if constexpr (PARTS == 1) {
-                        *reinterpret_cast<u32x2*>(d + static_cast<uint64_t>(t) * piece_pad + v) =
-                            u32x2{T::pack2(x[0], x[1]), T::pack2(x[2], x[3])};
-                    } else {
-                        uint32_t p[4][3];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) split3(x[r], p[r]);
-#pragma unroll
-                        for (int k = 0; k < PARTS; ++k) {
-                            const int q = kPartB[k];
-                            *reinterpret_cast<u32x2*>(d + (static_cast<uint64_t>(t) * PARTS + k) * piece_pad + v) =
-                                u32x2{p[0][q] | (p[1][q] << 16), p[2][q] | (p[3][q] << 16)};
-                        }
-                    }
-                }
+                if (d && t < g.n && v < piece_pad)
+                    *reinterpret_cast<u32x2*>(d + static_cast<uint64_t>(t) * piece_pad + v) =
+                        u32x2{T::pack2(x[0], x[1]), T::pack2(x[2], x[3])};
                 if (dt && t < t_pad) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (v + r >= g.m) continue;
-                        const float s = x[r] * factor[j];
-                        if constexpr (PARTS == 1) {
-                            T::Format::st(dt, static_cast<uint64_t>(v + r) * t_pad + t, s);
-                        } else {
-                            uint32_t p[3];
-                            split3(s, p);
-#pragma unroll
-                            for (int k = 0; k < PARTS; ++k)
-                                dt[(static_cast<uint64_t>(v + r) * PARTS + k) * t_pad + t] =
-                                    static_cast<uint16_t>(p[kPartB[k]]);
-                        }
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        if (v + r < g.m) T::Format::st(dt, static_cast<uint64_t>(v + r) * t_pad + t, x[r] * factor[j]);
                 }
             }
         }
@@ -401,37 +424,63 @@ struct HiddenEpilogue {
     }
 };
 
-// grad_hidden[t][h] = round(g[t] 2^-14 * the splits' sum), 0 for ignored tokens.
-template <class F>
+// grad_hidden[t][h] = round(g[t] 2^-14 * the splits' sum), 0 for ignored
+// tokens. U elements a thread, `lanes` threads a row.
+template <class F, int U>
 __global__ __launch_bounds__(kBlock) void finish_hidden(const float* acc, int splits, const float* g, Indices targets,
                                                         int64_t ignore, uint64_t vocab, uint64_t ntokens,
-                                                        uint64_t width, void* out, uint64_t ld)
+                                                        uint64_t width, void* out, uint64_t ld, int lanes)
 {
-    const uint64_t n = ntokens * width;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x; i < n;
-         i += static_cast<uint64_t>(gridDim.x) * kBlock) {
-        const uint64_t t = i / width;
-        float s = acc[i];
-        for (int k = 1; k < splits; ++k) s += acc[static_cast<uint64_t>(k) * n + i];
-        const bool on = load_target(targets, t, ignore, vocab) >= 0;
-        F::st(out, t * ld + (i - t * width), on ? s * (g[t] * (1.0f / kDScale)) : 0.0f);
+    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
+    if (t >= ntokens) return;
+    const bool on = load_target(targets, t, ignore, vocab) >= 0;
+    const float scale = on ? g[t] * (1.0f / kDScale) : 0.0f;
+    for (uint64_t c = (threadIdx.x & (lanes - 1)) * static_cast<uint64_t>(U); c < width; c += lanes * static_cast<uint64_t>(U)) {
+        float s[U] = {};
+        for (int k = 0; k < splits; ++k) {
+            const float* from = acc + (static_cast<uint64_t>(k) * ntokens + t) * width + c;
+            if constexpr (U == 1) {
+                s[0] += from[0];
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; u += 4) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(from + u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u + e] += v[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) s[u] = on ? s[u] * scale : 0.0f;
+        if constexpr (U == 1) F::st(out, t * ld + c, s[0]);
+        else stv_at<false>(out, (t * ld + c) * (16 / F::kEpv), F::pack(s));
     }
 }
 
 // grad_weight[v][h] = round(max |g| 2^-14 * sum).
-template <class F>
+template <class F, class T>
 struct WeightEpilogue {
     void* out;
     uint64_t ld;
     const RowScale* scale;
-    int vec;  // 4 elements at a time: the pitch and the address allow it
+    int vec;  // the elements that can be stored together: 1, 4, or 8 of 16 bits
 
     template <int MT, int NT, class S>
     __device__ __forceinline__ void operator()(Tile<MT, NT>& c, uint32_t m0, uint32_t n0, const GemmArgs& g, uint32_t,
-                                               uint32_t, const S&) const
+                                               uint32_t, const S& stage) const
     {
         const int lane = threadIdx.x & 63, quad = lane >> 4;
         const float s = scale->top * (1.0f / kDScale);
+        if constexpr (std::is_same<S, Staging>::value) {
+            if (vec == 8 && g.m % 8 == 0) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) c.v[i][j] *= s;
+                stage.template store_by_column<T>(c, static_cast<uint16_t*>(out), ld, g.n, g.m);
+                return;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const uint32_t v = n0 + j * 16 + (lane & 15);
@@ -443,7 +492,7 @@ struct WeightEpilogue {
                 float x[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[r] = c.v[i][j][r] * s;
-                if (vec && h + 3 < g.m) {
+                if (vec >= 4 && h + 3 < g.m) {
                     if constexpr (F::kEpv == 8)
                         *reinterpret_cast<u32x2*>(static_cast<char*>(out) + (row + h) * 2) = F::pack4(x);
                     else
@@ -461,37 +510,68 @@ struct WeightEpilogue {
 // ---------------------------------------------------------------------------
 // one call
 // ---------------------------------------------------------------------------
-int blocks_for(uint64_t units)
+uint64_t round_up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+
+// Threads a row of `units` and the grid that takes `rows` of them.
+int lanes_for(uint64_t units)
 {
-    const uint64_t want = (units + kBlock - 1) / kBlock;
-    return static_cast<int>(want < 1 ? 1 : want > 16384 ? 16384 : want);
+    int lanes = 1;
+    while (lanes < kBlock && static_cast<uint64_t>(lanes) < units) lanes *= 2;
+    return lanes;
+}
+dim3 grid_for(uint64_t rows, int lanes)
+{
+    const uint64_t per = kBlock / lanes;
+    return dim3(static_cast<uint32_t>((rows + per - 1) / per));
 }
 
-template <class F, int PARTS, bool IS_A>
+template <int PARTS>
 hipError_t pack(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, uint16_t* out, hipStream_t s)
 {
-    hipLaunchKernelGGL((pack_rows<F, PARTS, IS_A>), dim3(blocks_for(rows * pad)), dim3(kBlock), 0, s, in, ld, rows,
-                       width, pad, out);
+    constexpr uint64_t EB = PARTS == 1 ? 2 : 4;
+    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * EB % 16 == 0;
+    const int lanes = lanes_for(pad / 8);
+    if (vec) hipLaunchKernelGGL((pack_rows<PARTS, true>), grid_for(rows, lanes), dim3(kBlock), 0, s, in, ld, rows, width, pad, out, lanes);
+    else hipLaunchKernelGGL((pack_rows<PARTS, false>), grid_for(rows, lanes), dim3(kBlock), 0, s, in, ld, rows, width, pad, out, lanes);
     return hipGetLastError();
 }
 
-template <class T, class Epilogue>
-hipError_t logits(const GemmArgs& g, int tile_n, const Epilogue& epi, hipStream_t s)
+template <int PARTS>
+hipError_t transpose(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, uint16_t* out,
+                     const CrossEntropyArgs& a, int masked, hipStream_t s)
 {
-    if (tile_n == 16) return launch_gemm<T, 16, 8, 1>(g, epi, s);
-    if (tile_n == 64) return launch_gemm<T, 64, 4, 2>(g, epi, s);
-    return launch_gemm<T, 256, 2, 4>(g, epi, s);
+    constexpr uint64_t EB = PARTS == 1 ? 2 : 4;
+    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * EB % 16 == 0;
+    const dim3 grid(static_cast<uint32_t>(pad / 64), static_cast<uint32_t>((width + 63) / 64));
+    if (vec) hipLaunchKernelGGL((pack_transposed<PARTS, true>), grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked, a.ignore_index, a.vocab);
+    else hipLaunchKernelGGL((pack_transposed<PARTS, false>), grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked, a.ignore_index, a.vocab);
+    return hipGetLastError();
 }
+
+template <class T, int PARTS, class Epilogue>
+hipError_t product(const GemmArgs& g, int tile_n, const Epilogue& epi, hipStream_t s)
+{
+    if constexpr (PARTS == kPieces) {
+        return launch_gemm_pieces(g, epi, s);
+    } else {
+        if (tile_n == 16) return launch_gemm<T, 16, 8, 1>(g, epi, s);
+        if (tile_n == 64) return launch_gemm<T, 64, 4, 2>(g, epi, s);
+        return launch_gemm_large<T>(g, epi, s);
+    }
+}
+
+// Rows of statistics that a tile of kTileM vocabulary rows leaves: one for
+// each wave along it.
+uint64_t stat_rows_per_tile(int tile_n) { return tile_n == 16 ? 8 : tile_n == 256 ? 2 : 4; }
 
 // F: the storage type; T: the matrix instruction's.
 template <class F, class T, int PARTS>
 struct Call {
+    static constexpr int EB = 16 / F::kEpv;
     const CrossEntropyArgs& a;
     const CrossEntropyPlan& p;
     char* ws;
     hipStream_t s;
-
-    uint64_t part_k() const { return p.k_pad / PARTS; }
 
     // The logits' operands, packed where the plan says so.
     hipError_t hidden(const uint16_t** out, uint64_t* ld) const
@@ -503,12 +583,12 @@ struct Call {
         }
         uint16_t* to = reinterpret_cast<uint16_t*>(ws + p.hidden);
         *out = to;
-        *ld = p.k_pad;
-        return pack<F, PARTS, false>(a.hidden, a.ld_hidden, a.ntokens, a.width, part_k(), to, s);
+        *ld = p.k_pad * PARTS;
+        return pack<PARTS>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.k_pad, to, s);
     }
     hipError_t weight(uint64_t v0, uint64_t rows, const uint16_t** out, uint64_t* ld) const
     {
-        const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * (16 / F::kEpv);
+        const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * EB;
         if (!p.pack_weight) {
             *out = reinterpret_cast<const uint16_t*>(from);
             *ld = a.ld_weight;
@@ -516,8 +596,8 @@ struct Call {
         }
         uint16_t* to = reinterpret_cast<uint16_t*>(ws + p.weight);
         *out = to;
-        *ld = p.k_pad;
-        return pack<F, PARTS, true>(from, a.ld_weight, rows, a.width, part_k(), to, s);
+        *ld = p.k_pad * PARTS;
+        return pack<PARTS>(from, a.ld_weight, rows, a.width, p.k_pad, to, s);
     }
     GemmArgs logits_args(const uint16_t* w, uint64_t ldw, const uint16_t* x, uint64_t ldx, uint64_t rows) const
     {
@@ -528,7 +608,8 @@ struct Call {
         g.ldb = ldx;
         g.m = static_cast<uint32_t>(rows);
         g.n = static_cast<uint32_t>(a.ntokens);
-        g.k = g.k_all = static_cast<uint32_t>(p.k_pad);
+        // an operand that lies as given ends at the width, which is then a multiple of 8
+        g.k = g.k_all = static_cast<uint32_t>(p.pack_hidden && p.pack_weight ? p.k_pad : a.width);
         g.splits = 1;
         return g;
     }
@@ -541,17 +622,23 @@ struct Call {
         if (e != hipSuccess) return e;
         Stats* stats = reinterpret_cast<Stats*>(ws + p.stats);
         float* target_logit = reinterpret_cast<float*>(ws + p.target_logit);
-        const uint64_t waves_m = p.tile_n == 16 ? 8 : p.tile_n == 64 ? 4 : 2;
-        for (uint64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
-            const uint64_t rows = a.vocab - v0 < p.piece ? a.vocab - v0 : p.piece;
+        const uint64_t piece = p.pack_weight ? p.piece : a.vocab;  // pieces bound what is packed
+        for (uint64_t v0 = 0; v0 < a.vocab; v0 += piece) {
+            const uint64_t rows = a.vocab - v0 < piece ? a.vocab - v0 : piece;
             if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
             const StatsEpilogue epi{stats, target_logit, a.targets, a.ignore_index, a.vocab, v0, row0};
-            if ((e = logits<T>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
-            row0 += (rows + kTileM - 1) / kTileM * waves_m;
+            if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
+            row0 += (rows + kTileM - 1) / kTileM * stat_rows_per_tile(p.tile_n);
         }
-        hipLaunchKernelGGL(join_stats, dim3(static_cast<uint32_t>((a.ntokens + 15) / 16)), dim3(kBlock), 0, s, stats,
-                           row0, target_logit, a.targets, a.ignore_index, a.vocab, a.ntokens, a.losses, a.lse);
-        return hipGetLastError();
+        auto join = [&](auto kernel, uint32_t tokens) {
+            hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.ntokens + tokens - 1) / tokens)), dim3(kJoinBlock), 0,
+                               s, stats, row0, target_logit, a.targets, a.ignore_index, a.vocab, a.ntokens, a.losses,
+                               a.lse);
+            return hipGetLastError();
+        };
+        if (a.ntokens <= 32) return join(join_stats<1>, 1);
+        if (a.ntokens <= 512) return join(join_stats<4>, 4);
+        return join(join_stats<16>, 16);
     }
 
     hipError_t backward() const
@@ -566,40 +653,35 @@ struct Call {
         uint16_t* xt = reinterpret_cast<uint16_t*>(ws + p.hidden_t);
         float* acc = reinterpret_cast<float*>(ws + p.grad_hidden_acc);
         RowScale* scale = reinterpret_cast<RowScale*>(ws + p.row_scale);
-        const uint32_t cols = static_cast<uint32_t>((a.width + 63) / 64);
         hipLaunchKernelGGL(row_scale, dim3(1), dim3(1024), 0, s, a.grad_losses, a.targets, a.ignore_index, a.vocab,
                            a.ntokens, scale);
-        if (dt && a.ntokens)
-            hipLaunchKernelGGL((pack_transposed<F, PARTS>), dim3(static_cast<uint32_t>(p.t_pad / 64), cols),
-                               dim3(kBlock), 0, s, a.hidden, a.ld_hidden, a.ntokens, a.width, p.t_pad, xt, a.targets, 1,
-                               a.ignore_index, a.vocab);
         if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (dt && a.ntokens &&
+            (e = transpose<PARTS>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.t_pad, xt, a, 1, s)) != hipSuccess)
+            return e;
         for (uint64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
             const uint64_t rows = a.vocab - v0 < p.piece ? a.vocab - v0 : p.piece;
-            const uint64_t pad = (rows + kTileK - 1) / kTileK * kTileK;
+            const uint64_t pad = round_up(rows, kTileK);
             if (a.ntokens) {  // no token: the weight's gradient is the empty sum
                 if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
-                const DEpilogue<T, PARTS> epi{d, dt, a.lse, a.grad_losses, scale, a.targets,
-                                                               a.ignore_index, a.vocab, v0, pad, p.t_pad};
-                if ((e = logits<T>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
+                const DEpilogue<T> epi{d, dt, a.lse, a.grad_losses, scale, a.targets, a.ignore_index, a.vocab, v0, pad,
+                                       p.t_pad};
+                if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
             }
             if (d) {
-                const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * (16 / F::kEpv);
-                hipLaunchKernelGGL((pack_transposed<F, PARTS>), dim3(static_cast<uint32_t>(pad / 64), cols),
-                                   dim3(kBlock), 0, s, from, a.ld_weight, rows, a.width, pad, wt, a.targets, 0,
-                                   a.ignore_index, a.vocab);
-                if ((e = hipGetLastError()) != hipSuccess) return e;
+                const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * EB;
+                if ((e = transpose<PARTS>(from, a.ld_weight, rows, a.width, pad, wt, a, 0, s)) != hipSuccess) return e;
                 GemmArgs g{};
                 g.a = wt;
                 g.b = d;
                 g.lda = g.ldb = pad * PARTS;
                 g.m = static_cast<uint32_t>(a.width);
                 g.n = static_cast<uint32_t>(a.ntokens);
-                g.k_all = static_cast<uint32_t>(pad * PARTS);
+                g.k_all = static_cast<uint32_t>(pad);
                 g.splits = static_cast<uint32_t>(p.splits);
-                g.k = (g.k_all / kTileK + g.splits - 1) / g.splits * kTileK;
+                g.k = static_cast<uint32_t>(round_up((pad + p.splits - 1) / p.splits, kTileK));
                 const HiddenEpilogue he{acc, a.width, v0 > 0};
-                if ((e = logits<T>(g, p.tile_n, he, s)) != hipSuccess) return e;
+                if ((e = product<T, PARTS>(g, p.tile_n, he, s)) != hipSuccess) return e;
             }
             if (dt) {
                 GemmArgs g{};
@@ -608,26 +690,55 @@ struct Call {
                 g.lda = g.ldb = p.t_pad * PARTS;
                 g.m = static_cast<uint32_t>(a.width);
                 g.n = static_cast<uint32_t>(rows);
-                g.k = g.k_all = static_cast<uint32_t>(p.t_pad * PARTS);
+                g.k = g.k_all = static_cast<uint32_t>(p.t_pad);
                 g.splits = 1;
-                constexpr int EB = 16 / F::kEpv;
                 char* out = static_cast<char*>(a.grad_weight) + v0 * a.ld_grad_weight * EB;
-                const WeightEpilogue<F> we{out, a.ld_grad_weight, scale,
-                                           reinterpret_cast<uintptr_t>(out) % (4 * EB) == 0 && a.ld_grad_weight % 4 == 0};
-                if ((e = launch_gemm<T, 256, 2, 4>(g, we, s)) != hipSuccess) return e;
+                const uintptr_t mis = reinterpret_cast<uintptr_t>(out) | a.ld_grad_weight * EB;
+                const int vec = EB == 2 && mis % 16 == 0 ? 8 : mis % (4 * EB) == 0 ? 4 : 1;
+                const WeightEpilogue<F, T> we{out, a.ld_grad_weight, scale, vec};
+                if ((e = product<T, PARTS>(g, 256, we, s)) != hipSuccess) return e;
             }
         }
         if (d) {
-            hipLaunchKernelGGL((finish_hidden<F>), dim3(blocks_for(a.ntokens * a.width)), dim3(kBlock), 0, s, acc,
-                               p.splits, a.grad_losses, a.targets, a.ignore_index, a.vocab, a.ntokens, a.width,
-                               a.grad_hidden, a.ld_grad_hidden);
-            e = hipGetLastError();
+            const bool vec = a.width % F::kEpv == 0 && a.width % 4 == 0 && a.ld_grad_hidden % F::kEpv == 0 &&
+                             reinterpret_cast<uintptr_t>(a.grad_hidden) % 16 == 0;
+            const int lanes = lanes_for(vec ? a.width / F::kEpv : a.width);
+            auto finish = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, grid_for(a.ntokens, lanes), dim3(kBlock), 0, s, acc, p.splits, a.grad_losses,
+                                   a.targets, a.ignore_index, a.vocab, a.ntokens, a.width, a.grad_hidden,
+                                   a.ld_grad_hidden, lanes);
+                return hipGetLastError();
+            };
+            e = vec ? finish(finish_hidden<F, F::kEpv>) : finish(finish_hidden<F, 1>);
         }
         return e;
     }
 };
 
-uint64_t round_up(uint64_t x, uint64_t m) { return (x + m - 1) / m * m; }
+// What a call's products cost with pieces of `piece` rows, in depth steps of
+// the busiest CU: a product takes whole rounds of one tile a CU. `splits`
+// gets the best number of parts for the hidden gradient's sum.
+constexpr uint64_t kCUs = 256;
+double piece_cost(uint64_t rows, uint64_t ntokens, uint64_t width, uint64_t tile_n, uint64_t step, int* splits)
+{
+    auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
+    const uint64_t tv = up(rows, kTileM), tn = up(ntokens, tile_n), tw = up(width, kTileM);
+    const uint64_t tile_w = step == kPieceDepth ? kPiecesN : 256;
+    // each round also costs about four steps to start and to end in
+    double cost = static_cast<double>(up(tv * tn, kCUs) * (up(width, step) + 8)) +
+                  static_cast<double>(up(up(rows, tile_w) * tw, kCUs) * (up(ntokens, step) + 4));
+    double best = 0;
+    for (int k = 1; k <= 16; k *= 2) {
+        if (k > 1 && rows / k < 512) break;
+        // a part of the sum is written and read again: about a step for each of a tile's
+        const double c = static_cast<double>(up(tw * tn * k, kCUs) * (up(up(rows, step), k) + 8)) + 2.0 * (k - 1);
+        if (k == 1 || c < best) {
+            best = c;
+            *splits = k;
+        }
+    }
+    return cost + best + 24;  // four launches
+}
 
 }  // namespace
 
@@ -635,48 +746,58 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
 {
     CrossEntropyPlan p{};
     const bool f32 = dtype == AR_FLOAT32;
-    p.parts = f32 ? kF32Parts : 1;
-    // six parts of a multiple of 32 are a multiple of kTileK
-    p.k_pad = f32 ? round_up(width, 32) * p.parts : round_up(width, kTileK);
+    const uint64_t parts = f32 ? kPieces : 1, step = f32 ? kPieceDepth : kTileK;
+    p.k_pad = round_up(width, step);
     p.t_pad = round_up(ntokens, kTileK);
     // (backward, the tiles cover all of t_pad: they write its zeros)
-    p.tile_n = ntokens <= 16 && !backward ? 16 : ntokens <= 64 ? 64 : 256;
+    p.tile_n = f32 ? kPiecesN : ntokens <= 16 && !backward ? 16 : ntokens <= 64 ? 64 : 256;
     p.pack_hidden = p.pack_weight = true;  // the caller clears these where the operands can be read as they lie
-    // A piece's buffers come to about kPieceBytes; pieces are whole tiles.
-    constexpr uint64_t kPieceBytes = uint64_t(640) << 20;
-    uint64_t a_row = 2 * p.k_pad;
-    if (backward) a_row += 2 * p.parts * (2 * p.t_pad + width);
-    uint64_t piece = kPieceBytes / a_row / kTileM * kTileM;
-    if (piece < kTileM) piece = kTileM;
-    const uint64_t whole = round_up(vocab, kTileM);
-    const uint64_t pieces = (whole + piece - 1) / piece;
-    p.piece = round_up((vocab + pieces - 1) / (pieces ? pieces : 1), kTileM);
-    if (p.piece == 0) p.piece = kTileM;
-    p.piece_pad = p.piece;
-    // The hidden gradient sums over a piece: its product is split along that
-    // axis until there are a few workgroups for each CU.
-    const uint64_t tiles = (round_up(width, kTileM) / kTileM) * ((ntokens + p.tile_n - 1) / p.tile_n);
+    // A piece's buffers come to at most about kPieceBytes; pieces are whole tiles.
+    constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
+    const uint64_t row_bytes = 2 * parts * (p.k_pad + (backward ? 2 * p.t_pad + width : 0));
+    const uint64_t whole = round_up(vocab, kTileM) / kTileM;
+    uint64_t most = kPieceBytes / (row_bytes * kTileM);
+    if (most > 4096) most = 4096;  // the transposed piece's rows stay within a buffer's 2^31 bytes
+    most = most < 1 ? 1 : most > whole ? whole : most;
     p.splits = 1;
-    while (p.splits < 16 && tiles * p.splits < 256 && p.piece / (2 * p.splits) >= 512) p.splits *= 2;
-    const uint64_t waves_m = p.tile_n == 16 ? 8 : p.tile_n == 64 ? 4 : 2;
-    const uint64_t tiles_v = (p.piece / kTileM) * ((vocab + p.piece - 1) / p.piece);
-    p.stat_rows = tiles_v * waves_m;
+    if (!backward) {
+        const uint64_t pieces = (whole + most - 1) / most;
+        p.piece = (whole + pieces - 1) / pieces * kTileM;
+    } else {
+        // From half the largest size on, the one whose tiles fill the CUs best.
+        // 8192 x 131072 x 4096: pieces of 16384 rows end in full rounds, of
+        // 13312 the weight gradient's 832 tiles take four rounds for 3.25.
+        double best = 0;
+        const uint64_t stride = most / 64 + 1;
+        for (uint64_t m = most; m >= (most + 1) / 2 && m >= 1; m = m > stride ? m - stride : 0) {
+            const uint64_t rows = m * kTileM, full = vocab / rows, rest = vocab - full * rows;
+            int splits = 1, unused;
+            double c = piece_cost(full ? rows : rest, ntokens, width, p.tile_n, step, &splits) * (full ? full : 1);
+            if (full && rest) c += piece_cost(rest, ntokens, width, p.tile_n, step, &unused);
+            if (best == 0 || c < best) {
+                best = c;
+                p.piece = rows;
+                p.splits = splits;
+            }
+        }
+    }
+    p.stat_rows = (vocab + p.piece - 1) / p.piece * (p.piece / kTileM) * stat_rows_per_tile(p.tile_n);
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
         at += round_up(bytes, 256);
         return here;
     };
-    p.hidden = take(ntokens * p.k_pad * 2);
-    p.weight = take(p.piece * p.k_pad * 2);
+    p.hidden = take(ntokens * p.k_pad * parts * 2);
+    p.weight = take(p.piece * p.k_pad * parts * 2);
     if (!backward) {
         p.stats = take(p.stat_rows * ntokens * sizeof(Stats));
         p.target_logit = take(ntokens * 4);
     } else {
-        p.d = take(ntokens * p.piece_pad * p.parts * 2);
-        p.dt = take(p.piece * p.t_pad * p.parts * 2);
-        p.weight_t = take(width * p.piece_pad * p.parts * 2);
-        p.hidden_t = take(width * p.t_pad * p.parts * 2);
+        p.d = take(ntokens * p.piece * parts * 2);
+        p.dt = take(p.piece * p.t_pad * parts * 2);
+        p.weight_t = take(width * p.piece * parts * 2);
+        p.hidden_t = take(width * p.t_pad * parts * 2);
         p.grad_hidden_acc = take(static_cast<uint64_t>(p.splits) * ntokens * width * 4);
         p.row_scale = take(sizeof(RowScale));
     }
@@ -688,7 +809,7 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPla
                                 hipStream_t stream)
 {
     switch (dtype) {
-    case AR_FLOAT32: return Call<F32, MmaBF16, kF32Parts>{a, p, ws, stream}.forward();
+    case AR_FLOAT32: return Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.forward();
     case AR_FLOAT16: return Call<F16, MmaF16, 1>{a, p, ws, stream}.forward();
     case AR_BFLOAT16: return Call<BF16, MmaBF16, 1>{a, p, ws, stream}.forward();
     default: return hipErrorInvalidValue;
@@ -699,7 +820,7 @@ hipError_t launch_cross_entropy_backward(const CrossEntropyArgs& a, const CrossE
                                          char* ws, hipStream_t stream)
 {
     switch (dtype) {
-    case AR_FLOAT32: return Call<F32, MmaBF16, kF32Parts>{a, p, ws, stream}.backward();
+    case AR_FLOAT32: return Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.backward();
     case AR_FLOAT16: return Call<F16, MmaF16, 1>{a, p, ws, stream}.backward();
     case AR_BFLOAT16: return Call<BF16, MmaBF16, 1>{a, p, ws, stream}.backward();
     default: return hipErrorInvalidValue;

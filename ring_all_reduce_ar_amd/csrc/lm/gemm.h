@@ -1,12 +1,12 @@
-// gemm.h -- the matrix-core product that the cross entropy is made of.
+// gemm.h -- the matrix-core products that the cross entropy is made of.
 //
 //   C[m][n] = sum_k A[m][k] * B[n][k]
 //
-// for 16-bit A and B whose rows are contiguous along K, 16-byte aligned and a
-// multiple of kTileK long; C stays in fp32 registers and goes to an epilogue.
-// A workgroup takes kTileM rows of A and BN of B; 64-deep tiles of both go
-// from memory straight into LDS, two stages deep, so that the loads of one
-// stage run under the matrix instructions of the other.
+// for 16-bit A and B whose rows are contiguous along K and 16-byte aligned; C
+// stays in fp32 registers and goes to an epilogue. Tiles of both go from
+// memory straight into LDS. Three kernels: gemm_large for 256 x 256 tiles,
+// gemm_pieces for fp32 operands in three bf16 pieces, and gemm for few rows
+// of B, which is bound by reading A.
 //
 // LDS holds 128-byte rows as eight 16-byte columns; column c of row r lies at
 // c ^ (r & 7), so that the 16 rows of a fragment read spread over all banks.
@@ -55,15 +55,14 @@ struct MmaF16 {
     }
 };
 
-// Rows of A and B beyond M and N are read as the last ones (their results are
-// dropped by the epilogue), so no access leaves the operands.
+// Rows of A and B beyond M and N, and depths beyond k_all, are read as zeros.
 struct GemmArgs {
     const uint16_t* a;
     const uint16_t* b;
     uint64_t lda, ldb;  // elements
     uint32_t m, n;
-    uint32_t k;         // of one split; a multiple of kTileK
-    uint32_t k_all;     // splits * k may pass it
+    uint32_t k;         // of one split; a multiple of kTileK if there are several
+    uint32_t k_all;     // a multiple of 8 (of 32 for pieces); splits * k may pass it
     uint32_t tiles_m, tiles_n, splits;
 };
 
@@ -73,6 +72,18 @@ template <int MT, int NT>
 struct Tile {
     f32x4 v[MT][NT];
 };
+
+// A byte offset that lies past every buffer: the load gives zeros.
+constexpr uint32_t kPastEnd = 0x80000000u;
+
+// 64 rows from row `r0` of a matrix of `rows` rows; rows past the end lie
+// outside the buffer.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, uint64_t ld, uint32_t r0, uint32_t rows)
+{
+    const uint32_t left = rows > r0 ? min(rows - r0, 64u) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p + static_cast<uint64_t>(r0) * ld), 0,
+                                             static_cast<int>(left * static_cast<uint32_t>(ld) * 2), 0x00020000);
+}
 
 // Workgroups go round the eight XCDs one by one; each XCD gets a contiguous
 // part of the tile order, in which tiles of eight row blocks follow each
@@ -183,8 +194,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
     constexpr int BM = kTileM, BK = kTileK;
     constexpr int THREADS = 64 * WM * WN;
     constexpr int MT = BM / (16 * WM), NT = BN / (16 * WN);
-    constexpr int A_LOADS = BM * 8 / THREADS;                        // 16-byte loads of a thread for one stage of A
-    constexpr int B_LOADS = (BN * 8 + THREADS - 1) / THREADS;
+    static_assert(THREADS == 512 && BN <= 64, "a load takes 64 rows");
+    constexpr int A_LOADS = BM * 8 / THREADS;  // 16-byte loads of a thread for one stage of A
     __shared__ __attribute__((aligned(1024))) uint16_t lds_a[2][BM * BK];
     __shared__ __attribute__((aligned(1024))) uint16_t lds_b[2][BN * BK];
 
@@ -195,39 +206,22 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
     const int wm = wave / WN, wn = wave % WN;
     const uint32_t m_base = tm * BM, n_base = tn * BN;
     const uint32_t k0 = split * g.k;
-    const uint32_t k1 = min(k0 + g.k, g.k_all);
-
-    const uint16_t* pa[A_LOADS];
-    const uint16_t* pb[B_LOADS];
+    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
+    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
+    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) * 2 + col * 2;
+    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) * 2 + col * 2;
+    auto load = [&](int stage, uint32_t k) {
+        typedef __attribute__((address_space(3))) void lds_void;
+        const bool in = k + col < depth;
 #pragma unroll
-    for (int i = 0; i < A_LOADS; ++i) {
-        const int at = i * THREADS + tid, row = at >> 3, col = (at & 7) ^ (row & 7);
-        const uint32_t r = min(m_base + row, g.m - 1);
-        pa[i] = g.a + static_cast<uint64_t>(r) * g.lda + k0 + col * 8;
-    }
-#pragma unroll
-    for (int i = 0; i < B_LOADS; ++i) {
-        const int at = i * THREADS + tid, row = at >> 3, col = (at & 7) ^ (row & 7);
-        const uint32_t r = min(n_base + row, g.n - 1);
-        pb[i] = g.b + static_cast<uint64_t>(r) * g.ldb + k0 + col * 8;
-    }
-    auto load = [&](int stage) {
-#pragma unroll
-        for (int i = 0; i < A_LOADS; ++i) {
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)pa[i],
-                                             (__attribute__((address_space(3))) void*)(&lds_a[stage][(i * THREADS + wave * 64) * 8]),
-                                             16, 0, 0);
-            pa[i] += BK;
-        }
-#pragma unroll
-        for (int i = 0; i < B_LOADS; ++i) {
-            if ((BN * 8) % THREADS == 0 || i * THREADS + wave * 64 < BN * 8) {  // the same for a whole wave
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)pb[i],
-                                                 (__attribute__((address_space(3))) void*)(&lds_b[stage][(i * THREADS + wave * 64) * 8]),
-                                                 16, 0, 0);
-                pb[i] += BK;
-            }
-        }
+        for (int i = 0; i < A_LOADS; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.a + k0, g.lda, m_base + i * 64, g.m),
+                                                     (lds_void*)(&lds_a[stage][(i * THREADS + wave * 64) * 8]), 16,
+                                                     in ? off_a : kPastEnd, k * 2, 0, 0);
+        if (BN == 64 || wave * 8 < BN)  // the same for a whole wave
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.b + k0, g.ldb, n_base, g.n),
+                                                     (lds_void*)(&lds_b[stage][wave * 64 * 8]), 16,
+                                                     in ? off_b : kPastEnd, k * 2, 0, 0);
     };
 
     Tile<MT, NT> acc;
@@ -237,11 +231,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
         for (int j = 0; j < NT; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int frow = lane & 15, fcol = lane >> 4;
-    if (k0 < k1) load(0);  // a split past the end has nothing to add
+    if (depth) load(0, 0);  // a split past the end has nothing to add
     int stage = 0;
-    for (uint32_t k = k0; k < k1; k += BK, stage ^= 1) {
+    for (uint32_t k = 0; k < depth; k += BK, stage ^= 1) {
         __syncthreads();  // this stage has arrived, and nobody reads the other one any more
-        if (k + BK < k1) load(stage ^ 1);
+        if (k + BK < depth) load(stage ^ 1, k + BK);
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk) {
             const int col = ((kk * 4 + fcol) ^ (frow & 7)) * 8;
@@ -266,9 +260,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epi
 // ---------------------------------------------------------------------------
 // the large tile
 // ---------------------------------------------------------------------------
-// A byte offset that lies past every buffer: the load gives zeros.
-constexpr uint32_t kPastEnd = 0x80000000u;
-
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // Twelve 16-byte fragments from LDS and the wait for them: four groups of 16
@@ -326,15 +317,6 @@ __device__ __forceinline__ void meet()
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-}
-
-// 64 rows from row `r0` of a matrix of `rows` rows; rows past the end lie
-// outside the buffer.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, uint64_t ld, uint32_t r0, uint32_t rows)
-{
-    const uint32_t left = rows > r0 ? min(rows - r0, 64u) : 0;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p + static_cast<uint64_t>(r0) * ld), 0,
-                                             static_cast<int>(left * static_cast<uint32_t>(ld) * 2), 0x00020000);
 }
 
 // 256 x 256 x 64 tiles, 8 waves of 128 x 64. The two waves of a SIMD (w and
@@ -439,16 +421,275 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
     epi(acc, m_base + wm * 128, n_base + wn * 64, g, tm * 2 + wm, split, Staging{lds, wm * 128u, wn * 64u, m_base, n_base});
 }
 
+// ---------------------------------------------------------------------------
+// fp32 operands in three bf16 pieces
+// ---------------------------------------------------------------------------
+// x = x1 + x2 + x3 with 8 significant bits each. A row holds, for each 32 of
+// its depth, 32 first pieces, 32 second and 32 third ones (192 bytes). Six of
+// the nine products of pieces are summed: the other three are below 2^-24 of
+// the whole.
+constexpr int kPieces = 3;
+constexpr int kPieceDepth = 32;
+constexpr int kPiecesN = 128;  // columns of a tile
+
+// Twelve fragments: two groups of 16 rows at x and two at y, three pieces each.
+template <int X_OFF, int Y_OFF>
+__device__ __forceinline__ void read_pieces(i32x4 (&x0)[3], i32x4 (&x1)[3], i32x4 (&y0)[3], i32x4 (&y1)[3], uint32_t x,
+                                            uint32_t y)
+{
+    asm volatile(
+        "ds_read_b128 %0, %12 offset:%14\n"
+        "ds_read_b128 %1, %12 offset:%15\n"
+        "ds_read_b128 %2, %12 offset:%16\n"
+        "ds_read_b128 %3, %12 offset:%17\n"
+        "ds_read_b128 %4, %12 offset:%18\n"
+        "ds_read_b128 %5, %12 offset:%19\n"
+        "ds_read_b128 %6, %13 offset:%20\n"
+        "ds_read_b128 %7, %13 offset:%21\n"
+        "ds_read_b128 %8, %13 offset:%22\n"
+        "ds_read_b128 %9, %13 offset:%23\n"
+        "ds_read_b128 %10, %13 offset:%24\n"
+        "ds_read_b128 %11, %13 offset:%25\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x0[0]), "=&v"(x0[1]), "=&v"(x0[2]), "=&v"(x1[0]), "=&v"(x1[1]), "=&v"(x1[2]), "=&v"(y0[0]),
+          "=&v"(y0[1]), "=&v"(y0[2]), "=&v"(y1[0]), "=&v"(y1[1]), "=&v"(y1[2])
+        : "v"(x), "v"(y), "n"(X_OFF), "n"(X_OFF + 8192), "n"(X_OFF + 16384), "n"(X_OFF + 1024), "n"(X_OFF + 9216),
+          "n"(X_OFF + 17408), "n"(Y_OFF), "n"(Y_OFF + 8192), "n"(Y_OFF + 16384), "n"(Y_OFF + 1024), "n"(Y_OFF + 9216),
+          "n"(Y_OFF + 17408)
+        : "memory");
+}
+
+// All but the newest nine direct loads have arrived, in every wave.
+__device__ __forceinline__ void arrive9()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(9)\n s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A 256 x 128 tile of 16-bit values in the layout of pieces leaves in two
+// halves, each in whole rows.
+struct PieceStaging {
+    static constexpr bool kOn = true;
+    char* lds;
+    uint32_t wm, wn;          // the wave's 64 rows and 64 columns within the tile
+    uint32_t m_base, n_base;  // the tile's
+
+    static __device__ __forceinline__ uint32_t byte_of(uint32_t k, uint32_t piece)
+    {
+        return (k >> 5) * 192 + piece * 64 + (k & 31) * 2;
+    }
+
+    // out[n][m in pieces] for the first `rows` n and `cols` m (a multiple of 32).
+    template <class Split>
+    __device__ __forceinline__ void store_by_column(const Tile<4, 4>& x, uint16_t* out, uint64_t ld, uint32_t rows,
+                                                    uint32_t cols, Split split) const
+    {
+        constexpr uint32_t kRow = 256 * 6 + 16;  // the 16 keep the rows of a write off each other's banks
+        const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
+        for (uint32_t half = 0; half < 2; ++half) {
+            __syncthreads();
+            if (wn == half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        char* row = lds + (j * 16 + (lane & 15)) * kRow;
+                        uint32_t p[4][3];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) split(x.v[i][j][r], p[r]);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            *reinterpret_cast<u32x2*>(row + byte_of(wm * 64 + i * 16 + quad * 4, k)) =
+                                u32x2{p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16)};
+                    }
+                }
+            }
+            __syncthreads();
+            copy_rows<96, kRow>(out, ld, n_base + half * 64, 64, rows, m_base * 3, cols * 3);
+        }
+    }
+
+    // out[m][n in pieces]; neighbouring columns are exchanged as in Staging.
+    template <class Split>
+    __device__ __forceinline__ void store_by_row(const Tile<4, 4>& x, const float (&factor)[4], uint16_t* out,
+                                                 uint64_t ld, uint32_t rows, uint32_t cols, Split split) const
+    {
+        constexpr uint32_t kRow = 128 * 6 + 16;
+        const uint32_t lane = threadIdx.x & 63, quad = lane >> 4, odd = lane & 1;
+        for (uint32_t half = 0; half < 2; ++half) {
+            __syncthreads();
+            if (wm >> 1 == half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        char* row = lds + ((wm & 1) * 64 + i * 16 + quad * 4 + odd * 2) * kRow;
+                        uint32_t p[4][3];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) split(x.v[i][j][r] * factor[j], p[r]);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const uint32_t p01 = p[0][k] | (p[1][k] << 16), p23 = p[2][k] | (p[3][k] << 16);
+                            const uint32_t give = odd ? p01 : p23, keep = odd ? p23 : p01;
+                            const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+                            const uint32_t lo = odd ? got : keep, hi = odd ? keep : got;
+                            const uint32_t at = byte_of(wn * 64 + j * 16 + (lane & 14), k);
+                            *reinterpret_cast<uint32_t*>(row + at) = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+                            *reinterpret_cast<uint32_t*>(row + kRow + at) = __builtin_amdgcn_perm(hi, lo, 0x07060302);
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+            copy_rows<48, kRow>(out, ld, m_base + half * 128, 128, rows, n_base * 3, cols * 3);
+        }
+    }
+
+private:
+    template <uint32_t CHUNKS, uint32_t ROW>
+    __device__ __forceinline__ void copy_rows(uint16_t* out, uint64_t ld, uint32_t row0, uint32_t high, uint32_t rows,
+                                              uint32_t col0, uint32_t cols) const
+    {
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x; i < high * CHUNKS; i += 512) {
+            const uint32_t r = i / CHUNKS, c = i % CHUNKS;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * ROW + c * 16);
+            if (row0 + r < rows && col0 + c * 8 < cols)
+                *reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(row0 + r) * ld + col0 + c * 8) = v;
+        }
+    }
+};
+
+// gemm_large's scheme on 256 x 128 x 32 tiles of three pieces, 8 waves of 64 x
+// 64: 48 matrix instructions a half step. g.k, g.k_all: depths; lda, ldb: three
+// times the padded depth.
+template <class Epilogue>
+__global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Epilogue epi)
+{
+    using T = MmaBF16;
+    constexpr uint32_t kStage = 73728, kA1 = 24576, kB = 49152;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+    uint32_t tm, tn, split;
+    tile_of_workgroup(g, &tm, &tn, &split);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t wm = wave >> 1, wn = wave & 1;
+    const uint32_t m_base = tm * 256, n_base = tn * kPiecesN;
+    const uint32_t k0 = split * g.k;
+    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
+    const uint32_t steps = depth / kPieceDepth;
+
+    // A load takes 128 rows of one piece: the first or the last 32 of each
+    // wave's 64 rows of A, or the rows of B. 64-byte rows of four 16-byte
+    // columns; column c of row r lies at c ^ (r / 2 & 3).
+    const uint32_t row = tid >> 2, col = (tid & 3) ^ ((row >> 1) & 3);
+    const uint32_t off_a = ((row >> 5) * 64 + (row & 31)) * static_cast<uint32_t>(g.lda) * 2 + col * 16;
+    const uint32_t off_b = row * static_cast<uint32_t>(g.ldb) * 2 + col * 16;
+    auto rows_from = [&](const uint16_t* p, uint64_t ld, uint32_t r0, uint32_t rows) {
+        const uint32_t left = rows > r0 ? min(rows - r0, 256u) : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint16_t*>(p + static_cast<uint64_t>(k0) * kPieces + static_cast<uint64_t>(r0) * ld), 0,
+            static_cast<int>(left * static_cast<uint32_t>(ld) * 2), 0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t ra0 = rows_from(g.a, g.lda, m_base, g.m), ra1 = rows_from(g.a, g.lda, m_base + 32, g.m);
+    const __amdgpu_buffer_rsrc_t rb = rows_from(g.b, g.ldb, n_base, g.n);
+    auto fetch = [&](__amdgpu_buffer_rsrc_t x, uint32_t to, uint32_t off, uint32_t step) {
+        typedef __attribute__((address_space(3))) void lds_void;
+        const uint32_t v = step < steps ? off : kPastEnd, at = step * (kPieceDepth * kPieces * 2);
+        char* p = lds + to + wave * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)p, 16, v, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)(p + 8192), 16, v, at + 64, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)(p + 16384), 16, v, at + 128, 0, 0);
+    };
+
+    Tile<4, 4> acc;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    i32x4 fa0[2][3], fa1[2][3], fb[4][3];
+    auto multiply = [&](i32x4 (&f)[2][3], int i0) {
+        constexpr int kOfA[6] = {2, 1, 0, 1, 0, 0}, kOfB[6] = {0, 1, 2, 0, 1, 0};
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int k = 0; k < 6; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc.v[i0 + i][j] = T::mma(__builtin_bit_cast(T::Frag, f[i][kOfA[k]]),
+                                              __builtin_bit_cast(T::Frag, fb[j][kOfB[k]]), acc.v[i0 + i][j]);
+        __builtin_amdgcn_s_setprio(0);
+    };
+
+    if (steps) {
+        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+        const uint32_t frow = lane & 15, fcol = lane >> 4;
+        const uint32_t swizzled = (fcol ^ ((frow >> 1) & 3)) * 16;
+        uint32_t pa = base + (wm * 32 + frow) * 64 + swizzled, pa_next = pa + kStage;
+        uint32_t pb = base + kB + (wn * 64 + frow) * 64 + swizzled, pb_next = pb + kStage;
+        fetch(ra0, 0, off_a, 0);
+        fetch(rb, kB, off_b, 0);
+        fetch(ra1, kA1, off_a, 0);
+        fetch(ra0, kStage, off_a, 1);
+        fetch(rb, kStage + kB, off_b, 1);
+        arrive9();
+        read_pieces<0, 0>(fa0[0], fa0[1], fa1[0], fa1[1], pa, pa);
+        meet();  // the first quarter is read: step 0 loads it again
+        if (wave >= 4) meet();
+        uint32_t stage = 0, other = kStage;
+        for (uint32_t k = 0; k < steps; ++k) {
+            fetch(ra1, other + kA1, off_a, k + 1);
+            fetch(ra0, stage, off_a, k + 2);
+            read_pieces<0, 2048>(fb[0], fb[1], fb[2], fb[3], pb, pb);
+            arrive9();
+            multiply(fa0, 0);
+            meet();
+            fetch(rb, stage + kB, off_b, k + 2);
+            read_pieces<kA1, 0>(fa1[0], fa1[1], fa0[0], fa0[1], pa, pa_next);
+            arrive9();
+            multiply(fa1, 2);
+            meet();
+            uint32_t t = pa; pa = pa_next; pa_next = t;
+            t = pb; pb = pb_next; pb_next = t;
+            t = stage; stage = other; other = t;
+        }
+        if (wave < 4) meet();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    }
+    epi(acc, m_base + wm * 64, n_base + wn * 64, g, tm * 4 + wm, split, PieceStaging{lds, wm, wn, m_base, n_base});
+}
+
+template <class Epilogue>
+hipError_t launch_gemm_pieces(GemmArgs g, const Epilogue& epi, hipStream_t stream)
+{
+    g.tiles_m = (g.m + kTileM - 1) / kTileM;
+    g.tiles_n = (g.n + kPiecesN - 1) / kPiecesN;
+    hipLaunchKernelGGL((gemm_pieces<Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(512), 0, stream, g, epi);
+    return hipGetLastError();
+}
+
 template <class T, int BN, int WM, int WN, class Epilogue>
 hipError_t launch_gemm(GemmArgs g, const Epilogue& epi, hipStream_t stream)
 {
     g.tiles_m = (g.m + kTileM - 1) / kTileM;
     g.tiles_n = (g.n + BN - 1) / BN;
-    const dim3 grid(g.tiles_m * g.tiles_n * g.splits);
-    if constexpr (BN == 256)
-        hipLaunchKernelGGL((gemm_large<T, Epilogue>), grid, dim3(512), 0, stream, g, epi);
-    else
-        hipLaunchKernelGGL((gemm<T, BN, WM, WN, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, g, epi);
+    hipLaunchKernelGGL((gemm<T, BN, WM, WN, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(64 * WM * WN), 0,
+                       stream, g, epi);
+    return hipGetLastError();
+}
+
+template <class T, class Epilogue>
+hipError_t launch_gemm_large(GemmArgs g, const Epilogue& epi, hipStream_t stream)
+{
+    g.tiles_m = (g.m + kTileM - 1) / kTileM;
+    g.tiles_n = (g.n + 255) / 256;
+    hipLaunchKernelGGL((gemm_large<T, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(512), 0, stream, g, epi);
     return hipGetLastError();
 }
 

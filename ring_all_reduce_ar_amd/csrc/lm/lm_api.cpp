@@ -369,15 +369,19 @@ ar_result_t check_sizes(uint64_t ntokens, uint64_t rows, uint64_t width, const c
 // ---------------------------------------------------------------------------
 constexpr uint64_t kMaxGrid = uint64_t(1) << 31;
 
-bool plan_fits(uint64_t ntokens, uint64_t vocab, uint64_t width)
+// Depths (the width, and the tokens of a weight gradient) are below 2^24, of
+// fp32 below 2^20: 64 or 256 rows of an operand lie within 2^31 bytes.
+bool plan_fits(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype)
 {
-    return ntokens < kMaxIndex / 8 && vocab < kMaxIndex / 8 && width < (uint64_t(1) << 24) &&
-           ceil_div(ntokens, 256) * ceil_div(vocab, 256) < kMaxGrid / 16;
+    const uint64_t most = uint64_t(1) << (dtype == AR_FLOAT32 ? 20 : 24);
+    return ntokens < most && width < most && vocab < kMaxIndex / 8 &&
+           ceil_div(ntokens, 128) * ceil_div(vocab, 256) < kMaxGrid / 16;
 }
 
+// The operand can be read as it lies.
 bool direct(const void* p, size_t ld, uint64_t width, ar_dtype_t dtype)
 {
-    return dtype != AR_FLOAT32 && width % ar::lm::kTileK == 0 && rows16(p, ld, 2);
+    return dtype != AR_FLOAT32 && width % 8 == 0 && rows16(p, ld, 2) && ld < (size_t(1) << 24);
 }
 
 }  // namespace
@@ -532,7 +536,7 @@ AR_EXPORT ar_result_t ar_embedding_backward(ar_comm_t comm, const void* grad_out
 AR_EXPORT size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, size_t width, ar_dtype_t dtype,
                                                          int backward)
 {
-    if (!valid_dtype(dtype) || dtype == AR_INT32 || width == 0 || !plan_fits(ntokens, vocab, width))
+    if (!valid_dtype(dtype) || dtype == AR_INT32 || width == 0 || !plan_fits(ntokens, vocab, width, dtype))
         return static_cast<size_t>(-1);
     return ar::lm::plan_cross_entropy(ntokens, vocab, width, dtype, backward != 0).bytes;
 }
@@ -550,7 +554,7 @@ ar_result_t cross_entropy_common(ar_comm* comm, const void* hidden, const void* 
     if (rc == AR_SUCCESS) rc = check_sizes(ntokens, vocab, width, "vocab");
     if (rc != AR_SUCCESS) return rc;
     if (vocab == 0) return fail(AR_ERR_INVALID_ARGUMENT, "vocab is 0");
-    if (!plan_fits(ntokens, vocab, width))
+    if (!plan_fits(ntokens, vocab, width, dtype))
         return fail(AR_ERR_INVALID_ARGUMENT, "ntokens %zu, vocab %zu, width %zu: too large for one call", ntokens,
                     vocab, width);
     const size_t e = elem_size(dtype);

@@ -84,14 +84,10 @@ hipError_t launch_lookup_grad(const LookupGradArgs& a, ar_dtype_t dtype, ar_dtyp
                               hipStream_t stream);
 
 // ---- cross entropy --------------------------------------------------------------
-// The matrix core's tile: kTileM rows of the first operand by 256, 64 or 16 of
-// the second, kTileK deep.
+// The matrix core's tile: kTileM rows of the first operand by 256, 128, 64 or
+// 16 of the second, kTileK deep.
 constexpr int kTileM = 256;
 constexpr int kTileK = 64;
-// Parts that a fp32 operand is laid out as, side by side along K: three
-// bf16 pieces a = a1 + a2 + a3 and b = b1 + b2 + b3 as (a1 a1 a2 a1 a2 a3) and
-// (b1 b2 b1 b3 b2 b1), whose products sum to a*b but for terms below 2^-24.
-constexpr int kF32Parts = 6;
 
 struct CrossEntropyArgs {
     const void* hidden;
@@ -111,10 +107,8 @@ struct CrossEntropyArgs {
 // workspace (bytes from its start; unused ones are 0 long).
 struct CrossEntropyPlan {
     uint64_t piece;        // vocabulary rows a piece
-    int parts;             // 1, or kF32Parts
-    uint64_t k_pad;        // depth of the logits' product
-    uint64_t t_pad;        // tokens, up to a multiple of kTileK (of one part)
-    uint64_t piece_pad;    // piece, likewise
+    uint64_t k_pad;        // the width, up to whole steps
+    uint64_t t_pad;        // tokens, up to a multiple of kTileK
     bool pack_hidden, pack_weight;
     int tile_n;            // token tile of the logits' product
     int splits;            // parts of the vocabulary axis in the hidden gradient's product
