@@ -309,23 +309,37 @@ struct DEpilogue {
     {
         const int lane = threadIdx.x & 63;
         float factor[NT];  // of a token's column of dt
-        bool all = m0 + MT * 16 <= g.m;
         const float inv = 1.0f / scale->top;
-        uint32_t at[NT];
-        bool on[NT];
-        float l[NT];
+        const uint32_t mine = m0 + (lane >> 4) * 4;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const uint32_t t = n0 + j * 16 + (lane & 15);
             const int64_t y = t < g.n ? load_target(targets, t, ignore, vocab) : -1;
-            at[j] = target_at<MT>(y, v0 + m0 + (lane >> 4) * 4);
-            on[j] = y >= 0;
-            l[j] = on[j] ? lse[t] : 0.0f;
-            factor[j] = on[j] ? g_losses[t] * inv : 0.0f;
-            all = all && on[j];
+            const uint32_t at = target_at<MT>(y, v0 + mine);
+            const uint32_t keep = y >= 0 ? ~0u : 0u;  // zeros for an ignored token, even from a NaN
+            const float l = y >= 0 ? lse[t] : 0.0f;
+            factor[j] = y >= 0 ? g_losses[t] * inv : 0.0f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][r] - l, kLog2e, kDBits));
+                    acc.v[i][j][r] = as_f(as_u(p) & keep);
+                }
+            __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+            if (__any(at != kNoTarget)) {       // few tiles hold a target
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] -= at == 16 * i + r ? kDScale : 0.0f;
+            }
+            if (m0 + MT * 16 > g.m) {  // zeros below the vocabulary
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] = mine + 16 * i + r < g.m ? acc.v[i][j][r] : 0.0f;
+            }
         }
-        if (__all(all)) differences<true>(acc, at, on, l, m0, g);
-        else differences<false>(acc, at, on, l, m0, g);
         const uint32_t cols = static_cast<uint32_t>(piece_pad), tcols = static_cast<uint32_t>(t_pad);
         if constexpr (std::is_same<S, PieceStaging>::value) {
             auto split = [](float x, uint32_t (&p)[3]) { split3(x, p); };
@@ -340,31 +354,6 @@ struct DEpilogue {
     }
 
 private:
-    // acc = 2^14 (exp(acc - lse) - [v = y]). FULL: every row is one of the
-    // vocabulary and every token counts; else zeros where not.
-    template <bool FULL, int MT, int NT>
-    __device__ __forceinline__ void differences(Tile<MT, NT>& acc, const uint32_t (&at)[NT], const bool (&on)[NT],
-                                                const float (&l)[NT], uint32_t m0, const GemmArgs& g) const
-    {
-        const uint32_t mine = m0 + ((threadIdx.x & 63) >> 4) * 4;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][r] - l[j], kLog2e, kDBits));
-                    acc.v[i][j][r] = FULL || (on[j] && mine + 16 * i + r < g.m) ? p : 0.0f;
-                }
-            __builtin_amdgcn_sched_barrier(0);
-            if (!__any(at[j] != kNoTarget)) continue;  // few tiles hold a target
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc.v[i][j][r] -= at[j] == 16 * i + r ? kDScale : 0.0f;
-        }
-    }
-
     template <int MT, int NT>
     __device__ __forceinline__ void store(const Tile<MT, NT>& acc, const float (&factor)[NT], uint32_t m0, uint32_t n0,
                                           const GemmArgs& g) const
