@@ -80,94 +80,122 @@ hipError_t lookup_launch(const LookupArgs& a, bool vec, hipStream_t s)
 }
 
 // ---------------------------------------------------------------------------
+// zeros for the rows that no token meets
+// ---------------------------------------------------------------------------
+// Rows [r0, r1) without a presence flag, by `blocks` workgroups of THREADS
+// threads, of which this is the `block`-th; `lanes` (a power of two) threads a
+// row, kFillRows neighbouring rows one after the other. Any alignment: 16-byte stores from the row's first boundary on.
+constexpr int kFillRows = 4;
+template <class G, bool NT, int THREADS>
+__device__ __forceinline__ void fill_rows(const LookupGradArgs& a, uint64_t r0, uint64_t r1, uint32_t block,
+                                          uint32_t blocks, uint32_t lanes)
+{
+    constexpr uint32_t EB = 16 / G::kEpv;
+    const uint32_t lane = threadIdx.x & (lanes - 1), per = THREADS / lanes;
+    constexpr int B = kFillRows;  // rows whose flags are loaded together
+    for (uint64_t r = r0 + static_cast<uint64_t>(block) * per * B + threadIdx.x / lanes; r < r1;
+         r += static_cast<uint64_t>(blocks) * per * B) {
+        uint8_t met[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) met[k] = r + k * per < r1 ? a.present[r + k * per] : 1;
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (met[k]) continue;
+            char* row = static_cast<char*>(a.grad_weight) + (r + k * per) * a.ld_grad_weight * EB;
+            const uint64_t bytes = a.width * EB, to_line = -reinterpret_cast<uintptr_t>(row) & 15;
+            const uint64_t head = to_line < bytes ? to_line : bytes, body = (bytes - head) / 16, tail = head + body * 16;
+            for (uint64_t v = lane; v < body; v += lanes) stv_at<NT>(row + head, v * 16, u32x4{0, 0, 0, 0});
+            for (uint64_t b = lane * EB; b < head + (bytes - tail); b += lanes * EB)
+                G::st(row + (b < head ? b : tail + (b - head)), 0, 0.0f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // stable radix sort of the tokens' rows, least significant digit first
 // ---------------------------------------------------------------------------
-// Digits of one workgroup's keys, bin-major: hist[bin * blocks + block]. The
-// first pass reads the tokens and clears the presence bits; the last one sets
-// them.
-__global__ __launch_bounds__(kBlock) void sort_count(const LookupGradArgs a, int src, int shift, int bits, int first,
-                                                     int last)
+// At most kSortBlocks workgroups take `rounds` rounds of kSortThreads keys
+// each. hist[pass][block][digit] counts the keys of a workgroup; those of the
+// first pass come from the tokens, those of a later one are counted (whole
+// numbers, in any order) by the pass before as it moves keys to that
+// workgroup's range. So a pass is one launch: each workgroup sums the counts
+// that lie before its own by itself, 512 columns of at most 128.
+__global__ __launch_bounds__(kSortThreads) void sort_count(const LookupGradArgs a, uint32_t rounds, int bits)
 {
     __shared__ uint32_t bins[kSortBins];
     const int nb = 1 << bits;
-    for (int i = threadIdx.x; i < nb; i += kBlock) bins[i] = 0;
-    if (first) {
-        const uint64_t words = (a.rows + 31) / 32;
-        for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x; i < words;
-             i += static_cast<uint64_t>(gridDim.x) * kBlock)
-            a.present[i] = 0;
-    }
+    for (int i = threadIdx.x; i < nb; i += kSortThreads) bins[i] = 0;
     __syncthreads();
-    const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * kSortBlockKeys;
-    for (int k = threadIdx.x; k < kSortBlockKeys; k += kBlock) {
-        const uint64_t t = lo + k;
+    const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * rounds * kSortThreads;
+    for (uint32_t k = 0; k < rounds; ++k) {
+        const uint64_t t = lo + k * kSortThreads + threadIdx.x;
         if (t >= a.ntokens) break;
-        const uint32_t key =
-            first ? static_cast<uint32_t>(row_of(a.tokens, t, a.first_row, a.rows)) : a.key[src][t];
-        atomicAdd(&bins[(key >> shift) & (nb - 1)], 1u);
-        (void)last;
+        const uint32_t key = static_cast<uint32_t>(row_of(a.tokens, t, a.first_row, a.rows));
+        atomicAdd(&bins[key & (nb - 1)], 1u);
+        if (key < a.rows) a.present[key] = 1;  // by any number of threads
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nb; i += kBlock) a.hist[static_cast<uint64_t>(i) * gridDim.x + blockIdx.x] = bins[i];
+    for (int i = threadIdx.x; i < nb; i += kSortThreads) a.hist[blockIdx.x * kSortBins + i] = bins[i];
 }
 
-// Exclusive sums over `n` counts, by one workgroup.
-__global__ __launch_bounds__(1024) void sort_scan(uint32_t* hist, uint64_t n)
+// Moves a workgroup's keys to their places, in rounds so that equal digits keep
+// their order: a key's place is its digit's next free one, plus the equal
+// digits of earlier waves in the round, plus those of earlier lanes in its
+// wave. Workgroups from `blocks` on write zeros to a part of the rows without
+// tokens: the few that sort leave most of the chip idle.
+template <class G, bool NT>
+__global__ __launch_bounds__(kSortThreads) void sort_move(const LookupGradArgs a, uint32_t blocks, uint32_t rounds,
+                                                          int pass, int shift, int bits, int last, uint64_t r0,
+                                                          uint64_t r1, uint32_t lanes)
 {
-    __shared__ uint32_t waves[16];
-    __shared__ uint32_t carry;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (threadIdx.x == 0) carry = 0;
-    __syncthreads();
-    for (uint64_t lo = 0; lo < n; lo += 1024) {
-        const uint64_t i = lo + threadIdx.x;
-        const uint32_t v = i < n ? hist[i] : 0;
-        uint32_t s = v;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const uint32_t o = __shfl_up(s, d, 64);
-            if (lane >= d) s += o;
-        }
-        if (lane == 63) waves[wave] = s;
-        __syncthreads();
-        uint32_t before = carry, all = 0;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave) before += waves[w];
-            all += waves[w];
-        }
-        if (i < n) hist[i] = before + s - v;
-        __syncthreads();
-        if (threadIdx.x == 0) carry += all;
-        __syncthreads();
-    }
-}
-
-// Moves a workgroup's keys to their places, in rounds of kBlock keys so that
-// equal digits keep their order: a key's place is its bin's next free one,
-// plus the equal digits of earlier waves in the round, plus those of earlier
-// lanes in its wave.
-__global__ __launch_bounds__(kBlock) void sort_move(const LookupGradArgs a, int src, int shift, int bits, int first,
-                                                    int last)
-{
-    constexpr int W = kBlock / 64;
+    constexpr int W = kSortThreads / 64;
     __shared__ uint32_t next[kSortBins];
     __shared__ uint32_t mine[W][kSortBins];
-    const int nb = 1 << bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < nb; i += kBlock) {
-        next[i] = a.hist[static_cast<uint64_t>(i) * gridDim.x + blockIdx.x];
-#pragma unroll
-        for (int w = 0; w < W; ++w) mine[w][i] = 0;
+    __shared__ uint32_t sums[kSortBins / 64];
+    if (blockIdx.x >= blocks) {
+        fill_rows<G, NT, kSortThreads>(a, r0, r1, blockIdx.x - blocks, gridDim.x - blocks, lanes);
+        return;
     }
-    const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * kSortBlockKeys;
-    for (int k = 0; k < kSortBlockKeys && lo + k < a.ntokens; k += kBlock) {
+    const int nb = 1 << bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, src = pass & 1;
+    const uint32_t* hist = a.hist + static_cast<uint64_t>(pass) * kSortBlocks * kSortBins;
+    uint32_t* hist_next = a.hist + static_cast<uint64_t>(pass + 1) * kSortBlocks * kSortBins;
+    {
+        // the keys of smaller digits, and those of this digit in earlier workgroups
+        const int d = threadIdx.x;
+        uint32_t before = 0, all = 0, upto = 0;
+        if (d < kSortBins) {
+            if (d < nb) {
+#pragma unroll 8
+                for (uint32_t b = 0; b < blocks; ++b) {
+                    const uint32_t c = hist[b * kSortBins + d];
+                    all += c;
+                    if (b < blockIdx.x) before += c;
+                }
+            }
+            upto = all;
+#pragma unroll
+            for (int k = 1; k < 64; k *= 2) {
+                const uint32_t o = __shfl_up(upto, k, 64);
+                if (lane >= k) upto += o;
+            }
+            if (lane == 63) sums[wave] = upto;
+        }
+        for (int i = threadIdx.x; i < W * kSortBins; i += kSortThreads) (&mine[0][0])[i] = 0;
         __syncthreads();
-        const uint64_t t = lo + k + threadIdx.x;
+        if (d < kSortBins) {
+            uint32_t base = upto - all + before;
+            for (int w = 0; w < wave; ++w) base += sums[w];
+            next[d] = base;
+        }
+    }
+    const uint64_t lo = static_cast<uint64_t>(blockIdx.x) * rounds * kSortThreads;
+    for (uint32_t k = 0; k < rounds && lo + k * kSortThreads < a.ntokens; ++k) {
+        const uint64_t t = lo + k * kSortThreads + threadIdx.x;
         const bool ok = t < a.ntokens;
         uint32_t key = 0, pos = 0;
         if (ok) {
-            key = first ? static_cast<uint32_t>(row_of(a.tokens, t, a.first_row, a.rows)) : a.key[src][t];
-            pos = first ? static_cast<uint32_t>(t) : a.pos[src][t];
+            key = pass == 0 ? static_cast<uint32_t>(row_of(a.tokens, t, a.first_row, a.rows)) : a.key[src][t];
+            pos = pass == 0 ? static_cast<uint32_t>(t) : a.pos[src][t];
         }
         const uint32_t digit = (key >> shift) & (nb - 1);
         uint64_t same = __ballot(ok);
@@ -183,10 +211,14 @@ __global__ __launch_bounds__(kBlock) void sort_move(const LookupGradArgs a, int 
             for (int w = 0; w < wave; ++w) to += mine[w][digit];
             a.key[src ^ 1][to] = key;
             a.pos[src ^ 1][to] = pos;
-            if (last && key < a.rows) atomicOr(&a.present[key >> 5], 1u << (key & 31));
+            if (!last) {
+                const uint32_t block = to / (rounds * kSortThreads);
+                atomicAdd(&hist_next[block * kSortBins + ((key >> (shift + bits)) & (nb - 1))], 1u);
+            }
         }
+        if (k + 1 == rounds) break;
         __syncthreads();
-        for (int i = threadIdx.x; i < nb; i += kBlock) {
+        for (int i = threadIdx.x; i < nb; i += kSortThreads) {
             uint32_t add = 0;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
@@ -195,6 +227,7 @@ __global__ __launch_bounds__(kBlock) void sort_move(const LookupGradArgs a, int 
             }
             next[i] += add;
         }
+        __syncthreads();
     }
 }
 
@@ -230,127 +263,185 @@ __device__ __forceinline__ void put_row(const LookupGradArgs& a, uint64_t row, u
 }
 
 template <class F, int U>
-__device__ __forceinline__ void add_row(const LookupGradArgs& a, uint64_t t, uint64_t c, float* acc)
+__device__ __forceinline__ void get_row(const LookupGradArgs& a, uint64_t t, uint64_t c, float* x)
 {
     const uint64_t at = t * a.ld_grad_out + c;
     if constexpr (U == 1) {
-        acc[0] += F::ld(a.grad_out, at);
+        x[0] = F::ld(a.grad_out, at);
     } else {
         constexpr int E = F::kEpv;
 #pragma unroll
-        for (int k = 0; k < U; k += E) {
-            float y[E];
-            F::unpack(ldv_at<false>(a.grad_out, (at + k) * (16 / E)), y);
-#pragma unroll
-            for (int j = 0; j < E; ++j) acc[k + j] += y[j];
-        }
+        for (int k = 0; k < U; k += E) F::unpack(ldv_at<false>(a.grad_out, (at + k) * (16 / E)), x + k);
     }
 }
 
-// Workgroups below `chunks` sum kGradChunk positions of the sorted order each:
-// a run inside the chunk is written to its row, a run that began before it or
-// goes on after it leaves a partial sum (slot 0: from the chunk's start; slot
-// 1: to its end). The others write zeros to the rows without tokens.
+// `lanes` threads (a power of two, at least kGradLanes) sum kGradChunk
+// positions of the sorted order each over U columns: a run inside the chunk is
+// written to its row, a run that began before it or goes on after it leaves a
+// partial sum (slot 0: from the chunk's start; slot 1: to its end). Four rows
+// are loaded together and added in order.
 template <class F, class G, int U>
-__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted)
+__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
 {
-    const uint32_t* key = a.key[sorted];
-    const uint32_t* pos = a.pos[sorted];
-    const uint32_t rows = static_cast<uint32_t>(a.rows);
-    if (blockIdx.x < chunks) {
-        const uint64_t p0 = static_cast<uint64_t>(blockIdx.x) * kGradChunk;
-        const uint64_t p1 = min(p0 + kGradChunk, a.ntokens);
-        const uint32_t before = p0 > 0 ? key[p0 - 1] : UINT32_MAX;
-        const uint32_t after = p1 < a.ntokens ? key[p1] : UINT32_MAX;
-        for (uint64_t c = static_cast<uint64_t>(threadIdx.x) * U; c < a.width; c += kBlock * U) {
-            float acc[U] = {};
-            uint32_t cur = key[p0];
-            bool from_start = true;  // the run began at the chunk's first position
-            for (uint64_t p = p0; p < p1; ++p) {
-                if (cur >= rows) break;  // tokens of no row come last
-                add_row<F, U>(a, pos[p], c, acc);
-                const uint32_t nxt = p + 1 < p1 ? key[p + 1] : after;
-                const bool ends = p + 1 == p1;
-                if (nxt != cur || ends) {
-                    const bool open_front = from_start && before == cur;
-                    const bool open_back = ends && after == cur;
-                    if (!open_front && !open_back) {
-                        put_row<G, U>(a, cur, c, acc);
-                    } else {
-                        float* to = a.partial + (2ull * blockIdx.x + (open_front ? 0 : 1)) * a.width + c;
+    constexpr int K = kGradChunk, B = 4;
+    __shared__ uint32_t keys[kBlock / kGradLanes][K + 2];  // the one before the chunk, its own, the one after
+    __shared__ uint32_t places[kBlock / kGradLanes][K];
+    const uint32_t rows = static_cast<uint32_t>(a.rows), per = kBlock / lanes;
+    const uint64_t first = static_cast<uint64_t>(blockIdx.x) * per * K;  // the workgroup's first position
+    for (uint32_t i = threadIdx.x; i < per * (K + 2); i += kBlock) {
+        const uint32_t g = i / (K + 2), k = i % (K + 2);
+        const uint64_t p = first + static_cast<uint64_t>(g) * K + k;  // one past the place
+        const bool in = p >= 1 && p <= a.ntokens;
+        keys[g][k] = in ? a.key[sorted][p - 1] : UINT32_MAX;
+        if (k >= 1 && k <= K) places[g][k - 1] = in ? a.pos[sorted][p - 1] : 0;
+    }
+    __syncthreads();
+    const uint32_t group = threadIdx.x / lanes, chunk = blockIdx.x * per + group;
+    const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * U;
+    if (chunk >= chunks || c >= a.width) return;
+    const uint32_t* key = &keys[group][1];
+    const uint32_t* pos = places[group];
+    float acc[U] = {};
+    bool from_start = true;  // the run began at the chunk's first position
+    for (int p = 0; p < K && key[p] < rows; p += B) {  // tokens of no row come last
+        float x[B][U] = {};
 #pragma unroll
-                        for (int j = 0; j < U; ++j) to[j] = acc[j];
-                    }
+        for (int k = 0; k < B; ++k)
+            if (key[p + k] < rows) get_row<F, U>(a, pos[p + k], c, x[k]);
 #pragma unroll
-                    for (int j = 0; j < U; ++j) acc[j] = 0.0f;
-                    from_start = false;
-                    cur = nxt;
-                }
+        for (int k = 0; k < B; ++k) {
+            const uint32_t cur = key[p + k], nxt = key[p + k + 1];
+            if (cur >= rows) break;
+#pragma unroll
+            for (int j = 0; j < U; ++j) acc[j] += x[k][j];
+            if (nxt == cur && p + k + 1 < K) continue;
+            const bool open_front = from_start && key[-1] == cur, open_back = nxt == cur;
+            if (!open_front && !open_back) {
+                put_row<G, U>(a, cur, c, acc);
+            } else {
+                float* to = a.partial + (2ull * chunk + (open_front ? 0 : 1)) * a.width + c;
+#pragma unroll
+                for (int j = 0; j < U; ++j) to[j] = acc[j];
             }
+#pragma unroll
+            for (int j = 0; j < U; ++j) acc[j] = 0.0f;
+            from_start = false;
         }
-        return;
-    }
-    const float zero[U] = {};
-    for (uint64_t r = blockIdx.x - chunks; r < a.rows; r += gridDim.x - chunks) {
-        if ((a.present[r >> 5] >> (r & 31)) & 1) continue;
-        for (uint64_t c = static_cast<uint64_t>(threadIdx.x) * U; c < a.width; c += kBlock * U)
-            put_row<G, U>(a, r, c, zero);
     }
 }
 
-// Joins the partial sums of a run that goes over chunk borders, in order: one
-// workgroup for each chunk in which such a run begins.
+// Joins the partial sums of a run that goes over chunk borders, in order:
+// `lanes` threads for each chunk in which such a run begins, sixteen loads
+// together (the most frequent token of a text has a tenth of all positions).
 template <class G, int U>
-__global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t chunks, int sorted)
+__global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
 {
+    constexpr int B = 16;
     const uint32_t* key = a.key[sorted];
-    const uint64_t p0 = static_cast<uint64_t>(blockIdx.x) * kGradChunk, p1 = p0 + kGradChunk;
-    if (p1 >= a.ntokens) return;
+    const uint32_t chunk = blockIdx.x * (kBlock / lanes) + threadIdx.x / lanes;
+    const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * U;
+    const uint64_t p0 = static_cast<uint64_t>(chunk) * kGradChunk, p1 = p0 + kGradChunk;
+    if (p1 >= a.ntokens || c >= a.width) return;
     const uint32_t row = key[p1 - 1];
-    if (row >= a.rows || key[p1] != row) return;            // no run goes on
+    if (row >= a.rows || key[p1] != row) return;                 // no run goes on
     if (key[p0] == row && p0 > 0 && key[p0 - 1] == row) return;  // it began in an earlier chunk
-    for (uint64_t c = static_cast<uint64_t>(threadIdx.x) * U; c < a.width; c += kBlock * U) {
-        float acc[U];
-        const float* from = a.partial + (2ull * blockIdx.x + 1) * a.width + c;
+    float acc[U];
+    const float* from = a.partial + (2ull * chunk + 1) * a.width + c;
 #pragma unroll
-        for (int j = 0; j < U; ++j) acc[j] = from[j];
-        for (uint32_t b = blockIdx.x + 1; b < chunks; ++b) {
-            const uint64_t q0 = static_cast<uint64_t>(b) * kGradChunk;
-            if (key[q0] != row) break;
-            from = a.partial + 2ull * b * a.width + c;
+    for (int j = 0; j < U; ++j) acc[j] = from[j];
+    auto goes_on = [&](uint64_t b) { return b < chunks && key[b * kGradChunk] == row; };
+    uint64_t b = chunk + 1;
+    while (goes_on(b + B - 1)) {  // and so do the chunks before it
+        float x[B][U];
 #pragma unroll
-            for (int j = 0; j < U; ++j) acc[j] += from[j];
+        for (int k = 0; k < B; ++k) {
+            from = a.partial + 2ull * (b + k) * a.width + c;
+#pragma unroll
+            for (int j = 0; j < U; ++j) x[k][j] = from[j];
         }
-        put_row<G, U>(a, row, c, acc);
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+#pragma unroll
+            for (int j = 0; j < U; ++j) acc[j] += x[k][j];
+        b += B;
     }
+    for (; goes_on(b); ++b) {
+        from = a.partial + 2ull * b * a.width + c;
+#pragma unroll
+        for (int j = 0; j < U; ++j) acc[j] += from[j];
+    }
+    put_row<G, U>(a, row, c, acc);
+}
+
+// The presence flags and the counts that the sort adds to.
+__global__ __launch_bounds__(kBlock) void clear_words(uint32_t* words, uint64_t n)
+{
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x; i < n;
+         i += static_cast<uint64_t>(gridDim.x) * kBlock)
+        words[i] = 0;
+}
+
+template <class G, bool NT>
+__global__ __launch_bounds__(kSortThreads) void fill_all(const LookupGradArgs a, uint32_t lanes)
+{
+    fill_rows<G, NT, kSortThreads>(a, 0, a.rows, blockIdx.x, gridDim.x, lanes);
+}
+
+uint32_t lanes_for(uint64_t units, uint32_t least, uint32_t most)
+{
+    uint32_t lanes = least;
+    while (lanes < most && lanes < units) lanes *= 2;
+    return lanes;
+}
+
+template <class G, bool NT>
+hipError_t sort_and_fill(const LookupGradArgs& a, int* sorted, int num_cus, hipStream_t s)
+{
+    const uint32_t lanes = lanes_for((a.width * (16 / G::kEpv) + 15) / 16, 1, 256);
+    const uint64_t each = kSortThreads / lanes * kFillRows, wanted = (a.rows + each - 1) / each, cap = static_cast<uint64_t>(num_cus) * 8;
+    const uint32_t fillers = static_cast<uint32_t>(wanted < cap ? wanted : cap);
+    const uint64_t words = a.clear_words;
+    const uint64_t clearers = (words + kBlock - 1) / kBlock;
+    hipLaunchKernelGGL(clear_words, dim3(static_cast<uint32_t>(clearers < 1024 ? clearers : 1024)), dim3(kBlock), 0, s,
+                       reinterpret_cast<uint32_t*>(a.present), words);
+    if (a.ntokens == 0) {
+        hipLaunchKernelGGL((fill_all<G, NT>), dim3(fillers), dim3(kSortThreads), 0, s, a, lanes);
+        return hipGetLastError();
+    }
+    const uint64_t all = (a.ntokens + kSortThreads - 1) / kSortThreads;
+    const uint32_t rounds = static_cast<uint32_t>((all + kSortBlocks - 1) / kSortBlocks);
+    const uint32_t blocks = static_cast<uint32_t>((all + rounds - 1) / rounds);
+    const int passes = sort_passes(a.rows), bits = (sort_bits(a.rows) + passes - 1) / passes;
+    hipLaunchKernelGGL(sort_count, dim3(blocks), dim3(kSortThreads), 0, s, a, rounds, bits);
+    for (int p = 0; p < passes; ++p) {
+        const uint64_t r0 = a.rows * p / passes, r1 = a.rows * (p + 1) / passes;
+        hipLaunchKernelGGL((sort_move<G, NT>), dim3(blocks + (a.accumulate ? 0 : fillers)), dim3(kSortThreads), 0, s, a,
+                           blocks, rounds, p, p * bits, bits, p == passes - 1, r0, r1, lanes);
+    }
+    *sorted = passes & 1;
+    return hipGetLastError();
 }
 
 template <class F, class G, int U>
-hipError_t grad_launch(const LookupGradArgs& a, uint32_t chunks, int sorted, int num_cus, hipStream_t s)
+hipError_t grad_launch(const LookupGradArgs& a, uint32_t chunks, int sorted, hipStream_t s)
 {
-    const uint64_t rows_wanted = a.accumulate ? 0 : a.rows;
-    const uint64_t cap = static_cast<uint64_t>(num_cus) * 32;
-    const uint32_t zero = static_cast<uint32_t>(rows_wanted < cap ? rows_wanted : cap);
-    if (chunks + zero) hipLaunchKernelGGL((grad_sum<F, G, U>), dim3(chunks + zero), dim3(kBlock), 0, s, a, chunks, sorted);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || chunks < 2) return e;
-    hipLaunchKernelGGL((grad_join<G, U>), dim3(chunks), dim3(kBlock), 0, s, a, chunks, sorted);
+    const uint64_t units = (a.width + U - 1) / U;
+    const uint32_t lanes = lanes_for(units, kGradLanes, kBlock), per = kBlock / lanes;
+    const dim3 grid((chunks + per - 1) / per, static_cast<uint32_t>((units + lanes - 1) / lanes));
+    hipLaunchKernelGGL((grad_sum<F, G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+    if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
     return hipGetLastError();
 }
 
 template <class F, class G>
-hipError_t grad_vec(const LookupGradArgs& a, bool vec, uint32_t chunks, int sorted, int num_cus, hipStream_t s)
+hipError_t grad_call(const LookupGradArgs& a, bool vec, bool nt, int num_cus, hipStream_t s)
 {
     constexpr int U = F::kEpv > G::kEpv ? F::kEpv : G::kEpv;
-    return vec ? grad_launch<F, G, U>(a, chunks, sorted, num_cus, s) : grad_launch<F, G, 1>(a, chunks, sorted, num_cus, s);
-}
-
-// No token: the presence bits alone.
-__global__ __launch_bounds__(kBlock) void clear_present(uint32_t* present, uint64_t words)
-{
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kBlock + threadIdx.x; i < words;
-         i += static_cast<uint64_t>(gridDim.x) * kBlock)
-        present[i] = 0;
+    int sorted = 0;
+    const hipError_t e = nt ? sort_and_fill<G, true>(a, &sorted, num_cus, s) : sort_and_fill<G, false>(a, &sorted, num_cus, s);
+    if (e != hipSuccess || a.ntokens == 0) return e;
+    const uint32_t chunks = static_cast<uint32_t>((a.ntokens + kGradChunk - 1) / kGradChunk);
+    return vec ? grad_launch<F, G, U>(a, chunks, sorted, s) : grad_launch<F, G, 1>(a, chunks, sorted, s);
 }
 
 }  // namespace
@@ -366,35 +457,15 @@ hipError_t launch_lookup(const LookupArgs& a, ar_dtype_t dtype, bool vec, int nu
     }
 }
 
-hipError_t launch_lookup_grad(const LookupGradArgs& a, ar_dtype_t dtype, ar_dtype_t grad_dtype, bool vec, int num_cus,
-                              hipStream_t stream)
+hipError_t launch_lookup_grad(const LookupGradArgs& a, ar_dtype_t dtype, ar_dtype_t grad_dtype, bool vec, bool nt,
+                              int num_cus, hipStream_t stream)
 {
-    int sorted = 0;
-    const uint32_t chunks = static_cast<uint32_t>((a.ntokens + kGradChunk - 1) / kGradChunk);
-    if (a.ntokens) {
-        const uint32_t blocks = static_cast<uint32_t>((a.ntokens + kSortBlockKeys - 1) / kSortBlockKeys);
-        int bits = 1;
-        while ((a.rows >> bits) != 0) ++bits;  // keys are 0..rows
-        const int passes = (bits + 8) / 9, digit = (bits + passes - 1) / passes;
-        for (int p = 0; p < passes; ++p) {
-            const int first = p == 0, last = p == passes - 1, shift = p * digit, src = sorted;
-            hipLaunchKernelGGL(sort_count, dim3(blocks), dim3(kBlock), 0, stream, a, src, shift, digit, first, last);
-            hipLaunchKernelGGL(sort_scan, dim3(1), dim3(1024), 0, stream, a.hist,
-                               static_cast<uint64_t>(blocks) << digit);
-            hipLaunchKernelGGL(sort_move, dim3(blocks), dim3(kBlock), 0, stream, a, src, shift, digit, first, last);
-            const hipError_t e = hipGetLastError();
-            if (e != hipSuccess) return e;
-            sorted ^= 1;
-        }
-    } else {
-        hipLaunchKernelGGL(clear_present, dim3(64), dim3(kBlock), 0, stream, a.present, (a.rows + 31) / 32);
-    }
-    if (dtype == AR_FLOAT32) return grad_vec<F32, F32>(a, vec, chunks, sorted, num_cus, stream);
+    if (dtype == AR_FLOAT32) return grad_call<F32, F32>(a, vec, nt, num_cus, stream);
     if (dtype == AR_FLOAT16)
-        return grad_dtype == AR_FLOAT32 ? grad_vec<F16, F32>(a, vec, chunks, sorted, num_cus, stream)
-                                        : grad_vec<F16, F16>(a, vec, chunks, sorted, num_cus, stream);
-    return grad_dtype == AR_FLOAT32 ? grad_vec<BF16, F32>(a, vec, chunks, sorted, num_cus, stream)
-                                    : grad_vec<BF16, BF16>(a, vec, chunks, sorted, num_cus, stream);
+        return grad_dtype == AR_FLOAT32 ? grad_call<F16, F32>(a, vec, nt, num_cus, stream)
+                                        : grad_call<F16, F16>(a, vec, nt, num_cus, stream);
+    return grad_dtype == AR_FLOAT32 ? grad_call<BF16, F32>(a, vec, nt, num_cus, stream)
+                                    : grad_call<BF16, BF16>(a, vec, nt, num_cus, stream);
 }
 
 }  // namespace lm

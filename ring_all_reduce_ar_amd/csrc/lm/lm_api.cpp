@@ -349,8 +349,8 @@ bool grad_layout(uint64_t ntokens, uint64_t rows, uint64_t width, GradLayout* l)
     };
     for (int k = 0; k < 2; ++k) l->key[k] = take(ntokens, 4);
     for (int k = 0; k < 2; ++k) l->pos[k] = take(ntokens, 4);
-    l->hist = take(ceil_div(ntokens, ar::lm::kSortBlockKeys), ar::lm::kSortBins * 4);
-    l->present = take(ceil_div(rows, 32), 4);
+    l->present = take(rows, 1);
+    l->hist = take(ar::lm::sort_passes(rows), ntokens ? ar::lm::kSortBlocks * ar::lm::kSortBins * 4 : 0);
     l->partial = take(ceil_div(ntokens, ar::lm::kGradChunk) * 2, width * 4);
     l->bytes = std::max<size_t>(at, 16);
     return ok;
@@ -522,13 +522,16 @@ AR_EXPORT ar_result_t ar_embedding_backward(ar_comm_t comm, const void* grad_out
             a.key[k] = reinterpret_cast<uint32_t*>(ws + l.key[k]);
             a.pos[k] = reinterpret_cast<uint32_t*>(ws + l.pos[k]);
         }
+        a.present = reinterpret_cast<uint8_t*>(ws + l.present);
         a.hist = reinterpret_cast<uint32_t*>(ws + l.hist);
-        a.present = reinterpret_cast<uint32_t*>(ws + l.present);
+        a.clear_words = (l.partial - l.present) / 4;
         a.partial = reinterpret_cast<float*>(ws + l.partial);
         const size_t unit = 16 / std::min(e, ge);  // elements a thread takes together
         const bool vec = width % unit == 0 && rows16(grad_weight, ld_grad_weight, ge) &&
                          (ntokens == 0 || rows16(grad_out, ld_grad_out, e));
-        const hipError_t err = ar::lm::launch_lookup_grad(a, dtype, grad_dtype, vec, comm->num_cus, stream);
+        const uint64_t touched = ntokens * width * e + (accumulate ? 0 : rows * width * ge);
+        const bool nt = call_nt(comm, touched, kLastLevelCacheBytes);
+        const hipError_t err = ar::lm::launch_lookup_grad(a, dtype, grad_dtype, vec, nt, comm->num_cus, stream);
         return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
     });
 }

@@ -59,11 +59,23 @@ struct LookupArgs {
 };
 hipError_t launch_lookup(const LookupArgs& a, ar_dtype_t dtype, bool vec, int num_cus, hipStream_t stream);
 
-// Keys of one radix pass for a workgroup, and positions of the sorted order
-// for a workgroup of the sum.
-constexpr int kSortBlockKeys = 2048;
+// The sort: at most kSortBlocks workgroups of kSortThreads threads, digits of
+// at most 9 bits. The sum: kGradChunk positions of the sorted order for at
+// least kGradLanes threads.
+constexpr int kSortThreads = 1024;
+constexpr int kSortBlocks = 128;
 constexpr int kSortBins = 512;
 constexpr int kGradChunk = 32;
+constexpr int kGradLanes = 4;
+
+// Bits of a key (keys are 0..rows), and the passes over 9 of them at a time.
+inline int sort_bits(uint64_t rows)
+{
+    int bits = 1;
+    while ((rows >> bits) != 0) ++bits;
+    return bits;
+}
+inline int sort_passes(uint64_t rows) { return (sort_bits(rows) + 8) / 9; }
 
 struct LookupGradArgs {
     const void* grad_out;
@@ -76,12 +88,14 @@ struct LookupGradArgs {
     // workspace
     uint32_t* key[2];
     uint32_t* pos[2];
-    uint32_t* hist;     // kSortBins * sort blocks
-    uint32_t* present;  // one bit for each row
-    float* partial;     // 2 * width floats for each chunk
+    uint8_t* present;      // a flag for each row, and right behind them
+    uint32_t* hist;        // [sort_passes][kSortBlocks][kSortBins]
+    uint64_t clear_words;  // of both
+    float* partial;        // 2 * width floats for each chunk
 };
-hipError_t launch_lookup_grad(const LookupGradArgs& a, ar_dtype_t dtype, ar_dtype_t grad_dtype, bool vec, int num_cus,
-                              hipStream_t stream);
+// `vec`: rows of both matrices in 16-byte vectors; `nt`: non-temporal zeros.
+hipError_t launch_lookup_grad(const LookupGradArgs& a, ar_dtype_t dtype, ar_dtype_t grad_dtype, bool vec, bool nt,
+                              int num_cus, hipStream_t stream);
 
 // ---- cross entropy --------------------------------------------------------------
 // The matrix core's tile: kTileM rows of the first operand by 256, 128, 64 or
