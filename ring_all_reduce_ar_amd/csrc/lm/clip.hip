@@ -4,8 +4,9 @@
 //
 // Squares and their sums are doubles: they neither overflow nor lose small
 // gradients beside large ones, and fp64 adds at the rate of HBM cost nothing
-// here. Each workgroup leaves one partial; one workgroup joins them in a fixed
-// order, so the same call gives the same bits.
+// here. Each workgroup leaves one partial, and they are joined in a fixed order,
+// so the same call gives the same bits: by every workgroup of the scaling pass
+// for itself where there are few (kClipJoinEach), else by a launch of one.
 #include "../kernels_impl.h"
 #include "lm_kernels.h"
 
@@ -56,11 +57,30 @@ __device__ __forceinline__ void take(const float* x, int inf, double& sum, float
     }
 }
 
+// All partials, by every thread of a workgroup.
+template <int THREADS>
+__device__ __forceinline__ double join_partials(const ClipWorkspace* ws, int slots, int inf)
+{
+    double v = 0.0;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < slots; i += THREADS) v = join_norm(v, ws->partial[i], inf);
+    return block_join<THREADS>(v, inf);
+}
+
+__device__ __forceinline__ double norm_of(double joined, int inf) { return inf ? joined : __builtin_sqrt(joined); }
+
+__device__ __forceinline__ float scale_of(double total, double max_norm)
+{
+    const double s = max_norm / (total + kClipEps);
+    return static_cast<float>(s > 1.0 ? 1.0 : s);  // a NaN stays one
+}
+
 // One pass over a batch of tensors (see ClipKind). A tile is M kBlock-vector
 // quarters of a piece, or kBlock elements where the pointers of a tensor
 // differ in their offset from a 16-byte boundary.
 template <class F, int KIND, int OP, bool NT, int M>
-__global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst, int inf, int first, ClipWorkspace* ws)
+__global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst, int inf, int first, int slots,
+                                                    double max_norm, ClipWorkspace* ws, float* norm_out)
 {
     constexpr int E = F::kEpv;
     const MultiHeader& h = a.h;
@@ -69,7 +89,20 @@ __global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst,
     cpiece* pieces = (cpiece*)(ctable + h.pieces_offset);
     double sum = 0.0;
     float top = 0.0f;
-    const float scale = KIND == kClipApply ? ws->scale : 1.0f;
+    float scale = 1.0f;
+    bool scaled = KIND != kClipApply;
+    // Called by the whole workgroup, after its first loads were issued.
+    auto need_scale = [&] {
+        if (scaled) return;
+        scaled = true;
+        if (slots) {
+            const double total = norm_of(join_partials<kBlock>(ws, slots, inf), inf);
+            scale = scale_of(total, max_norm);
+            if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(total);
+        } else {
+            scale = ws->scale;
+        }
+    };
     for (uint32_t tile = blockIdx.x; tile < h.ntiles; tile += gridDim.x) {
         const MultiPiece pc = load_piece(pieces + multi_find_piece(pieces, h.npieces, tile));
         cuptr* block = (cuptr*)(ctable) + pc.ptrs;
@@ -122,6 +155,7 @@ __global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst,
                 } else {
                     u32x4 x[M];
                     load_stage<M, NT>(x, src[0], off);
+                    need_scale();
 #pragma unroll
                     for (int m = 0; m < M; ++m) F::unpack(x[m], acc[m]);
                 }
@@ -143,6 +177,7 @@ __global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst,
                         if (ok[m]) take<E>(acc[m], inf, sum, top);
                 }
             }
+            need_scale();
             if (ti == 0) {
                 // elements before the first whole vector and after the last
                 const uint64_t vstart = a0 + vb * E, vend = a0 + ve * E;
@@ -155,6 +190,7 @@ __global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst,
                     element(k < nhead ? pc.j0 + k : tail_start + (k - nhead));
             }
         } else {
+            need_scale();
             const uint64_t i = pc.j0 + static_cast<uint64_t>(ti) * kBlock + threadIdx.x;
             if (i < j_end) element(i);
         }
@@ -171,69 +207,84 @@ __global__ __launch_bounds__(kBlock) void clip_pass(const MultiArgs a, int ndst,
 __global__ __launch_bounds__(kJoinBlock) void clip_join(int slots, int inf, double max_norm, ClipWorkspace* ws,
                                                         float* norm_out)
 {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < slots; i += kJoinBlock) v = join_norm(v, ws->partial[i], inf);
-    v = block_join<kJoinBlock>(v, inf);
+    const double total = norm_of(join_partials<kJoinBlock>(ws, slots, inf), inf);
     if (threadIdx.x == 0) {
-        const double total = inf ? v : __builtin_sqrt(v);
-        const double s = max_norm / (total + kClipEps);
-        ws->total = total;
-        ws->scale = static_cast<float>(s > 1.0 ? 1.0 : s);  // a NaN stays one
+        ws->scale = scale_of(total, max_norm);
         if (norm_out) *norm_out = static_cast<float>(total);
     }
 }
 
+struct PassArgs {
+    int ndst, inf, first, slots;
+    double max_norm;
+    ClipWorkspace* ws;
+    float* norm_out;
+};
+
+template <class F, int KIND, int OP, bool NT, int M>
+hipError_t pass_tiles(const MultiArgs& a, const PassArgs& p, int grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((clip_pass<F, KIND, OP, NT, M>), dim3(grid), dim3(kBlock), 0, s, a, p.ndst, p.inf, p.first,
+                       p.slots, p.max_norm, p.ws, p.norm_out);
+    return hipGetLastError();
+}
+
 template <class F, int KIND, int OP, bool NT>
-hipError_t pass_m(const MultiArgs& a, int ndst, int inf, int first, int grid, ClipWorkspace* ws, hipStream_t s)
+hipError_t pass_m(const MultiArgs& a, const PassArgs& p, int grid, hipStream_t s)
 {
     constexpr int EB = 16 / F::kEpv;
     if constexpr (KIND == kClipReduce) {
         constexpr int MA = clip_tiles(kClipReduce, kRankMajorAnyMany, EB), MF = clip_tiles(kClipReduce, 1, EB);
-        if (a.h.n >= kRankMajorAnyMany)
-            hipLaunchKernelGGL((clip_pass<F, KIND, OP, NT, MA>), dim3(grid), dim3(kBlock), 0, s, a, ndst, inf, first, ws);
-        else
-            hipLaunchKernelGGL((clip_pass<F, KIND, OP, NT, MF>), dim3(grid), dim3(kBlock), 0, s, a, ndst, inf, first, ws);
+        return a.h.n >= kRankMajorAnyMany ? pass_tiles<F, KIND, OP, NT, MA>(a, p, grid, s)
+                                          : pass_tiles<F, KIND, OP, NT, MF>(a, p, grid, s);
     } else {
-        constexpr int M = clip_tiles(static_cast<ClipKind>(KIND), 1, EB);
-        hipLaunchKernelGGL((clip_pass<F, KIND, OP, NT, M>), dim3(grid), dim3(kBlock), 0, s, a, ndst, inf, first, ws);
+        return pass_tiles<F, KIND, OP, NT, clip_tiles(static_cast<ClipKind>(KIND), 1, EB)>(a, p, grid, s);
     }
-    return hipGetLastError();
 }
 
 template <class F, bool NT>
-hipError_t pass_kind(ClipKind kind, const MultiArgs& a, int ndst, ar_op_t op, int inf, int first, int grid,
-                     ClipWorkspace* ws, hipStream_t s)
+hipError_t pass_kind(ClipKind kind, const MultiArgs& a, ar_op_t op, const PassArgs& p, int grid, hipStream_t s)
 {
     switch (kind) {
-    case kClipMeasure: return pass_m<F, kClipMeasure, AR_SUM, NT>(a, ndst, inf, first, grid, ws, s);
-    case kClipApply: return pass_m<F, kClipApply, AR_SUM, NT>(a, ndst, inf, first, grid, ws, s);
+    case kClipMeasure: return pass_m<F, kClipMeasure, AR_SUM, NT>(a, p, grid, s);
+    case kClipApply: return pass_m<F, kClipApply, AR_SUM, NT>(a, p, grid, s);
     case kClipReduce:
-        if (op == AR_SUM) return pass_m<F, kClipReduce, AR_SUM, NT>(a, ndst, inf, first, grid, ws, s);
-        if (op == AR_AVG) return pass_m<F, kClipReduce, AR_AVG, NT>(a, ndst, inf, first, grid, ws, s);
+        if (op == AR_SUM) return pass_m<F, kClipReduce, AR_SUM, NT>(a, p, grid, s);
+        if (op == AR_AVG) return pass_m<F, kClipReduce, AR_AVG, NT>(a, p, grid, s);
     }
     return hipErrorInvalidValue;
 }
 
 template <class F>
-hipError_t pass_nt(ClipKind kind, const MultiArgs& a, int ndst, ar_op_t op, int inf, bool nt, int first, int grid,
-                   ClipWorkspace* ws, hipStream_t s)
+hipError_t pass_nt(ClipKind kind, const MultiArgs& a, ar_op_t op, bool nt, const PassArgs& p, int grid, hipStream_t s)
 {
-    return nt ? pass_kind<F, true>(kind, a, ndst, op, inf, first, grid, ws, s)
-              : pass_kind<F, false>(kind, a, ndst, op, inf, first, grid, ws, s);
+    return nt ? pass_kind<F, true>(kind, a, op, p, grid, s) : pass_kind<F, false>(kind, a, op, p, grid, s);
+}
+
+hipError_t pass(ClipKind kind, const MultiArgs& a, ar_dtype_t dtype, ar_op_t op, bool nt, const PassArgs& p, int grid,
+                hipStream_t s)
+{
+    switch (dtype) {
+    case AR_FLOAT32: return pass_nt<F32>(kind, a, op, nt, p, grid, s);
+    case AR_FLOAT16: return pass_nt<F16>(kind, a, op, nt, p, grid, s);
+    case AR_BFLOAT16: return pass_nt<BF16>(kind, a, op, nt, p, grid, s);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
-hipError_t launch_clip_pass(ClipKind kind, const MultiArgs& a, int ndst, ar_dtype_t dtype, ar_op_t op, ar_norm_t norm,
-                            bool nt, bool first, int grid, ClipWorkspace* ws, hipStream_t stream)
+hipError_t launch_clip_norm(ClipKind kind, const MultiArgs& a, ar_dtype_t dtype, ar_op_t op, ar_norm_t norm, bool nt,
+                            bool first, int grid, ClipWorkspace* ws, hipStream_t stream)
 {
-    const int inf = norm == AR_NORM_INF, f = first;
-    switch (dtype) {
-    case AR_FLOAT32: return pass_nt<F32>(kind, a, ndst, op, inf, nt, f, grid, ws, stream);
-    case AR_FLOAT16: return pass_nt<F16>(kind, a, ndst, op, inf, nt, f, grid, ws, stream);
-    case AR_BFLOAT16: return pass_nt<BF16>(kind, a, ndst, op, inf, nt, f, grid, ws, stream);
-    default: return hipErrorInvalidValue;
-    }
+    return pass(kind, a, dtype, op, nt, PassArgs{1, norm == AR_NORM_INF, first, 0, 0.0, ws, nullptr}, grid, stream);
+}
+
+hipError_t launch_clip_apply(const MultiArgs& a, int ndst, ar_dtype_t dtype, ar_norm_t norm, bool nt, int slots,
+                             double max_norm, int grid, ClipWorkspace* ws, float* norm_out, hipStream_t stream)
+{
+    return pass(kClipApply, a, dtype, AR_SUM, nt, PassArgs{ndst, norm == AR_NORM_INF, 0, slots, max_norm, ws, norm_out},
+                grid, stream);
 }
 
 hipError_t launch_clip_join(int slots, ar_norm_t norm, double max_norm, ClipWorkspace* ws, float* norm_out,

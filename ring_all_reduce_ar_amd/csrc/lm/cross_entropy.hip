@@ -543,8 +543,8 @@ hipError_t product(const GemmArgs& g, int tile_n, const Epilogue& epi, hipStream
     if constexpr (PARTS == kPieces) {
         return launch_gemm_pieces(g, epi, s);
     } else {
-        if (tile_n == 16) return launch_gemm<T, 16, 8, 1>(g, epi, s);
-        if (tile_n == 64) return launch_gemm<T, 64, 4, 2>(g, epi, s);
+        if (tile_n == 16) return launch_gemm_few<T, 16>(g, epi, s);
+        if (tile_n == 64) return launch_gemm_few<T, 64>(g, epi, s);
         return launch_gemm_large<T>(g, epi, s);
     }
 }

@@ -5,8 +5,8 @@
 // for 16-bit A and B whose rows are contiguous along K and 16-byte aligned; C
 // stays in fp32 registers and goes to an epilogue. Tiles of both go from
 // memory straight into LDS. Three kernels: gemm_large for 256 x 256 tiles,
-// gemm_pieces for fp32 operands in three bf16 pieces, and gemm for few rows
-// of B, which is bound by reading A.
+// gemm_pieces for fp32 operands in three bf16 pieces, and gemm_few for few
+// rows of B, which is bound by reading A.
 //
 // LDS holds 128-byte rows as eight 16-byte columns; column c of row r lies at
 // c ^ (r & 7), so that the 16 rows of a fragment read spread over all banks.
@@ -188,75 +188,6 @@ private:
     }
 };
 
-template <class T, int BN, int WM, int WN, class Epilogue>
-__global__ __launch_bounds__(64 * WM * WN) void gemm(const GemmArgs g, const Epilogue epi)
-{
-    constexpr int BM = kTileM, BK = kTileK;
-    constexpr int THREADS = 64 * WM * WN;
-    constexpr int MT = BM / (16 * WM), NT = BN / (16 * WN);
-    static_assert(THREADS == 512 && BN <= 64, "a load takes 64 rows");
-    constexpr int A_LOADS = BM * 8 / THREADS;  // 16-byte loads of a thread for one stage of A
-    __shared__ __attribute__((aligned(1024))) uint16_t lds_a[2][BM * BK];
-    __shared__ __attribute__((aligned(1024))) uint16_t lds_b[2][BN * BK];
-
-    uint32_t tm, tn, split;
-    tile_of_workgroup(g, &tm, &tn, &split);
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
-    const uint32_t m_base = tm * BM, n_base = tn * BN;
-    const uint32_t k0 = split * g.k;
-    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
-    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
-    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) * 2 + col * 2;
-    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) * 2 + col * 2;
-    auto load = [&](int stage, uint32_t k) {
-        typedef __attribute__((address_space(3))) void lds_void;
-        const bool in = k + col < depth;
-#pragma unroll
-        for (int i = 0; i < A_LOADS; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.a + k0, g.lda, m_base + i * 64, g.m),
-                                                     (lds_void*)(&lds_a[stage][(i * THREADS + wave * 64) * 8]), 16,
-                                                     in ? off_a : kPastEnd, k * 2, 0, 0);
-        if (BN == 64 || wave * 8 < BN)  // the same for a whole wave
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.b + k0, g.ldb, n_base, g.n),
-                                                     (lds_void*)(&lds_b[stage][wave * 64 * 8]), 16,
-                                                     in ? off_b : kPastEnd, k * 2, 0, 0);
-    };
-
-    Tile<MT, NT> acc;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    const int frow = lane & 15, fcol = lane >> 4;
-    if (depth) load(0, 0);  // a split past the end has nothing to add
-    int stage = 0;
-    for (uint32_t k = 0; k < depth; k += BK, stage ^= 1) {
-        __syncthreads();  // this stage has arrived, and nobody reads the other one any more
-        if (k + BK < depth) load(stage ^ 1, k + BK);
-#pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            const int col = ((kk * 4 + fcol) ^ (frow & 7)) * 8;
-            typename T::Frag fa[MT], fb[NT];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                fa[i] = *reinterpret_cast<const typename T::Frag*>(
-                    &lds_a[stage][((wm * MT + i) * 16 + frow) * BK + col]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                fb[j] = *reinterpret_cast<const typename T::Frag*>(
-                    &lds_b[stage][((wn * NT + j) * 16 + frow) * BK + col]);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc.v[i][j] = T::mma(fa[i], fb[j], acc.v[i][j]);
-        }
-    }
-    epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * WM + wm, split, NoStaging{});
-}
-
 // ---------------------------------------------------------------------------
 // the large tile
 // ---------------------------------------------------------------------------
@@ -302,6 +233,22 @@ __device__ __forceinline__ void read_fragments4(i32x4 (&b0)[2], i32x4 (&b1)[2], 
         "s_waitcnt lgkmcnt(0)"
         : "=&v"(b0[0]), "=&v"(b0[1]), "=&v"(b1[0]), "=&v"(b1[1])
         : "v"(pb0), "v"(pb1)
+        : "memory");
+}
+
+__device__ __forceinline__ void read_fragments6(i32x4 (&a)[2][2], i32x4 (&b)[2], uint32_t pa0, uint32_t pa1,
+                                                uint32_t pb0, uint32_t pb1)
+{
+    asm volatile(
+        "ds_read_b128 %0, %6\n"
+        "ds_read_b128 %1, %7\n"
+        "ds_read_b128 %2, %6 offset:2048\n"
+        "ds_read_b128 %3, %7 offset:2048\n"
+        "ds_read_b128 %4, %8\n"
+        "ds_read_b128 %5, %9\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(b[0]), "=&v"(b[1])
+        : "v"(pa0), "v"(pa1), "v"(pb0), "v"(pb1)
         : "memory");
 }
 
@@ -419,6 +366,90 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
         __syncthreads();
     }
     epi(acc, m_base + wm * 128, n_base + wn * 64, g, tm * 2 + wm, split, Staging{lds, wm * 128u, wn * 64u, m_base, n_base});
+}
+
+// ---------------------------------------------------------------------------
+// few rows of B
+// ---------------------------------------------------------------------------
+// The time is that of reading A once: four stages of 64 deep, three of them in
+// flight (120 KiB a CU), each waited for when it is due. 16 or 64 rows of B,
+// whose stage has room for 64 either way, so that every wave has as many loads
+// in flight. WM waves along A.
+template <class T, int BN, class Epilogue>
+__global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilogue epi)
+{
+    static_assert(BN == 16 || BN == 64, "tiles of B");
+    constexpr int WM = BN == 16 ? 8 : 4, WN = 8 / WM, MT = 16 / WM, NT = BN / (16 * WN);
+    constexpr uint32_t kStage = 40960, kB = 32768, kStages = 4;
+    __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+    uint32_t tm, tn, split;
+    tile_of_workgroup(g, &tm, &tn, &split);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t wm = wave / WN, wn = wave % WN;
+    const uint32_t m_base = tm * kTileM, n_base = tn * BN;
+    const uint32_t k0 = split * g.k;
+    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
+    const uint32_t steps = (depth + kTileK - 1) / kTileK;
+
+    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
+    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) * 2 + col * 2;
+    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) * 2 + col * 2;
+    const uint32_t n_rows = BN == 64 ? g.n : min(g.n, n_base + BN);
+    auto fetch = [&](uint32_t to, uint32_t step) {
+        typedef __attribute__((address_space(3))) void lds_void;
+        const uint32_t at = step * kTileK;
+        const bool in = at + col < depth;
+        char* p = lds + to + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.a + k0, g.lda, m_base + i * 64, g.m),
+                                                     (lds_void*)(p + i * 8192), 16, in ? off_a : kPastEnd, at * 2, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.b + k0, g.ldb, n_base, n_rows), (lds_void*)(p + kB), 16,
+                                                 in ? off_b : kPastEnd, at * 2, 0, 0);
+    };
+
+    Tile<MT, NT> acc;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (steps) {
+        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+        const int frow = lane & 15, fcol = lane >> 4;
+        const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
+        const uint32_t pa = base + (wm * MT * 16 + frow) * 128 + swizzled;
+        const uint32_t pb = base + kB + (wn * NT * 16 + frow) * 128 + swizzled;
+        fetch(0, 0);
+        fetch(kStage, 1);
+        fetch(2 * kStage, 2);
+        uint32_t stage = 0, ahead = 3 * kStage;
+        i32x4 fa[MT][2], fb[NT][2];
+        for (uint32_t k = 0; k < steps; ++k) {
+            // this stage has arrived in every wave, and nobody reads the one before any more
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(10)\n s_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(ahead, k + 3);
+            const uint32_t xa = pa + stage, xb = pb + stage;
+            if constexpr (BN == 64) read_fragments<0, 0>(fa, fb[0], fb[1], xa, xa ^ 64, xb, xb ^ 64);
+            else read_fragments6(fa, fb[0], xa, xa ^ 64, xb, xb ^ 64);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        acc.v[i][j] = T::mma(__builtin_bit_cast(typename T::Frag, fa[i][kk]),
+                                             __builtin_bit_cast(typename T::Frag, fb[j][kk]), acc.v[i][j]);
+            ahead = stage;
+            stage = stage == (kStages - 1) * kStage ? 0 : stage + kStage;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * WM + wm, split, NoStaging{});
 }
 
 // ---------------------------------------------------------------------------
@@ -564,9 +595,10 @@ private:
 };
 
 // gemm_large's scheme on 256 x 128 x 32 tiles of three pieces, 8 waves of 64 x
-// 64: 48 matrix instructions a half step. g.k, g.k_all: depths; lda, ldb: three
-// times the padded depth.
-template <class Epilogue>
+// 64: 48 matrix instructions a half step. With at most 16 columns only the
+// first quarter of a wave's is multiplied (NJ = 1). g.k, g.k_all: depths; lda,
+// ldb: three times the padded depth.
+template <int NJ, class Epilogue>
 __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Epilogue epi)
 {
     using T = MmaBF16;
@@ -620,7 +652,7 @@ __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Ep
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < NJ; ++j)
                     acc.v[i0 + i][j] = T::mma(__builtin_bit_cast(T::Frag, f[i][kOfA[k]]),
                                               __builtin_bit_cast(T::Frag, fb[j][kOfB[k]]), acc.v[i0 + i][j]);
         __builtin_amdgcn_s_setprio(0);
@@ -670,17 +702,18 @@ hipError_t launch_gemm_pieces(GemmArgs g, const Epilogue& epi, hipStream_t strea
 {
     g.tiles_m = (g.m + kTileM - 1) / kTileM;
     g.tiles_n = (g.n + kPiecesN - 1) / kPiecesN;
-    hipLaunchKernelGGL((gemm_pieces<Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(512), 0, stream, g, epi);
+    const dim3 grid(g.tiles_m * g.tiles_n * g.splits);
+    if (g.n <= 16) hipLaunchKernelGGL((gemm_pieces<1, Epilogue>), grid, dim3(512), 0, stream, g, epi);
+    else hipLaunchKernelGGL((gemm_pieces<4, Epilogue>), grid, dim3(512), 0, stream, g, epi);
     return hipGetLastError();
 }
 
-template <class T, int BN, int WM, int WN, class Epilogue>
-hipError_t launch_gemm(GemmArgs g, const Epilogue& epi, hipStream_t stream)
+template <class T, int BN, class Epilogue>
+hipError_t launch_gemm_few(GemmArgs g, const Epilogue& epi, hipStream_t stream)
 {
     g.tiles_m = (g.m + kTileM - 1) / kTileM;
     g.tiles_n = (g.n + BN - 1) / BN;
-    hipLaunchKernelGGL((gemm<T, BN, WM, WN, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(64 * WM * WN), 0,
-                       stream, g, epi);
+    hipLaunchKernelGGL((gemm_few<T, BN, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(512), 0, stream, g, epi);
     return hipGetLastError();
 }
 

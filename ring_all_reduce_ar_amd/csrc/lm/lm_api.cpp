@@ -222,16 +222,20 @@ ar_result_t run_clip(const ar_comm* comm, ar::lm::ClipKind first_kind, const Bat
     const int grid = static_cast<int>(std::min<uint32_t>(most, ar::lm::kClipSlots));
     bool head = true;
     for (const auto& a : first.list()) {
-        const hipError_t e = ar::lm::launch_clip_pass(first_kind, a, 1, dtype, op, norm, nt, head, grid, ws, stream);
+        const hipError_t e = ar::lm::launch_clip_norm(first_kind, a, dtype, op, norm, nt, head, grid, ws, stream);
         if (e != hipSuccess) return hip_fail(e, "kernel launch");
         head = false;
     }
-    hipError_t e = ar::lm::launch_clip_join(grid, norm, max_norm, ws, norm_out, stream);
-    if (e != hipSuccess) return hip_fail(e, "kernel launch");
+    const bool each = apply && !apply->list().empty() && grid <= ar::lm::kClipJoinEach;
+    if (!each) {
+        const hipError_t e = ar::lm::launch_clip_join(grid, norm, max_norm, ws, norm_out, stream);
+        if (e != hipSuccess) return hip_fail(e, "kernel launch");
+    }
     if (!apply) return AR_SUCCESS;
     for (const auto& a : apply->list()) {
         const int gx = static_cast<int>(std::min<uint64_t>(a.h.ntiles, kMaxGridX));
-        e = ar::lm::launch_clip_pass(ar::lm::kClipApply, a, ndst, dtype, op, norm, nt, false, gx, ws, stream);
+        const hipError_t e = ar::lm::launch_clip_apply(a, ndst, dtype, norm, nt, each ? grid : 0, max_norm, gx, ws,
+                                                       norm_out, stream);
         if (e != hipSuccess) return hip_fail(e, "kernel launch");
     }
     return AR_SUCCESS;

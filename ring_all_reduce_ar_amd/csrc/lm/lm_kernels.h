@@ -12,13 +12,16 @@ namespace lm {
 
 // ---- gradient norm and clip -------------------------------------------------
 // Norm passes leave one double per workgroup in the workspace, at most
-// kClipSlots, which one workgroup then joins.
+// kClipSlots. Up to kClipJoinEach of them are joined by each workgroup that
+// scales, behind its first loads: 150000 bf16 elements in 15 us a call rather
+// than 20 with a launch in between. 1600 of them (8 ranks x 25 MiB) cost as much
+// in every workgroup as the launch does, 90 against 87 us.
 constexpr int kClipSlots = 8192;
+constexpr int kClipJoinEach = 256;
 
 struct ClipWorkspace {
-    double total;   // the norm
-    float scale;    // min(1, max_norm / (total + eps))
-    float pad[13];
+    float scale;  // min(1, max_norm / (norm + eps)), where a launch of its own joins
+    float pad[15];
     double partial[kClipSlots];
 };
 
@@ -34,14 +37,18 @@ __host__ __device__ constexpr int clip_tiles(ClipKind kind, int nsources, int el
     return kind == kClipReduce ? rank_major_any_tiles(nsources, elem_bytes) : 4;
 }
 
-// One batch: `a.h.n` sources and then `ndst` destinations for each tensor of
-// the table. `first`: the batch's partials are stored rather than joined to
-// those of earlier batches.
-hipError_t launch_clip_pass(ClipKind kind, const MultiArgs& a, int ndst, ar_dtype_t dtype, ar_op_t op, ar_norm_t norm,
-                            bool nt, bool first, int grid, ClipWorkspace* ws, hipStream_t stream);
+// One batch: `a.h.n` sources and then the destinations for each tensor of the
+// table. kClipMeasure and kClipReduce; `first`: the batch's partials are stored
+// rather than joined to those of earlier batches.
+hipError_t launch_clip_norm(ClipKind kind, const MultiArgs& a, ar_dtype_t dtype, ar_op_t op, ar_norm_t norm, bool nt,
+                            bool first, int grid, ClipWorkspace* ws, hipStream_t stream);
 // Joins `slots` partials into the norm and the scale; `norm_out` may be null.
 hipError_t launch_clip_join(int slots, ar_norm_t norm, double max_norm, ClipWorkspace* ws, float* norm_out,
                             hipStream_t stream);
+// kClipApply with `ndst` destinations a tensor: by the scale of `slots`
+// partials, or, where that is 0, by the joined one.
+hipError_t launch_clip_apply(const MultiArgs& a, int ndst, ar_dtype_t dtype, ar_norm_t norm, bool nt, int slots,
+                             double max_norm, int grid, ClipWorkspace* ws, float* norm_out, hipStream_t stream);
 
 // ---- embedding ----------------------------------------------------------------
 struct Indices {
