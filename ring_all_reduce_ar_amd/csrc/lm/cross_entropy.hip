@@ -11,9 +11,10 @@
 // are gemm.h's, with both operands contiguous along the summed axis, so W and
 // X are also laid out transposed, and d is written in both orders.
 //
-// fp32 operands are laid out as three bf16 pieces each: six bf16 products give
-// the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the fp32 matrix
-// instructions end at 0.16.
+// fp32 operands of more than 64 tokens are laid out as three bf16 pieces each:
+// six bf16 products give the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the
+// fp32 matrix instructions end at 0.16. With fewer tokens the time is that of
+// reading the weight, which then stays as it is.
 #include <type_traits>
 
 #include "gemm.h"
@@ -60,30 +61,27 @@ __device__ __forceinline__ void split3(float x, uint32_t (&p)[3])
 // ---------------------------------------------------------------------------
 // Stores eight depths k..k+7 (k a multiple of 8) of a row: as they are, or in pieces.
 template <int PARTS, class Raw>
-__device__ __forceinline__ void put8(uint16_t* row, uint64_t k, const Raw (&x)[8])
+__device__ __forceinline__ void put8(char* row, uint64_t k, const Raw (&x)[8])
 {
     if constexpr (PARTS == 1) {
-        u32x4 v;
+        u32x4 v[sizeof(x) / 16];
+        __builtin_memcpy(v, x, sizeof(x));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = x[2 * i] | (static_cast<uint32_t>(x[2 * i + 1]) << 16);
-        *reinterpret_cast<u32x4*>(row + k) = v;
+        for (uint32_t i = 0; i < sizeof(x) / 16; ++i) *reinterpret_cast<u32x4*>(row + k * sizeof(Raw) + i * 16) = v[i];
     } else {
         uint32_t p[8][3];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split3(x[i], p[i]);
-        uint16_t* at = row + (k / kPieceDepth) * (kPieceDepth * kPieces) + k % kPieceDepth;
+        char* at = row + (k / kPieceDepth) * (kPieceDepth * kPieces * 2) + k % kPieceDepth * 2;
 #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
             u32x4 v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = p[2 * i][q] | (p[2 * i + 1][q] << 16);
-            *reinterpret_cast<u32x4*>(at + q * kPieceDepth) = v;
+            *reinterpret_cast<u32x4*>(at + q * (kPieceDepth * 2)) = v;
         }
     }
 }
-
-template <int PARTS>
-using RawOf = typename std::conditional<PARTS == 1, uint16_t, float>::type;
 
 // Eight elements from a 16-byte boundary, or one by one as far as they go.
 template <class Raw, bool VEC>
@@ -103,32 +101,35 @@ __device__ __forceinline__ void get8(const void* in, uint64_t at, uint64_t left,
     for (int i = 0; i < 8; ++i) x[i] = static_cast<uint64_t>(i) < left ? gptr<Raw>(in)[at + i] : Raw(0);
 }
 
+// Bytes of one element of an operand.
+template <int PARTS, class Raw>
+constexpr uint64_t operand_bytes() { return PARTS == 1 ? sizeof(Raw) : kPieces * 2; }
+
 // out[r] = in[r] in pieces (or as it is, on a 16-byte boundary), zeros from
 // `width` up to `pad`. `lanes` (a power of two) threads a row.
-template <int PARTS, bool VEC>
+template <int PARTS, class Raw, bool VEC>
 __global__ __launch_bounds__(kBlock) void pack_rows(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
-                                                    uint64_t pad, uint16_t* out, int lanes)
+                                                    uint64_t pad, char* out, int lanes)
 {
     const uint64_t r = static_cast<uint64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
     if (r >= rows) return;
     for (uint64_t c = (threadIdx.x & (lanes - 1)) * 8ull; c < pad; c += lanes * 8ull) {
-        RawOf<PARTS> x[8];
-        get8<RawOf<PARTS>, VEC>(in, r * ld + c, c < width ? width - c : 0, x);
-        put8<PARTS>(out + r * pad * PARTS, c, x);
+        Raw x[8];
+        get8<Raw, VEC>(in, r * ld + c, c < width ? width - c : 0, x);
+        put8<PARTS>(out + r * pad * operand_bytes<PARTS, Raw>(), c, x);
     }
 }
 
 // out[c] = the column c of `in` for rows below `rows`, zeros up to `pad` (a
-// multiple of 64) and in rows whose target is ignored (whatever they hold).
-// 64 x 64 tiles through LDS; a lane takes eight rows of one column, eight
-// lanes 128 bytes (or three times 64, twice).
-template <int PARTS, bool VEC>
+// multiple of 8) and in rows whose target is ignored (whatever they hold).
+// 64 x 64 tiles through LDS; a lane takes eight rows of one column, eight lanes
+// 128 bytes of 16-bit elements.
+template <int PARTS, class Raw, bool VEC>
 __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
-                                                          uint64_t pad, uint16_t* out, Indices targets, int masked,
+                                                          uint64_t pad, char* out, Indices targets, int masked,
                                                           int64_t ignore, uint64_t vocab)
 {
-    using Raw = RawOf<PARTS>;
-    __shared__ Raw tile[64][PARTS == 1 ? 66 : 65];
+    __shared__ Raw tile[64][sizeof(Raw) == 2 ? 66 : 65];
     const uint64_t r0 = static_cast<uint64_t>(blockIdx.x) * 64, c0 = static_cast<uint64_t>(blockIdx.y) * 64;
     const int slot = threadIdx.x & 7;
 #pragma unroll
@@ -142,6 +143,7 @@ __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64
         for (int k = 0; k < 8; ++k) tile[row][slot * 8 + k] = x[k];
     }
     __syncthreads();
+    if (r0 + slot * 8 >= pad) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int c = i * 32 + (threadIdx.x >> 3);
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64
         Raw x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = tile[slot * 8 + k][c];
-        put8<PARTS>(out + (c0 + c) * pad * PARTS, r0 + slot * 8, x);
+        put8<PARTS>(out + (c0 + c) * pad * operand_bytes<PARTS, Raw>(), r0 + slot * 8, x);
     }
 }
 
@@ -294,8 +296,8 @@ __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices target
 // the same times g[t] / max |g| for the weight's.
 template <class T>
 struct DEpilogue {
-    uint16_t* d;
-    uint16_t* dt;
+    typename T::Elem* d;
+    typename T::Elem* dt;
     const float* lse;
     const float* g_losses;
     const RowScale* scale;
@@ -366,9 +368,11 @@ private:
             for (int i = 0; i < MT; ++i) {
                 const uint32_t v = m0 + quad * 4 + 16 * i;
                 const f32x4 x = acc.v[i][j];
-                if (d && t < g.n && v < piece_pad)
-                    *reinterpret_cast<u32x2*>(d + static_cast<uint64_t>(t) * piece_pad + v) =
-                        u32x2{T::pack2(x[0], x[1]), T::pack2(x[2], x[3])};
+                if (d && t < g.n && v < piece_pad) {
+                    auto* at = d + static_cast<uint64_t>(t) * piece_pad + v;
+                    if constexpr (sizeof(*at) == 4) *reinterpret_cast<f32x4*>(at) = x;
+                    else *reinterpret_cast<u32x2*>(at) = u32x2{T::pack2(x[0], x[1]), T::pack2(x[2], x[3])};
+                }
                 if (dt && t < t_pad) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
@@ -514,27 +518,30 @@ dim3 grid_for(uint64_t rows, int lanes)
     return dim3(static_cast<uint32_t>((rows + per - 1) / per));
 }
 
-template <int PARTS>
-hipError_t pack(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, uint16_t* out, hipStream_t s)
+template <int PARTS, class Raw>
+hipError_t pack(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, char* out, hipStream_t s)
 {
-    constexpr uint64_t EB = PARTS == 1 ? 2 : 4;
-    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * EB % 16 == 0;
+    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * sizeof(Raw) % 16 == 0;
     const int lanes = lanes_for(pad / 8);
-    if (vec) hipLaunchKernelGGL((pack_rows<PARTS, true>), grid_for(rows, lanes), dim3(kBlock), 0, s, in, ld, rows, width, pad, out, lanes);
-    else hipLaunchKernelGGL((pack_rows<PARTS, false>), grid_for(rows, lanes), dim3(kBlock), 0, s, in, ld, rows, width, pad, out, lanes);
-    return hipGetLastError();
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid_for(rows, lanes), dim3(kBlock), 0, s, in, ld, rows, width, pad, out, lanes);
+        return hipGetLastError();
+    };
+    return vec ? launch(pack_rows<PARTS, Raw, true>) : launch(pack_rows<PARTS, Raw, false>);
 }
 
-template <int PARTS>
-hipError_t transpose(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, uint16_t* out,
+template <int PARTS, class Raw>
+hipError_t transpose(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, char* out,
                      const CrossEntropyArgs& a, int masked, hipStream_t s)
 {
-    constexpr uint64_t EB = PARTS == 1 ? 2 : 4;
-    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * EB % 16 == 0;
-    const dim3 grid(static_cast<uint32_t>(pad / 64), static_cast<uint32_t>((width + 63) / 64));
-    if (vec) hipLaunchKernelGGL((pack_transposed<PARTS, true>), grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked, a.ignore_index, a.vocab);
-    else hipLaunchKernelGGL((pack_transposed<PARTS, false>), grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked, a.ignore_index, a.vocab);
-    return hipGetLastError();
+    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * sizeof(Raw) % 16 == 0;
+    const dim3 grid(static_cast<uint32_t>((pad + 63) / 64), static_cast<uint32_t>((width + 63) / 64));
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked,
+                           a.ignore_index, a.vocab);
+        return hipGetLastError();
+    };
+    return vec ? launch(pack_transposed<PARTS, Raw, true>) : launch(pack_transposed<PARTS, Raw, false>);
 }
 
 template <class T, int PARTS, class Epilogue>
@@ -544,8 +551,10 @@ hipError_t product(const GemmArgs& g, int tile_n, const Epilogue& epi, hipStream
         return launch_gemm_pieces(g, epi, s);
     } else {
         if (tile_n == 16) return launch_gemm_few<T, 16>(g, epi, s);
-        if (tile_n == 64) return launch_gemm_few<T, 64>(g, epi, s);
-        return launch_gemm_large<T>(g, epi, s);
+        if constexpr (sizeof(typename T::Elem) == 2) {
+            if (tile_n == 256) return launch_gemm_large<T>(g, epi, s);
+        }
+        return launch_gemm_few<T, 64>(g, epi, s);
     }
 }
 
@@ -556,39 +565,39 @@ uint64_t stat_rows_per_tile(int tile_n) { return tile_n == 16 ? 8 : tile_n == 25
 // F: the storage type; T: the matrix instruction's.
 template <class F, class T, int PARTS>
 struct Call {
-    static constexpr int EB = 16 / F::kEpv;
+    using Raw = typename std::conditional<PARTS == 1, typename T::Elem, float>::type;  // as the caller's tensors hold it
+    using Elem = typename T::Elem;
+    static constexpr uint64_t EB = sizeof(Raw), OB = operand_bytes<PARTS, Raw>();
     const CrossEntropyArgs& a;
     const CrossEntropyPlan& p;
     char* ws;
     hipStream_t s;
 
-    // The logits' operands, packed where the plan says so.
-    hipError_t hidden(const uint16_t** out, uint64_t* ld) const
+    // The logits' operands, packed where the plan says so, and their pitch in bytes.
+    hipError_t hidden(const char** out, uint64_t* ld) const
     {
         if (!p.pack_hidden) {
-            *out = static_cast<const uint16_t*>(a.hidden);
-            *ld = a.ld_hidden;
+            *out = static_cast<const char*>(a.hidden);
+            *ld = a.ld_hidden * EB;
             return hipSuccess;
         }
-        uint16_t* to = reinterpret_cast<uint16_t*>(ws + p.hidden);
-        *out = to;
-        *ld = p.k_pad * PARTS;
-        return pack<PARTS>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.k_pad, to, s);
+        *out = ws + p.hidden;
+        *ld = p.k_pad * OB;
+        return pack<PARTS, Raw>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.k_pad, ws + p.hidden, s);
     }
-    hipError_t weight(uint64_t v0, uint64_t rows, const uint16_t** out, uint64_t* ld) const
+    hipError_t weight(uint64_t v0, uint64_t rows, const char** out, uint64_t* ld) const
     {
         const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * EB;
         if (!p.pack_weight) {
-            *out = reinterpret_cast<const uint16_t*>(from);
-            *ld = a.ld_weight;
+            *out = from;
+            *ld = a.ld_weight * EB;
             return hipSuccess;
         }
-        uint16_t* to = reinterpret_cast<uint16_t*>(ws + p.weight);
-        *out = to;
-        *ld = p.k_pad * PARTS;
-        return pack<PARTS>(from, a.ld_weight, rows, a.width, p.k_pad, to, s);
+        *out = ws + p.weight;
+        *ld = p.k_pad * OB;
+        return pack<PARTS, Raw>(from, a.ld_weight, rows, a.width, p.k_pad, ws + p.weight, s);
     }
-    GemmArgs logits_args(const uint16_t* w, uint64_t ldw, const uint16_t* x, uint64_t ldx, uint64_t rows) const
+    GemmArgs logits_args(const char* w, uint64_t ldw, const char* x, uint64_t ldx, uint64_t rows) const
     {
         GemmArgs g{};
         g.a = w;
@@ -597,7 +606,7 @@ struct Call {
         g.ldb = ldx;
         g.m = static_cast<uint32_t>(rows);
         g.n = static_cast<uint32_t>(a.ntokens);
-        // an operand that lies as given ends at the width, which is then a multiple of 8
+        // an operand that lies as given ends at the width, then whole 16-byte columns
         g.k = g.k_all = static_cast<uint32_t>(p.pack_hidden && p.pack_weight ? p.k_pad : a.width);
         g.splits = 1;
         return g;
@@ -605,7 +614,7 @@ struct Call {
 
     hipError_t forward() const
     {
-        const uint16_t *x, *w;
+        const char *x, *w;
         uint64_t ldx, ldw, row0 = 0;
         hipError_t e = hidden(&x, &ldx);
         if (e != hipSuccess) return e;
@@ -632,21 +641,20 @@ struct Call {
 
     hipError_t backward() const
     {
-        const uint16_t *x = nullptr, *w = nullptr;
+        const char *x = nullptr, *w = nullptr;
         uint64_t ldx = 0, ldw = 0;
         hipError_t e = a.ntokens ? hidden(&x, &ldx) : hipSuccess;
         if (e != hipSuccess) return e;
-        uint16_t* d = a.grad_hidden && a.ntokens ? reinterpret_cast<uint16_t*>(ws + p.d) : nullptr;
-        uint16_t* dt = a.grad_weight ? reinterpret_cast<uint16_t*>(ws + p.dt) : nullptr;
-        uint16_t* wt = reinterpret_cast<uint16_t*>(ws + p.weight_t);
-        uint16_t* xt = reinterpret_cast<uint16_t*>(ws + p.hidden_t);
+        Elem* d = a.grad_hidden && a.ntokens ? reinterpret_cast<Elem*>(ws + p.d) : nullptr;
+        Elem* dt = a.grad_weight ? reinterpret_cast<Elem*>(ws + p.dt) : nullptr;
+        char *wt = ws + p.weight_t, *xt = ws + p.hidden_t;
         float* acc = reinterpret_cast<float*>(ws + p.grad_hidden_acc);
         RowScale* scale = reinterpret_cast<RowScale*>(ws + p.row_scale);
         hipLaunchKernelGGL(row_scale, dim3(1), dim3(1024), 0, s, a.grad_losses, a.targets, a.ignore_index, a.vocab,
                            a.ntokens, scale);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (dt && a.ntokens &&
-            (e = transpose<PARTS>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.t_pad, xt, a, 1, s)) != hipSuccess)
+            (e = transpose<PARTS, Raw>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.t_pad, xt, a, 1, s)) != hipSuccess)
             return e;
         for (uint64_t v0 = 0; v0 < a.vocab; v0 += p.piece) {
             const uint64_t rows = a.vocab - v0 < p.piece ? a.vocab - v0 : p.piece;
@@ -659,11 +667,11 @@ struct Call {
             }
             if (d) {
                 const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * EB;
-                if ((e = transpose<PARTS>(from, a.ld_weight, rows, a.width, pad, wt, a, 0, s)) != hipSuccess) return e;
+                if ((e = transpose<PARTS, Raw>(from, a.ld_weight, rows, a.width, pad, wt, a, 0, s)) != hipSuccess) return e;
                 GemmArgs g{};
                 g.a = wt;
-                g.b = d;
-                g.lda = g.ldb = pad * PARTS;
+                g.b = reinterpret_cast<const char*>(d);
+                g.lda = g.ldb = pad * OB;
                 g.m = static_cast<uint32_t>(a.width);
                 g.n = static_cast<uint32_t>(a.ntokens);
                 g.k_all = static_cast<uint32_t>(pad);
@@ -675,8 +683,8 @@ struct Call {
             if (dt) {
                 GemmArgs g{};
                 g.a = xt;
-                g.b = dt;
-                g.lda = g.ldb = p.t_pad * PARTS;
+                g.b = reinterpret_cast<const char*>(dt);
+                g.lda = g.ldb = p.t_pad * OB;
                 g.m = static_cast<uint32_t>(a.width);
                 g.n = static_cast<uint32_t>(rows);
                 g.k = g.k_all = static_cast<uint32_t>(p.t_pad);
@@ -708,16 +716,16 @@ struct Call {
 // the busiest CU: a product takes whole rounds of one tile a CU. `splits`
 // gets the best number of parts for the hidden gradient's sum.
 constexpr uint64_t kCUs = 256;
-double piece_cost(uint64_t rows, uint64_t ntokens, uint64_t width, uint64_t tile_n, uint64_t step, int* splits)
+double piece_cost(uint64_t rows, uint64_t ntokens, uint64_t width, uint64_t tile_n, uint64_t tile_w, uint64_t step,
+                  int* splits)
 {
     auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
     const uint64_t tv = up(rows, kTileM), tn = up(ntokens, tile_n), tw = up(width, kTileM);
-    const uint64_t tile_w = step == kPieceDepth ? kPiecesN : 256;
     // each round also costs about four steps to start and to end in
     double cost = static_cast<double>(up(tv * tn, kCUs) * (up(width, step) + 8)) +
                   static_cast<double>(up(up(rows, tile_w) * tw, kCUs) * (up(ntokens, step) + 4));
     double best = 0;
-    for (int k = 1; k <= 16; k *= 2) {
+    for (int k = 1; k <= 64; k *= 2) {
         if (k > 1 && rows / k < 512) break;
         // a part of the sum is written and read again: about a step for each of a tile's
         const double c = static_cast<double>(up(tw * tn * k, kCUs) * (up(up(rows, step), k) + 8)) + 2.0 * (k - 1);
@@ -735,15 +743,16 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
 {
     CrossEntropyPlan p{};
     const bool f32 = dtype == AR_FLOAT32;
-    const uint64_t parts = f32 ? kPieces : 1, step = f32 ? kPieceDepth : kTileK;
+    p.pieces = f32 && ntokens > 64;
+    p.tile_n = ntokens <= 16 ? 16 : ntokens <= 64 ? 64 : f32 ? kPiecesN : 256;
+    const uint64_t ob = p.pieces ? kPieces * 2 : f32 ? 4 : 2, step = f32 ? 32 : kTileK;
     p.k_pad = round_up(width, step);
-    p.t_pad = round_up(ntokens, kTileK);
-    // (backward, the tiles cover all of t_pad: they write its zeros)
-    p.tile_n = f32 ? kPiecesN : ntokens <= 16 && !backward ? 16 : ntokens <= 64 ? 64 : 256;
+    p.t_pad = round_up(ntokens, p.tile_n == 16 ? 16 : kTileK);  // the tiles cover it: they write its zeros
+    const uint64_t tile_w = p.pieces ? kPiecesN : f32 ? 64 : 256;
     p.pack_hidden = p.pack_weight = true;  // the caller clears these where the operands can be read as they lie
     // A piece's buffers come to at most about kPieceBytes; pieces are whole tiles.
     constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
-    const uint64_t row_bytes = 2 * parts * (p.k_pad + (backward ? 2 * p.t_pad + width : 0));
+    const uint64_t row_bytes = ob * (p.k_pad + (backward ? 2 * p.t_pad + width : 0));
     const uint64_t whole = round_up(vocab, kTileM) / kTileM;
     uint64_t most = kPieceBytes / (row_bytes * kTileM);
     if (most > 4096) most = 4096;  // the transposed piece's rows stay within a buffer's 2^31 bytes
@@ -761,8 +770,8 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         for (uint64_t m = most; m >= (most + 1) / 2 && m >= 1; m = m > stride ? m - stride : 0) {
             const uint64_t rows = m * kTileM, full = vocab / rows, rest = vocab - full * rows;
             int splits = 1, unused;
-            double c = piece_cost(full ? rows : rest, ntokens, width, p.tile_n, step, &splits) * (full ? full : 1);
-            if (full && rest) c += piece_cost(rest, ntokens, width, p.tile_n, step, &unused);
+            double c = piece_cost(full ? rows : rest, ntokens, width, p.tile_n, tile_w, step, &splits) * (full ? full : 1);
+            if (full && rest) c += piece_cost(rest, ntokens, width, p.tile_n, tile_w, step, &unused);
             if (best == 0 || c < best) {
                 best = c;
                 p.piece = rows;
@@ -777,16 +786,16 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         at += round_up(bytes, 256);
         return here;
     };
-    p.hidden = take(ntokens * p.k_pad * parts * 2);
-    p.weight = take(p.piece * p.k_pad * parts * 2);
+    p.hidden = take(ntokens * p.k_pad * ob);
+    p.weight = take(p.piece * p.k_pad * ob);
     if (!backward) {
         p.stats = take(p.stat_rows * ntokens * sizeof(Stats));
         p.target_logit = take(ntokens * 4);
     } else {
-        p.d = take(ntokens * p.piece * parts * 2);
-        p.dt = take(p.piece * p.t_pad * parts * 2);
-        p.weight_t = take(width * p.piece * parts * 2);
-        p.hidden_t = take(width * p.t_pad * parts * 2);
+        p.d = take(ntokens * p.piece * ob);
+        p.dt = take(p.piece * p.t_pad * ob);
+        p.weight_t = take(width * p.piece * ob);
+        p.hidden_t = take(width * p.t_pad * ob);
         p.grad_hidden_acc = take(static_cast<uint64_t>(p.splits) * ntokens * width * 4);
         p.row_scale = take(sizeof(RowScale));
     }
@@ -798,7 +807,9 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPla
                                 hipStream_t stream)
 {
     switch (dtype) {
-    case AR_FLOAT32: return Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.forward();
+    case AR_FLOAT32:
+        return p.pieces ? Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.forward()
+                        : Call<F32, MmaF32, 1>{a, p, ws, stream}.forward();
     case AR_FLOAT16: return Call<F16, MmaF16, 1>{a, p, ws, stream}.forward();
     case AR_BFLOAT16: return Call<BF16, MmaBF16, 1>{a, p, ws, stream}.forward();
     default: return hipErrorInvalidValue;
@@ -809,7 +820,9 @@ hipError_t launch_cross_entropy_backward(const CrossEntropyArgs& a, const CrossE
                                          char* ws, hipStream_t stream)
 {
     switch (dtype) {
-    case AR_FLOAT32: return Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.backward();
+    case AR_FLOAT32:
+        return p.pieces ? Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.backward()
+                        : Call<F32, MmaF32, 1>{a, p, ws, stream}.backward();
     case AR_FLOAT16: return Call<F16, MmaF16, 1>{a, p, ws, stream}.backward();
     case AR_BFLOAT16: return Call<BF16, MmaBF16, 1>{a, p, ws, stream}.backward();
     default: return hipErrorInvalidValue;

@@ -2,7 +2,7 @@
 //
 //   C[m][n] = sum_k A[m][k] * B[n][k]
 //
-// for 16-bit A and B whose rows are contiguous along K and 16-byte aligned; C
+// for A and B whose rows are contiguous along K and 16-byte aligned; C
 // stays in fp32 registers and goes to an epilogue. Tiles of both go from
 // memory straight into LDS. Three kernels: gemm_large for 256 x 256 tiles,
 // gemm_pieces for fp32 operands in three bf16 pieces, and gemm_few for few
@@ -29,7 +29,10 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// A matrix instruction: the operands' storage, and a fragment, 16 bytes of a
+// row's depth for each lane.
 struct MmaBF16 {
+    using Elem = uint16_t;
     using Frag = bf16x8;
     using Format = detail::BF16;
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c)
@@ -43,6 +46,7 @@ struct MmaBF16 {
     }
 };
 struct MmaF16 {
+    using Elem = uint16_t;
     using Frag = f16x8;
     using Format = detail::F16;
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c)
@@ -55,14 +59,28 @@ struct MmaF16 {
     }
 };
 
+// Its depth is four; the order in which a row's depth is summed is free as long
+// as both operands keep to it, so a lane's four values are four of them.
+struct MmaF32 {
+    using Elem = float;
+    using Frag = f32x4;
+    using Format = detail::F32;
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c)
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+};
+
 // Rows of A and B beyond M and N, and depths beyond k_all, are read as zeros.
 struct GemmArgs {
-    const uint16_t* a;
-    const uint16_t* b;
-    uint64_t lda, ldb;  // elements
+    const char* a;
+    const char* b;
+    uint64_t lda, ldb;  // bytes
     uint32_t m, n;
-    uint32_t k;         // of one split; a multiple of kTileK if there are several
-    uint32_t k_all;     // a multiple of 8 (of 32 for pieces); splits * k may pass it
+    uint32_t k;         // elements of one split; a multiple of kTileK if there are several
+    uint32_t k_all;     // whole 16-byte columns (32 elements of pieces); splits * k may pass it
     uint32_t tiles_m, tiles_n, splits;
 };
 
@@ -76,13 +94,13 @@ struct Tile {
 // A byte offset that lies past every buffer: the load gives zeros.
 constexpr uint32_t kPastEnd = 0x80000000u;
 
-// 64 rows from row `r0` of a matrix of `rows` rows; rows past the end lie
-// outside the buffer.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t* p, uint64_t ld, uint32_t r0, uint32_t rows)
+// 64 rows from row `r0` of a matrix of `rows` rows, `ld` (below 2^25) bytes
+// apart; rows past the end lie outside the buffer.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const char* p, uint64_t ld, uint32_t r0, uint32_t rows)
 {
     const uint32_t left = rows > r0 ? min(rows - r0, 64u) : 0;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p + static_cast<uint64_t>(r0) * ld), 0,
-                                             static_cast<int>(left * static_cast<uint32_t>(ld) * 2), 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p + static_cast<uint64_t>(r0) * ld), 0,
+                                             static_cast<int>(left * static_cast<uint32_t>(ld)), 0x00020000);
 }
 
 // Workgroups go round the eight XCDs one by one; each XCD gets a contiguous
@@ -292,9 +310,9 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
     const uint32_t steps = (depth + kTileK - 1) / kTileK;
 
     const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
-    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) * 2 + col * 2;
-    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) * 2 + col * 2;
-    const uint16_t *a = g.a + k0, *b = g.b + k0;
+    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) + col * 2;
+    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) + col * 2;
+    const char *a = g.a + static_cast<uint64_t>(k0) * 2, *b = g.b + static_cast<uint64_t>(k0) * 2;
     const __amdgpu_buffer_rsrc_t ra0 = row_buffer(a, g.lda, m_base, g.m), ra1 = row_buffer(a, g.lda, m_base + 64, g.m);
     const __amdgpu_buffer_rsrc_t ra2 = row_buffer(a, g.lda, m_base + 128, g.m), ra3 = row_buffer(a, g.lda, m_base + 192, g.m);
     const __amdgpu_buffer_rsrc_t rb0 = row_buffer(b, g.ldb, n_base, g.n), rb1 = row_buffer(b, g.ldb, n_base + 64, g.n);
@@ -371,10 +389,11 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
 // ---------------------------------------------------------------------------
 // few rows of B
 // ---------------------------------------------------------------------------
-// The time is that of reading A once: four stages of 64 deep, three of them in
-// flight (120 KiB a CU), each waited for when it is due. 16 or 64 rows of B,
-// whose stage has room for 64 either way, so that every wave has as many loads
-// in flight. WM waves along A.
+// The time is that of reading A once: four stages of 128 bytes a row, three of
+// them in flight (120 KiB a CU), each waited for when it is due. 16 or 64 rows
+// of B, whose stage has room for 64 either way, so that every wave has as many
+// loads in flight. fp32 rows are read as they are: their matrix instructions'
+// 157 TFLOP/s keep up with the memory here.
 template <class T, int BN, class Epilogue>
 __global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilogue epi)
 {
@@ -391,23 +410,25 @@ __global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilo
     const uint32_t m_base = tm * kTileM, n_base = tn * BN;
     const uint32_t k0 = split * g.k;
     const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
-    const uint32_t steps = (depth + kTileK - 1) / kTileK;
+    constexpr uint32_t EB = sizeof(typename T::Elem), kDepth = 128 / EB;
+    const uint32_t steps = (depth + kDepth - 1) / kDepth;
 
-    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
-    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) * 2 + col * 2;
-    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) * 2 + col * 2;
+    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 16;  // bytes
+    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) + col;
+    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) + col;
+    const char *a = g.a + static_cast<uint64_t>(k0) * EB, *b = g.b + static_cast<uint64_t>(k0) * EB;
     const uint32_t n_rows = BN == 64 ? g.n : min(g.n, n_base + BN);
     auto fetch = [&](uint32_t to, uint32_t step) {
         typedef __attribute__((address_space(3))) void lds_void;
-        const uint32_t at = step * kTileK;
-        const bool in = at + col < depth;
+        const uint32_t at = step * 128;
+        const bool in = at + col < depth * EB;
         char* p = lds + to + wave * 1024;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.a + k0, g.lda, m_base + i * 64, g.m),
-                                                     (lds_void*)(p + i * 8192), 16, in ? off_a : kPastEnd, at * 2, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(g.b + k0, g.ldb, n_base, n_rows), (lds_void*)(p + kB), 16,
-                                                 in ? off_b : kPastEnd, at * 2, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(a, g.lda, m_base + i * 64, g.m),
+                                                     (lds_void*)(p + i * 8192), 16, in ? off_a : kPastEnd, at, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(b, g.ldb, n_base, n_rows), (lds_void*)(p + kB), 16,
+                                                 in ? off_b : kPastEnd, at, 0, 0);
     };
 
     Tile<MT, NT> acc;
@@ -595,10 +616,9 @@ private:
 };
 
 // gemm_large's scheme on 256 x 128 x 32 tiles of three pieces, 8 waves of 64 x
-// 64: 48 matrix instructions a half step. With at most 16 columns only the
-// first quarter of a wave's is multiplied (NJ = 1). g.k, g.k_all: depths; lda,
-// ldb: three times the padded depth.
-template <int NJ, class Epilogue>
+// 64: 48 matrix instructions a half step. g.k, g.k_all: depths; lda,
+// ldb: six bytes for each of the padded depth.
+template <class Epilogue>
 __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Epilogue epi)
 {
     using T = MmaBF16;
@@ -619,13 +639,13 @@ __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Ep
     // wave's 64 rows of A, or the rows of B. 64-byte rows of four 16-byte
     // columns; column c of row r lies at c ^ (r / 2 & 3).
     const uint32_t row = tid >> 2, col = (tid & 3) ^ ((row >> 1) & 3);
-    const uint32_t off_a = ((row >> 5) * 64 + (row & 31)) * static_cast<uint32_t>(g.lda) * 2 + col * 16;
-    const uint32_t off_b = row * static_cast<uint32_t>(g.ldb) * 2 + col * 16;
-    auto rows_from = [&](const uint16_t* p, uint64_t ld, uint32_t r0, uint32_t rows) {
+    const uint32_t off_a = ((row >> 5) * 64 + (row & 31)) * static_cast<uint32_t>(g.lda) + col * 16;
+    const uint32_t off_b = row * static_cast<uint32_t>(g.ldb) + col * 16;
+    auto rows_from = [&](const char* p, uint64_t ld, uint32_t r0, uint32_t rows) {
         const uint32_t left = rows > r0 ? min(rows - r0, 256u) : 0;
         return __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p + static_cast<uint64_t>(k0) * kPieces + static_cast<uint64_t>(r0) * ld), 0,
-            static_cast<int>(left * static_cast<uint32_t>(ld) * 2), 0x00020000);
+            const_cast<char*>(p + static_cast<uint64_t>(k0) * (kPieces * 2) + static_cast<uint64_t>(r0) * ld), 0,
+            static_cast<int>(left * static_cast<uint32_t>(ld)), 0x00020000);
     };
     const __amdgpu_buffer_rsrc_t ra0 = rows_from(g.a, g.lda, m_base, g.m), ra1 = rows_from(g.a, g.lda, m_base + 32, g.m);
     const __amdgpu_buffer_rsrc_t rb = rows_from(g.b, g.ldb, n_base, g.n);
@@ -652,7 +672,7 @@ __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Ep
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                for (int j = 0; j < 4; ++j)
                     acc.v[i0 + i][j] = T::mma(__builtin_bit_cast(T::Frag, f[i][kOfA[k]]),
                                               __builtin_bit_cast(T::Frag, fb[j][kOfB[k]]), acc.v[i0 + i][j]);
         __builtin_amdgcn_s_setprio(0);
@@ -702,9 +722,7 @@ hipError_t launch_gemm_pieces(GemmArgs g, const Epilogue& epi, hipStream_t strea
 {
     g.tiles_m = (g.m + kTileM - 1) / kTileM;
     g.tiles_n = (g.n + kPiecesN - 1) / kPiecesN;
-    const dim3 grid(g.tiles_m * g.tiles_n * g.splits);
-    if (g.n <= 16) hipLaunchKernelGGL((gemm_pieces<1, Epilogue>), grid, dim3(512), 0, stream, g, epi);
-    else hipLaunchKernelGGL((gemm_pieces<4, Epilogue>), grid, dim3(512), 0, stream, g, epi);
+    hipLaunchKernelGGL((gemm_pieces<Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(512), 0, stream, g, epi);
     return hipGetLastError();
 }
 

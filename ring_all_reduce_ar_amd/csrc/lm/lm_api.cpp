@@ -383,9 +383,9 @@ bool plan_fits(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtyp
 }
 
 // The operand can be read as it lies.
-bool direct(const void* p, size_t ld, uint64_t width, ar_dtype_t dtype)
+bool direct(const void* p, size_t ld, uint64_t width, size_t elem, bool pieces)
 {
-    return dtype != AR_FLOAT32 && width % 8 == 0 && rows16(p, ld, 2) && ld < (size_t(1) << 24);
+    return !pieces && width * elem % 16 == 0 && rows16(p, ld, elem) && ld < (size_t(1) << 25) / elem;
 }
 
 }  // namespace
@@ -570,8 +570,8 @@ ar_result_t cross_entropy_common(ar_comm* comm, const void* hidden, const void* 
     if (rc == AR_SUCCESS) rc = check_vector("targets", targets, ntokens, index_bytes(index), reads);
     if (rc != AR_SUCCESS) return rc;
     *plan = ar::lm::plan_cross_entropy(ntokens, vocab, width, dtype, backward);
-    plan->pack_hidden = !direct(hidden, *ld_hidden, width, dtype);
-    plan->pack_weight = !direct(weight, *ld_weight, width, dtype);
+    plan->pack_hidden = !direct(hidden, *ld_hidden, width, e, plan->pieces);
+    plan->pack_weight = !direct(weight, *ld_weight, width, e, plan->pieces);
     return check_workspace(comm, plan->bytes);
 }
 

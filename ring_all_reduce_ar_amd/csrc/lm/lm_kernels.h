@@ -129,7 +129,8 @@ struct CrossEntropyArgs {
 struct CrossEntropyPlan {
     uint64_t piece;        // vocabulary rows a piece
     uint64_t k_pad;        // the width, up to whole steps
-    uint64_t t_pad;        // tokens, up to a multiple of kTileK
+    uint64_t t_pad;        // tokens, up to a multiple of kTileK (of 16 if there are no more)
+    bool pieces;           // fp32 operands in bf16 pieces
     bool pack_hidden, pack_weight;
     int tile_n;            // token tile of the logits' product
     int splits;            // parts of the vocabulary axis in the hidden gradient's product
