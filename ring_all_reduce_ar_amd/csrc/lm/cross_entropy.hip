@@ -558,9 +558,15 @@ hipError_t product(const GemmArgs& g, int tile_n, const Epilogue& epi, hipStream
     }
 }
 
-// Rows of statistics that a tile of kTileM vocabulary rows leaves: one for
-// each wave along it.
-uint64_t stat_rows_per_tile(int tile_n) { return tile_n == 16 ? 8 : tile_n == 256 ? 2 : 4; }
+// Rows of statistics that the logits of `rows` vocabulary rows leave: one for
+// each wave along a tile.
+uint64_t stat_rows_of(uint64_t rows, uint64_t ntokens, int tile_n)
+{
+    if (tile_n > 64) return (rows + kTileM - 1) / kTileM * (tile_n == 256 ? 2 : 4);
+    const uint64_t tile_m = few_tile_m(rows, ntokens, 1, tile_n);
+    const uint64_t waves = (tile_m == kTileM ? 8 : 4) / (tile_n == 16 ? 1 : 2);
+    return (rows + tile_m - 1) / tile_m * waves;
+}
 
 // F: the storage type; T: the matrix instruction's.
 template <class F, class T, int PARTS>
@@ -626,7 +632,7 @@ struct Call {
             if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
             const StatsEpilogue epi{stats, target_logit, a.targets, a.ignore_index, a.vocab, v0, row0};
             if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
-            row0 += (rows + kTileM - 1) / kTileM * stat_rows_per_tile(p.tile_n);
+            row0 += stat_rows_of(rows, a.ntokens, p.tile_n);
         }
         auto join = [&](auto kernel, uint32_t tokens) {
             hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.ntokens + tokens - 1) / tokens)), dim3(kJoinBlock), 0,
@@ -779,7 +785,12 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
             }
         }
     }
-    p.stat_rows = (vocab + p.piece - 1) / p.piece * (p.piece / kTileM) * stat_rows_per_tile(p.tile_n);
+    {  // in pieces, or, where the weight is read as it lies, at once
+        const uint64_t full = vocab / p.piece, rest = vocab % p.piece;
+        const uint64_t pieces = full * stat_rows_of(p.piece, ntokens, p.tile_n) + stat_rows_of(rest, ntokens, p.tile_n);
+        const uint64_t once = stat_rows_of(vocab, ntokens, p.tile_n);
+        p.stat_rows = pieces > once ? pieces : once;
+    }
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;

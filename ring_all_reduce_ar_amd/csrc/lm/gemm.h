@@ -94,13 +94,20 @@ struct Tile {
 // A byte offset that lies past every buffer: the load gives zeros.
 constexpr uint32_t kPastEnd = 0x80000000u;
 
-// 64 rows from row `r0` of a matrix of `rows` rows, `ld` (below 2^25) bytes
-// apart; rows past the end lie outside the buffer.
+// Up to 64 rows from row `r0` of a matrix of `rows` rows, `ld` (below 2^25)
+// bytes apart; rows past the end lie outside the buffer.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const char* p, uint64_t ld, uint32_t r0, uint32_t rows)
 {
     const uint32_t left = rows > r0 ? min(rows - r0, 64u) : 0;
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p + static_cast<uint64_t>(r0) * ld), 0,
                                              static_cast<int>(left * static_cast<uint32_t>(ld)), 0x00020000);
+}
+
+// Sixteen bytes a lane, straight into LDS from `to` (of the wave) on; the
+// instruction's own offset would move both ends, so `at` is the scalar one.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t from, char* to, uint32_t off, uint32_t at)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, off, at, 0, 0);
 }
 
 // Workgroups go round the eight XCDs one by one; each XCD gets a contiguous
@@ -254,27 +261,61 @@ __device__ __forceinline__ void read_fragments4(i32x4 (&b0)[2], i32x4 (&b1)[2], 
         : "memory");
 }
 
-__device__ __forceinline__ void read_fragments6(i32x4 (&a)[2][2], i32x4 (&b)[2], uint32_t pa0, uint32_t pa1,
-                                                uint32_t pb0, uint32_t pb1)
+// MT groups of 16 rows at a0 and a1, NT at b0 and b1.
+template <int MT, int NT>
+__device__ __forceinline__ void read_few(i32x4 (&a)[MT][2], i32x4 (&b)[NT][2], uint32_t a0, uint32_t a1, uint32_t b0,
+                                         uint32_t b1)
 {
-    asm volatile(
-        "ds_read_b128 %0, %6\n"
-        "ds_read_b128 %1, %7\n"
-        "ds_read_b128 %2, %6 offset:2048\n"
-        "ds_read_b128 %3, %7 offset:2048\n"
-        "ds_read_b128 %4, %8\n"
-        "ds_read_b128 %5, %9\n"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(b[0]), "=&v"(b[1])
-        : "v"(pa0), "v"(pa1), "v"(pb0), "v"(pb1)
-        : "memory");
+    if constexpr (MT == 4 && NT == 2) {
+        read_fragments<0, 0>(a, b[0], b[1], a0, a1, b0, b1);
+    } else if constexpr (MT == 2 && NT == 2) {
+        asm volatile(
+            "ds_read_b128 %0, %8\n"
+            "ds_read_b128 %1, %9\n"
+            "ds_read_b128 %2, %8 offset:2048\n"
+            "ds_read_b128 %3, %9 offset:2048\n"
+            "ds_read_b128 %4, %10\n"
+            "ds_read_b128 %5, %11\n"
+            "ds_read_b128 %6, %10 offset:2048\n"
+            "ds_read_b128 %7, %11 offset:2048\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(b[0][0]), "=&v"(b[0][1]),
+              "=&v"(b[1][0]), "=&v"(b[1][1])
+            : "v"(a0), "v"(a1), "v"(b0), "v"(b1)
+            : "memory");
+    } else if constexpr (MT == 2) {
+        static_assert(NT == 1, "");
+        asm volatile(
+            "ds_read_b128 %0, %6\n"
+            "ds_read_b128 %1, %7\n"
+            "ds_read_b128 %2, %6 offset:2048\n"
+            "ds_read_b128 %3, %7 offset:2048\n"
+            "ds_read_b128 %4, %8\n"
+            "ds_read_b128 %5, %9\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(b[0][0]), "=&v"(b[0][1])
+            : "v"(a0), "v"(a1), "v"(b0), "v"(b1)
+            : "memory");
+    } else {
+        static_assert(MT == 1 && NT == 1, "");
+        asm volatile(
+            "ds_read_b128 %0, %4\n"
+            "ds_read_b128 %1, %5\n"
+            "ds_read_b128 %2, %6\n"
+            "ds_read_b128 %3, %7\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(b[0][0]), "=&v"(b[0][1])
+            : "v"(a0), "v"(a1), "v"(b0), "v"(b1)
+            : "memory");
+    }
 }
 
-// All but the newest six direct loads have arrived, in every wave.
-__device__ __forceinline__ void arrive6()
+// All but the newest N direct loads have arrived, in every wave.
+template <int N>
+__device__ __forceinline__ void arrive()
 {
     __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(6)\n s_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0)\n s_barrier" : : "n"(N) : "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 __device__ __forceinline__ void meet()
@@ -320,10 +361,9 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
     auto fetch = [&](__amdgpu_buffer_rsrc_t x, __amdgpu_buffer_rsrc_t y, uint32_t to, uint32_t off, uint32_t step) {
         const uint32_t at = step * kTileK;
         const uint32_t v = at + col < depth ? off : kPastEnd;
-        typedef __attribute__((address_space(3))) void lds_void;
         char* p = lds + to + wave * 1024;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)p, 16, v, at * 2, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(y, (lds_void*)(p + 8192), 16, v, at * 2, 0, 0);
+        load_to_lds(x, p, v, at * 2);
+        load_to_lds(y, p + 8192, v, at * 2);
     };
 
     Tile<8, 4> acc;
@@ -357,7 +397,7 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
         fetch(ra1, ra3, kA1, off_a, 0);
         fetch(ra0, ra2, kStage, off_a, 1);
         fetch(rb0, rb1, kStage + kB, off_b, 1);
-        arrive6();
+        arrive<6>();
         read_fragments4(fa0[0], fa0[1], pa, pa ^ 64);
         if (wave >= 4) meet();
         uint32_t stage = 0;
@@ -365,13 +405,13 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
             fetch(rb2, rb3, (stage ^ kStage) + kB1, off_b, k + 1);
             fetch(ra1, ra3, (stage ^ kStage) + kA1, off_a, k + 1);
             read_fragments<0, 4096>(fb, fa0[2], fa0[3], pb, pb ^ 64, pa, pa ^ 64);
-            arrive6();
+            arrive<6>();
             multiply(fa0, 0);
             meet();
             fetch(ra0, ra2, stage, off_a, k + 2);
             fetch(rb0, rb1, stage + kB, off_b, k + 2);
             read_fragments<kA1, 0>(fa1, fa0[0], fa0[1], pa, pa ^ 64, pa ^ kStage, pa ^ kStage ^ 64);
-            arrive6();
+            arrive<6>();
             multiply(fa1, 4);
             meet();
             pa ^= kStage;
@@ -389,25 +429,40 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
 // ---------------------------------------------------------------------------
 // few rows of B
 // ---------------------------------------------------------------------------
-// The time is that of reading A once: four stages of 128 bytes a row, three of
-// them in flight (120 KiB a CU), each waited for when it is due. 16 or 64 rows
-// of B, whose stage has room for 64 either way, so that every wave has as many
-// loads in flight. fp32 rows are read as they are: their matrix instructions'
-// 157 TFLOP/s keep up with the memory here.
-template <class T, int BN, class Epilogue>
-__global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilogue epi)
+// The time is that of reading A once: stages of 128 bytes a row, all but one of
+// them in flight, each waited for when it is due. 256 rows of A and 16 or 64 of
+// B with four stages (120 KiB in flight a CU), or 64 rows of A with six, where
+// the larger tiles are fewer than the CUs. fp32 rows are read as they are:
+// their matrix instructions' 157 TFLOP/s keep up with the memory here. 65536 x
+// 2048 fp16 for 3 rows of B: 43 us from the last-level cache, about 52 from HBM.
+constexpr int kFewM = 64;
+
+template <int BM, int BN>
+struct FewShape {
+    static_assert((BM == kTileM || BM == kFewM) && (BN == 16 || BN == 64), "tiles");
+    static constexpr int kThreads = BM == kTileM ? 512 : 256, kWaves = kThreads / 64;
+    static constexpr int kRows = kThreads / 8;                    // of one load
+    static constexpr int kRowsB = BN > kRows ? BN : kRows;        // every wave has as many loads in flight
+    static constexpr int kLoadsA = BM / kRows, kLoadsB = kRowsB / kRows;
+    static constexpr int kStages = BM == kTileM ? 4 : 6;
+    static constexpr uint32_t kB = BM * 128, kStage = kB + kRowsB * 128;
+    static constexpr int WN = BN == 16 ? 1 : 2, WM = kWaves / WN;  // waves
+    static constexpr int MT = BM / (16 * WM), NT = BN / (16 * WN);
+};
+
+template <class T, int BM, int BN, int THREADS, class Epilogue>
+__global__ __launch_bounds__(THREADS) void gemm_few(const GemmArgs g, const Epilogue epi)
 {
-    static_assert(BN == 16 || BN == 64, "tiles of B");
-    constexpr int WM = BN == 16 ? 8 : 4, WN = 8 / WM, MT = 16 / WM, NT = BN / (16 * WN);
-    constexpr uint32_t kStage = 40960, kB = 32768, kStages = 4;
-    __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage];
+    using S = FewShape<BM, BN>;
+    constexpr int MT = S::MT, NT = S::NT;
+    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStage];
     uint32_t tm, tn, split;
     tile_of_workgroup(g, &tm, &tn, &split);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t wm = wave / WN, wn = wave % WN;
-    const uint32_t m_base = tm * kTileM, n_base = tn * BN;
+    const uint32_t wm = wave / S::WN, wn = wave % S::WN;
+    const uint32_t m_base = tm * BM, n_base = tn * BN;
     const uint32_t k0 = split * g.k;
     const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
     constexpr uint32_t EB = sizeof(typename T::Elem), kDepth = 128 / EB;
@@ -417,18 +472,18 @@ __global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilo
     const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) + col;
     const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) + col;
     const char *a = g.a + static_cast<uint64_t>(k0) * EB, *b = g.b + static_cast<uint64_t>(k0) * EB;
-    const uint32_t n_rows = BN == 64 ? g.n : min(g.n, n_base + BN);
+    const uint32_t n_rows = min(g.n, n_base + BN);
     auto fetch = [&](uint32_t to, uint32_t step) {
-        typedef __attribute__((address_space(3))) void lds_void;
         const uint32_t at = step * 128;
         const bool in = at + col < depth * EB;
         char* p = lds + to + wave * 1024;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(a, g.lda, m_base + i * 64, g.m),
-                                                     (lds_void*)(p + i * 8192), 16, in ? off_a : kPastEnd, at, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(row_buffer(b, g.ldb, n_base, n_rows), (lds_void*)(p + kB), 16,
-                                                 in ? off_b : kPastEnd, at, 0, 0);
+        for (int i = 0; i < S::kLoadsA; ++i)
+            load_to_lds(row_buffer(a, g.lda, m_base + i * S::kRows, g.m), p + i * S::kRows * 128, in ? off_a : kPastEnd, at);
+#pragma unroll
+        for (int i = 0; i < S::kLoadsB; ++i)
+            load_to_lds(row_buffer(b, g.ldb, n_base + i * S::kRows, n_rows), p + S::kB + i * S::kRows * 128,
+                        in ? off_b : kPastEnd, at);
     };
 
     Tile<MT, NT> acc;
@@ -442,21 +497,18 @@ __global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilo
         const int frow = lane & 15, fcol = lane >> 4;
         const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
         const uint32_t pa = base + (wm * MT * 16 + frow) * 128 + swizzled;
-        const uint32_t pb = base + kB + (wn * NT * 16 + frow) * 128 + swizzled;
-        fetch(0, 0);
-        fetch(kStage, 1);
-        fetch(2 * kStage, 2);
-        uint32_t stage = 0, ahead = 3 * kStage;
+        const uint32_t pb = base + S::kB + (wn * NT * 16 + frow) * 128 + swizzled;
+        constexpr int kAhead = S::kStages - 1;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i * S::kStage, i);
+        uint32_t stage = 0, ahead = kAhead * S::kStage;
         i32x4 fa[MT][2], fb[NT][2];
         for (uint32_t k = 0; k < steps; ++k) {
             // this stage has arrived in every wave, and nobody reads the one before any more
-            __builtin_amdgcn_sched_barrier(0);
-            asm volatile("s_waitcnt vmcnt(10)\n s_barrier" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-            fetch(ahead, k + 3);
+            arrive<(kAhead - 1) * (S::kLoadsA + S::kLoadsB)>();
+            fetch(ahead, k + kAhead);
             const uint32_t xa = pa + stage, xb = pb + stage;
-            if constexpr (BN == 64) read_fragments<0, 0>(fa, fb[0], fb[1], xa, xa ^ 64, xb, xb ^ 64);
-            else read_fragments6(fa, fb[0], xa, xa ^ 64, xb, xb ^ 64);
+            read_few<MT, NT>(fa, fb, xa, xa ^ 64, xb, xb ^ 64);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -466,11 +518,11 @@ __global__ __launch_bounds__(512, 2) void gemm_few(const GemmArgs g, const Epilo
                         acc.v[i][j] = T::mma(__builtin_bit_cast(typename T::Frag, fa[i][kk]),
                                              __builtin_bit_cast(typename T::Frag, fb[j][kk]), acc.v[i][j]);
             ahead = stage;
-            stage = stage == (kStages - 1) * kStage ? 0 : stage + kStage;
+            stage = stage == kAhead * S::kStage ? 0 : stage + S::kStage;
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * WM + wm, split, NoStaging{});
+    epi(acc, m_base + wm * MT * 16, n_base + wn * NT * 16, g, tm * S::WM + wm, split, NoStaging{});
 }
 
 // ---------------------------------------------------------------------------
@@ -509,14 +561,6 @@ __device__ __forceinline__ void read_pieces(i32x4 (&x0)[3], i32x4 (&x1)[3], i32x
           "n"(X_OFF + 17408), "n"(Y_OFF), "n"(Y_OFF + 8192), "n"(Y_OFF + 16384), "n"(Y_OFF + 1024), "n"(Y_OFF + 9216),
           "n"(Y_OFF + 17408)
         : "memory");
-}
-
-// All but the newest nine direct loads have arrived, in every wave.
-__device__ __forceinline__ void arrive9()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_waitcnt vmcnt(9)\n s_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
 }
 
 // A 256 x 128 tile of 16-bit values in the layout of pieces leaves in two
@@ -650,12 +694,11 @@ __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Ep
     const __amdgpu_buffer_rsrc_t ra0 = rows_from(g.a, g.lda, m_base, g.m), ra1 = rows_from(g.a, g.lda, m_base + 32, g.m);
     const __amdgpu_buffer_rsrc_t rb = rows_from(g.b, g.ldb, n_base, g.n);
     auto fetch = [&](__amdgpu_buffer_rsrc_t x, uint32_t to, uint32_t off, uint32_t step) {
-        typedef __attribute__((address_space(3))) void lds_void;
         const uint32_t v = step < steps ? off : kPastEnd, at = step * (kPieceDepth * kPieces * 2);
         char* p = lds + to + wave * 1024;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)p, 16, v, at, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)(p + 8192), 16, v, at + 64, 0, 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (lds_void*)(p + 16384), 16, v, at + 128, 0, 0);
+        load_to_lds(x, p, v, at);
+        load_to_lds(x, p + 8192, v, at + 64);
+        load_to_lds(x, p + 16384, v, at + 128);
     };
 
     Tile<4, 4> acc;
@@ -689,7 +732,7 @@ __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Ep
         fetch(ra1, kA1, off_a, 0);
         fetch(ra0, kStage, off_a, 1);
         fetch(rb, kStage + kB, off_b, 1);
-        arrive9();
+        arrive<9>();
         read_pieces<0, 0>(fa0[0], fa0[1], fa1[0], fa1[1], pa, pa);
         meet();  // the first quarter is read: step 0 loads it again
         if (wave >= 4) meet();
@@ -698,12 +741,12 @@ __global__ __launch_bounds__(512, 2) void gemm_pieces(const GemmArgs g, const Ep
             fetch(ra1, other + kA1, off_a, k + 1);
             fetch(ra0, stage, off_a, k + 2);
             read_pieces<0, 2048>(fb[0], fb[1], fb[2], fb[3], pb, pb);
-            arrive9();
+            arrive<9>();
             multiply(fa0, 0);
             meet();
             fetch(rb, stage + kB, off_b, k + 2);
             read_pieces<kA1, 0>(fa1[0], fa1[1], fa0[0], fa0[1], pa, pa_next);
-            arrive9();
+            arrive<9>();
             multiply(fa1, 2);
             meet();
             uint32_t t = pa; pa = pa_next; pa_next = t;
@@ -726,13 +769,29 @@ hipError_t launch_gemm_pieces(GemmArgs g, const Epilogue& epi, hipStream_t strea
     return hipGetLastError();
 }
 
-template <class T, int BN, class Epilogue>
-hipError_t launch_gemm_few(GemmArgs g, const Epilogue& epi, hipStream_t stream)
+// Rows of A a tile: small ones where the large ones would leave CUs idle.
+inline uint32_t few_tile_m(uint64_t m, uint64_t n, uint64_t splits, uint64_t tile_n)
 {
-    g.tiles_m = (g.m + kTileM - 1) / kTileM;
+    constexpr uint64_t kCUs = 256;
+    return (m + kTileM - 1) / kTileM * ((n + tile_n - 1) / tile_n) * splits < kCUs ? kFewM : kTileM;
+}
+
+template <class T, int BM, int BN, class Epilogue>
+hipError_t launch_few_tiles(GemmArgs g, const Epilogue& epi, hipStream_t stream)
+{
+    g.tiles_m = (g.m + BM - 1) / BM;
     g.tiles_n = (g.n + BN - 1) / BN;
-    hipLaunchKernelGGL((gemm_few<T, BN, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(512), 0, stream, g, epi);
+    constexpr int kThreads = FewShape<BM, BN>::kThreads;
+    hipLaunchKernelGGL((gemm_few<T, BM, BN, kThreads, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits),
+                       dim3(kThreads), 0, stream, g, epi);
     return hipGetLastError();
+}
+
+template <class T, int BN, class Epilogue>
+hipError_t launch_gemm_few(const GemmArgs& g, const Epilogue& epi, hipStream_t stream)
+{
+    return few_tile_m(g.m, g.n, g.splits, BN) == kFewM ? launch_few_tiles<T, kFewM, BN>(g, epi, stream)
+                                                       : launch_few_tiles<T, kTileM, BN>(g, epi, stream);
 }
 
 template <class T, class Epilogue>
