@@ -564,7 +564,8 @@ __device__ __forceinline__ void read_pieces(i32x4 (&x0)[3], i32x4 (&x1)[3], i32x
 }
 
 // A 256 x 128 tile of 16-bit values in the layout of pieces leaves in two
-// halves, each in whole rows.
+// halves, each in whole rows: the first and the last 32 of each wave's 64 rows
+// (or columns), so that all waves work on both.
 struct PieceStaging {
     static constexpr bool kOn = true;
     char* lds;
@@ -583,27 +584,27 @@ struct PieceStaging {
     {
         constexpr uint32_t kRow = 256 * 6 + 16;  // the 16 keep the rows of a write off each other's banks
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
-        for (uint32_t half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
             __syncthreads();
-            if (wn == half) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+            for (int jj = 0; jj < 2; ++jj) {
+                const int j = half * 2 + jj;
+                __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        char* row = lds + (j * 16 + (lane & 15)) * kRow;
-                        uint32_t p[4][3];
+                for (int i = 0; i < 4; ++i) {
+                    char* row = lds + (wn * 32 + jj * 16 + (lane & 15)) * kRow;
+                    uint32_t p[4][3];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) split(x.v[i][j][r], p[r]);
+                    for (int r = 0; r < 4; ++r) split(x.v[i][j][r], p[r]);
 #pragma unroll
-                        for (int k = 0; k < 3; ++k)
-                            *reinterpret_cast<u32x2*>(row + byte_of(wm * 64 + i * 16 + quad * 4, k)) =
-                                u32x2{p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16)};
-                    }
+                    for (int k = 0; k < 3; ++k)
+                        *reinterpret_cast<u32x2*>(row + byte_of(wm * 64 + i * 16 + quad * 4, k)) =
+                            u32x2{p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16)};
                 }
             }
             __syncthreads();
-            copy_rows<96, kRow>(out, ld, n_base + half * 64, 64, rows, m_base * 3, cols * 3);
+            copy_rows<96, kRow>(out, ld, n_base + half * 32, 64, rows, m_base * 3, cols * 3);
         }
     }
 
@@ -614,33 +615,33 @@ struct PieceStaging {
     {
         constexpr uint32_t kRow = 128 * 6 + 16;
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4, odd = lane & 1;
-        for (uint32_t half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
             __syncthreads();
-            if (wm >> 1 == half) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    __builtin_amdgcn_sched_barrier(0);
+            for (int j = 0; j < 4; ++j) {
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        char* row = lds + ((wm & 1) * 64 + i * 16 + quad * 4 + odd * 2) * kRow;
-                        uint32_t p[4][3];
+                for (int ii = 0; ii < 2; ++ii) {
+                    const int i = half * 2 + ii;
+                    char* row = lds + (wm * 32 + ii * 16 + quad * 4 + odd * 2) * kRow;
+                    uint32_t p[4][3];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) split(x.v[i][j][r] * factor[j], p[r]);
+                    for (int r = 0; r < 4; ++r) split(x.v[i][j][r] * factor[j], p[r]);
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const uint32_t p01 = p[0][k] | (p[1][k] << 16), p23 = p[2][k] | (p[3][k] << 16);
-                            const uint32_t give = odd ? p01 : p23, keep = odd ? p23 : p01;
-                            const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);  // lane ^ 1
-                            const uint32_t lo = odd ? got : keep, hi = odd ? keep : got;
-                            const uint32_t at = byte_of(wn * 64 + j * 16 + (lane & 14), k);
-                            *reinterpret_cast<uint32_t*>(row + at) = __builtin_amdgcn_perm(hi, lo, 0x05040100);
-                            *reinterpret_cast<uint32_t*>(row + kRow + at) = __builtin_amdgcn_perm(hi, lo, 0x07060302);
-                        }
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t p01 = p[0][k] | (p[1][k] << 16), p23 = p[2][k] | (p[3][k] << 16);
+                        const uint32_t give = odd ? p01 : p23, keep = odd ? p23 : p01;
+                        const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+                        const uint32_t lo = odd ? got : keep, hi = odd ? keep : got;
+                        const uint32_t at = byte_of(wn * 64 + j * 16 + (lane & 14), k);
+                        *reinterpret_cast<uint32_t*>(row + at) = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+                        *reinterpret_cast<uint32_t*>(row + kRow + at) = __builtin_amdgcn_perm(hi, lo, 0x07060302);
                     }
                 }
             }
             __syncthreads();
-            copy_rows<48, kRow>(out, ld, m_base + half * 128, 128, rows, n_base * 3, cols * 3);
+            copy_rows<48, kRow>(out, ld, m_base + half * 32, 128, rows, n_base * 3, cols * 3);
         }
     }
 
@@ -653,8 +654,9 @@ private:
         for (uint32_t i = threadIdx.x; i < high * CHUNKS; i += 512) {
             const uint32_t r = i / CHUNKS, c = i % CHUNKS;
             const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * ROW + c * 16);
-            if (row0 + r < rows && col0 + c * 8 < cols)
-                *reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(row0 + r) * ld + col0 + c * 8) = v;
+            const uint32_t to = row0 + r / 32 * 64 + r % 32;
+            if (to < rows && col0 + c * 8 < cols)
+                *reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(to) * ld + col0 + c * 8) = v;
         }
     }
 };
