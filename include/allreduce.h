@@ -349,8 +349,8 @@ ar_result_t ar_clip_grads(ar_comm_t comm, int ntensors, const void* const sendbu
                           float* norm_out, hipStream_t stream);
 
 /* ar_all_reduce_multi (SUM or AVG; other ops UNSUPPORTED) and ar_clip_grads of
- * its replicated result as one call, bit for bit, in fewer passes: the
- * reduction writes one copy and its norm, the clip reads that copy and writes
+ * its replicated result as one call (the same but for the order in which the
+ * norm's fp64 squares are summed), in fewer passes: the reduction writes one copy and its norm, the clip reads that copy and writes
  * every rank's: 2(N+1)S bytes where the two calls move (3N+2)S. In place per
  * tensor and rank is allowed. */
 ar_result_t ar_all_reduce_clip(ar_comm_t comm, int ntensors, const void* const sendbufs[], void* const recvbufs[],
@@ -391,8 +391,12 @@ size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, siz
  *   losses[t] = lse[t] - z[t][targets[t]].
  * A token whose target is ignore_index or outside [0, vocab) is ignored: its
  * loss is 0 (its lse is still given). Products of fp16 and bf16 are summed in
- * fp32; fp32 products are made of bf16 pieces that hold all 24 bits. losses
- * and lse are fp32. */
+ * fp32; fp32 products are exact to 2^-24 (fp32 matrix instructions up to 64
+ * tokens, else bf16 pieces that hold all 24 bits). losses and lse are fp32.
+ * ntokens and width are below 2^24, of fp32 below 2^20. Operands whose rows are
+ * on 16-byte boundaries and whole multiples of 16 bytes long are read as they
+ * lie (fp32 only up to 64 tokens); others are first laid out in the workspace,
+ * at most 1 GiB of the weight at a time. */
 ar_result_t ar_linear_cross_entropy(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
                                     ar_index_t index, float* losses, float* lse, size_t ntokens, size_t vocab,
                                     size_t width, size_t ld_hidden, size_t ld_weight, long long ignore_index,

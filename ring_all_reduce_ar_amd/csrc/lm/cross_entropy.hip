@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kJoinBlock) void join_stats(const Stats* stats, uin
 // backward
 // ---------------------------------------------------------------------------
 struct RowScale {
-    float top;  // the largest |g| of the rows that count, 1 if there is none
+    float top;  // the largest |g| of the rows that count, at least the least normal number
 };
 
 __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices targets, int64_t ignore, uint64_t vocab,
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices target
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 16; ++w) top = fmaxf(top, waves[w]);
-        out->top = top > 0.0f ? top : 1.0f;
+        out->top = fmaxf(top, 0x1p-126f);  // whose reciprocal is finite
     }
 }
 

@@ -186,3 +186,24 @@ def test_binding_takes_row_pitches_from_tensors():
         ar._index(None, x)
     with pytest.raises(ValueError):
         ar.ar_grad_norm(host_comm(), [at(0)], [4], at(1), "f32", layout="mirrored", stream=0)
+
+
+def test_depths_that_no_buffer_spans():
+    """fp32 widths and tokens below 2^20, 16-bit ones below 2^24."""
+    size = ar.ar_linear_cross_entropy_workspace_bytes
+    for dtype, most in (("f32", 1 << 20), ("bf16", 1 << 24)):
+        assert size(64, 300, most - 1, dtype) > 0 and size(most - 1, 300, 8, dtype) > 0
+        for bad in ((64, 300, most), (most, 300, 8)):
+            with pytest.raises(ValueError):
+                size(*bad, dtype)
+
+
+def test_lists_of_addresses():
+    """Addresses alone, tensors among them, and what is neither."""
+    x = torch.zeros(4)
+    assert list(ar._ptrs([1, 2, (1 << 64) - 8])) == [1, 2, (1 << 64) - 8]
+    assert list(ar._ptrs([16, x])) == [16, x.data_ptr()] and list(ar._ptrs((x, 16))) == [x.data_ptr(), 16]
+    assert list(ar._ptrs([])) == []
+    for bad in ([1, "2"], [1, 2.0], [1, None], ["1"]):
+        with pytest.raises(TypeError):
+            ar._ptrs(bad)
