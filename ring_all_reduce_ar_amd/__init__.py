@@ -191,10 +191,13 @@ def _ptr_pair(sendbufs, recvbufs):
     return s, (s if recvbufs is sendbufs else _ptrs(recvbufs))
 
 
+# torch.cuda.current_stream(device).cuda_stream without the Stream object around it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device: int):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(device) if _current_stream else torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -410,11 +413,18 @@ def _rows(buf, ld: int):
         return buf, ld
     if buf is None:
         return None, ld
-    if ld == 0 and buf.dim() == 2:
-        if buf.shape[1] > 1 and buf.stride(1) != 1:
-            raise ValueError("the rows of a matrix must be contiguous")
-        return buf.data_ptr(), buf.stride(0) if buf.shape[0] > 1 else 0
-    return buf.data_ptr() if ld else _addr(buf), ld
+    if ld:
+        return buf.data_ptr(), ld
+    pitch, shape = buf.stride(), buf.shape
+    if len(shape) != 2:
+        return _addr(buf), 0
+    if pitch[1] != 1 and shape[1] > 1:
+        raise ValueError("the rows of a matrix must be contiguous")
+    if shape[0] <= 1:
+        return buf.data_ptr(), 0
+    if pitch[0] < shape[1]:  # as an expanded tensor's
+        raise ValueError("the rows of a matrix must not overlap")
+    return buf.data_ptr(), pitch[0]
 
 
 def ar_embedding(comm, weight, tokens, out, ntokens: int, rows: int, width: int, dtype, scale: float = 1.0,

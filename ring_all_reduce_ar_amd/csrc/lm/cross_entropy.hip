@@ -15,7 +15,9 @@
 // six bf16 products give the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the
 // fp32 matrix instructions end at 0.16. With fewer tokens the time is that of
 // reading the weight, which then stays as it is.
+#include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "gemm.h"
 
@@ -383,22 +385,52 @@ private:
     }
 };
 
-// One split's sums of the hidden gradient: acc[split][t][h], over all pieces.
-struct HiddenEpilogue {
+// Calls put(row, column, value) for a tile's results in C[row][column].
+template <int MT, int NT, class Put>
+__device__ __forceinline__ void each_result(const Tile<MT, NT>& c, uint32_t m0, uint32_t n0, const GemmArgs& g, Put put)
+{
+    const int lane = threadIdx.x & 63, quad = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t row = m0 + quad * 4 + 16 * i + r;
+            if (row >= g.m) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t col = n0 + j * 16 + (lane & 15);
+                if (col < g.n) put(row, col, c.v[i][j][r]);
+            }
+        }
+}
+
+// One split's sums of a gradient: acc[split][row][h]; the hidden gradient's go
+// over all pieces of the vocabulary. The product's rows are the columns h, or
+// (BY_ROW) the gradient's rows.
+template <bool BY_ROW>
+struct SumEpilogue {
     float* acc;
-    uint64_t width;
+    uint64_t rows, width;
     int add;
 
     template <int MT, int NT, class S>
     __device__ __forceinline__ void operator()(Tile<MT, NT>& c, uint32_t m0, uint32_t n0, const GemmArgs& g, uint32_t,
                                                uint32_t split, const S&) const
     {
+        float* part = acc + split * rows * width;
+        if constexpr (BY_ROW) {
+            each_result(c, m0, n0, g, [&](uint32_t t, uint32_t h, float x) {
+                float* at = part + t * width + h;
+                *at = add ? *at + x : x;
+            });
+            return;
+        }
         const int lane = threadIdx.x & 63, quad = lane >> 4;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const uint32_t t = n0 + j * 16 + (lane & 15);
             if (t >= g.n) continue;
-            float* row = acc + (static_cast<uint64_t>(split) * g.n + t) * width;
+            float* row = part + t * width;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 const uint32_t h = m0 + quad * 4 + 16 * i;
@@ -417,21 +449,24 @@ struct HiddenEpilogue {
     }
 };
 
-// grad_hidden[t][h] = round(g[t] 2^-14 * the splits' sum), 0 for ignored
-// tokens. U elements a thread, `lanes` threads a row.
-template <class F, int U>
-__global__ __launch_bounds__(kBlock) void finish_hidden(const float* acc, int splits, const float* g, Indices targets,
-                                                        int64_t ignore, uint64_t vocab, uint64_t ntokens,
-                                                        uint64_t width, void* out, uint64_t ld, int lanes)
+// out[row][h] = round(scale 2^-14 * the splits' sum), U elements a thread, `lanes`
+// threads a row. The hidden gradient's scale is g[t], and 0 for ignored tokens;
+// the weight's is max |g|.
+template <class F, int U, bool WEIGHT>
+__global__ __launch_bounds__(kBlock) void finish_sum(const float* acc, int splits, const float* g, Indices targets,
+                                                     int64_t ignore, uint64_t vocab, const RowScale* top, uint64_t rows,
+                                                     uint64_t width, void* out, uint64_t ld, int lanes)
 {
-    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
-    if (t >= ntokens) return;
-    const bool on = load_target(targets, t, ignore, vocab) >= 0;
-    const float scale = on ? g[t] * (1.0f / kDScale) : 0.0f;
-    for (uint64_t c = (threadIdx.x & (lanes - 1)) * static_cast<uint64_t>(U); c < width; c += lanes * static_cast<uint64_t>(U)) {
+    const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
+    if (row >= rows) return;
+    const bool on = WEIGHT || load_target(targets, row, ignore, vocab) >= 0;
+    const float scale = (WEIGHT ? top->top : on ? g[row] : 0.0f) * (1.0f / kDScale);
+    for (uint64_t c = (threadIdx.x & (lanes - 1)) * static_cast<uint64_t>(U); c < width;
+         c += lanes * static_cast<uint64_t>(U)) {
         float s[U] = {};
+#pragma unroll 8
         for (int k = 0; k < splits; ++k) {
-            const float* from = acc + (static_cast<uint64_t>(k) * ntokens + t) * width + c;
+            const float* from = acc + (static_cast<uint64_t>(k) * rows + row) * width + c;
             if constexpr (U == 1) {
                 s[0] += from[0];
             } else {
@@ -445,13 +480,14 @@ __global__ __launch_bounds__(kBlock) void finish_hidden(const float* acc, int sp
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) s[u] = on ? s[u] * scale : 0.0f;
-        if constexpr (U == 1) F::st(out, t * ld + c, s[0]);
-        else stv_at<false>(out, (t * ld + c) * (16 / F::kEpv), F::pack(s));
+        if constexpr (U == 1) F::st(out, row * ld + c, s[0]);
+        else stv_at<false>(out, (row * ld + c) * (16 / F::kEpv), F::pack(s));
     }
 }
 
-// grad_weight[v][h] = round(max |g| 2^-14 * sum).
-template <class F, class T>
+// grad_weight[v][h] = round(max |g| 2^-14 * sum). The product's rows are the
+// columns h, or (BY_VOCAB) the vocabulary's.
+template <class F, class T, bool BY_VOCAB>
 struct WeightEpilogue {
     void* out;
     uint64_t ld;
@@ -464,6 +500,10 @@ struct WeightEpilogue {
     {
         const int lane = threadIdx.x & 63, quad = lane >> 4;
         const float s = scale->top * (1.0f / kDScale);
+        if constexpr (BY_VOCAB) {
+            each_result(c, m0, n0, g, [&](uint32_t v, uint32_t h, float x) { F::st(out, v * ld + h, x * s); });
+            return;
+        }
         if constexpr (std::is_same<S, Staging>::value) {
             if (vec == 8 && g.m % 8 == 0) {
 #pragma unroll
@@ -558,6 +598,22 @@ hipError_t product(const GemmArgs& g, int tile_n, const Epilogue& epi, hipStream
     }
 }
 
+GemmArgs swapped(GemmArgs g)
+{
+    std::swap(g.a, g.b);
+    std::swap(g.lda, g.ldb);
+    std::swap(g.m, g.n);
+    return g;
+}
+
+// Whether the gradients' products have the model's columns as rows of B rather
+// than of A: tiles of pieces are 256 x 128, so that a width of 770 is padded to
+// 1024 as rows of A and to 896 as rows of B. MEASURED
+bool columns_in_b(uint64_t width, uint64_t other)
+{
+    return round_up(width, kPiecesN) * round_up(other, kTileM) < round_up(width, kTileM) * round_up(other, kPiecesN);
+}
+
 // Rows of statistics that the logits of `rows` vocabulary rows leave: one for
 // each wave along a tile.
 uint64_t stat_rows_of(uint64_t rows, uint64_t ntokens, int tile_n)
@@ -616,6 +672,33 @@ struct Call {
         g.k = g.k_all = static_cast<uint32_t>(p.pack_hidden && p.pack_weight ? p.k_pad : a.width);
         g.splits = 1;
         return g;
+    }
+
+    // A gradient's product, whose rows of A are the model's columns and which has
+    // `other` rows of B, or the other way round.
+    template <class ByColumn, class ByRow>
+    hipError_t in_order(const GemmArgs& g, uint64_t other, int tile_n, const ByColumn& by_column,
+                        const ByRow& by_row) const
+    {
+        if constexpr (PARTS == kPieces) {
+            if (columns_in_b(a.width, other)) return product<T, PARTS>(swapped(g), tile_n, by_row, s);
+        }
+        return product<T, PARTS>(g, tile_n, by_column, s);
+    }
+
+    template <bool WEIGHT>
+    hipError_t finish(const float* sums, int splits, const RowScale* scale, uint64_t rows, void* out, uint64_t ld) const
+    {
+        // (few results take a thread each: 6 x 256 of 128 splits in 8 us rather than 37)
+        const bool vec = a.width % F::kEpv == 0 && ld % F::kEpv == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                         rows * a.width >= (1u << 18);
+        const int lanes = lanes_for(vec ? a.width / F::kEpv : a.width);
+        auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid_for(rows, lanes), dim3(kBlock), 0, s, sums, splits, a.grad_losses, a.targets,
+                               a.ignore_index, a.vocab, scale, rows, a.width, out, ld, lanes);
+            return hipGetLastError();
+        };
+        return vec ? launch(finish_sum<F, F::kEpv, WEIGHT>) : launch(finish_sum<F, 1, WEIGHT>);
     }
 
     hipError_t forward() const
@@ -683,8 +766,9 @@ struct Call {
                 g.k_all = static_cast<uint32_t>(pad);
                 g.splits = static_cast<uint32_t>(p.splits);
                 g.k = static_cast<uint32_t>(round_up((pad + p.splits - 1) / p.splits, kTileK));
-                const HiddenEpilogue he{acc, a.width, v0 > 0};
-                if ((e = product<T, PARTS>(g, p.tile_n, he, s)) != hipSuccess) return e;
+                const SumEpilogue<false> by_column{acc, a.ntokens, a.width, v0 > 0};
+                const SumEpilogue<true> by_token{acc, a.ntokens, a.width, v0 > 0};
+                if ((e = in_order(g, a.ntokens, p.tile_n, by_column, by_token)) != hipSuccess) return e;
             }
             if (dt) {
                 GemmArgs g{};
@@ -693,54 +777,87 @@ struct Call {
                 g.lda = g.ldb = p.t_pad * OB;
                 g.m = static_cast<uint32_t>(a.width);
                 g.n = static_cast<uint32_t>(rows);
-                g.k = g.k_all = static_cast<uint32_t>(p.t_pad);
-                g.splits = 1;
+                g.k_all = static_cast<uint32_t>(p.t_pad);
+                g.splits = static_cast<uint32_t>(p.weight_splits);
+                g.k = static_cast<uint32_t>(round_up((p.t_pad + p.weight_splits - 1) / p.weight_splits, kTileK));
                 char* out = static_cast<char*>(a.grad_weight) + v0 * a.ld_grad_weight * EB;
-                const uintptr_t mis = reinterpret_cast<uintptr_t>(out) | a.ld_grad_weight * EB;
-                const int vec = EB == 2 && mis % 16 == 0 ? 8 : mis % (4 * EB) == 0 ? 4 : 1;
-                const WeightEpilogue<F, T> we{out, a.ld_grad_weight, scale, vec};
-                if ((e = product<T, PARTS>(g, 256, we, s)) != hipSuccess) return e;
+                if (p.weight_splits > 1) {
+                    float* sums = reinterpret_cast<float*>(ws + p.grad_weight_acc);
+                    const SumEpilogue<false> by_column{sums, rows, a.width, 0};
+                    const SumEpilogue<true> by_vocab{sums, rows, a.width, 0};
+                    if ((e = in_order(g, rows, 256, by_column, by_vocab)) != hipSuccess) return e;
+                    if ((e = finish<true>(sums, p.weight_splits, scale, rows, out, a.ld_grad_weight)) != hipSuccess) return e;
+                } else {
+                    const uintptr_t mis = reinterpret_cast<uintptr_t>(out) | a.ld_grad_weight * EB;
+                    const int vec = EB == 2 && mis % 16 == 0 ? 8 : mis % (4 * EB) == 0 ? 4 : 1;
+                    const WeightEpilogue<F, T, false> by_column{out, a.ld_grad_weight, scale, vec};
+                    const WeightEpilogue<F, T, true> by_vocab{out, a.ld_grad_weight, scale, vec};
+                    if ((e = in_order(g, rows, 256, by_column, by_vocab)) != hipSuccess) return e;
+                }
             }
         }
-        if (d) {
-            const bool vec = a.width % F::kEpv == 0 && a.width % 4 == 0 && a.ld_grad_hidden % F::kEpv == 0 &&
-                             reinterpret_cast<uintptr_t>(a.grad_hidden) % 16 == 0;
-            const int lanes = lanes_for(vec ? a.width / F::kEpv : a.width);
-            auto finish = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, grid_for(a.ntokens, lanes), dim3(kBlock), 0, s, acc, p.splits, a.grad_losses,
-                                   a.targets, a.ignore_index, a.vocab, a.ntokens, a.width, a.grad_hidden,
-                                   a.ld_grad_hidden, lanes);
-                return hipGetLastError();
-            };
-            e = vec ? finish(finish_hidden<F, F::kEpv>) : finish(finish_hidden<F, 1>);
-        }
+        if (d) e = finish<false>(acc, p.splits, scale, a.ntokens, a.grad_hidden, a.ld_grad_hidden);
         return e;
     }
 };
 
-// What a call's products cost with pieces of `piece` rows, in depth steps of
-// the busiest CU: a product takes whole rounds of one tile a CU. `splits`
-// gets the best number of parts for the hidden gradient's sum.
+// What a call's products cost with pieces of `rows` rows, in depth steps of the
+// busiest CU: a product takes whole rounds of one tile a CU.
 constexpr uint64_t kCUs = 256;
-double piece_cost(uint64_t rows, uint64_t ntokens, uint64_t width, uint64_t tile_n, uint64_t tile_w, uint64_t step,
-                  int* splits)
+struct Shape {
+    uint64_t ntokens, width, tile_n, tile_w, step;  // tile_w: columns of the weight gradient's tiles
+    bool pieces;
+};
+
+uint64_t up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+// Tiles of a gradient's product with `other` rows.
+uint64_t gradient_tiles(const Shape& x, uint64_t other, uint64_t tile)
 {
-    auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
-    const uint64_t tv = up(rows, kTileM), tn = up(ntokens, tile_n), tw = up(width, kTileM);
-    // each round also costs about four steps to start and to end in
-    double cost = static_cast<double>(up(tv * tn, kCUs) * (up(width, step) + 8)) +
-                  static_cast<double>(up(up(rows, tile_w) * tw, kCUs) * (up(ntokens, step) + 4));
+    return x.pieces && columns_in_b(x.width, other) ? up(x.width, kPiecesN) * up(other, kTileM)
+                                                    : up(x.width, kTileM) * up(other, tile);
+}
+
+// The best number of parts for a sum over `depth` with so many tiles, and its
+// cost. A round costs about eight steps to start and to end in; parts are
+// written and read again, about two steps each; `join` is the cost of a launch
+// that only a split sum needs.
+double split_cost(uint64_t tiles, uint64_t depth, uint64_t step, double join, int* splits)
+{
     double best = 0;
-    for (int k = 1; k <= 64; k *= 2) {
-        if (k > 1 && rows / k < 512) break;
-        // a part of the sum is written and read again: about a step for each of a tile's
-        const double c = static_cast<double>(up(tw * tn * k, kCUs) * (up(up(rows, step), k) + 8)) + 2.0 * (k - 1);
-        if (k == 1 || c < best) {
+    for (uint64_t rounds = 0; rounds <= 2; ++rounds) {  // unsplit, or parts that fill one round or two
+        uint64_t k = 1;
+        if (rounds) {
+            k = std::min({rounds * kCUs / std::max<uint64_t>(tiles, 1), uint64_t(64), depth / 128});
+            if (k < 2) continue;
+        }
+        const double c = static_cast<double>(up(tiles * k, kCUs) * (up(up(depth, step), k) + 8)) +
+                         (k > 1 ? 2.0 * k + join : 0.0);
+        if (best == 0 || c < best) {
             best = c;
-            *splits = k;
+            *splits = static_cast<int>(k);
         }
     }
-    return cost + best + 24;  // four launches
+    return best;
+}
+
+double piece_cost(const Shape& x, uint64_t rows, int* splits, int* weight_splits)
+{
+    return static_cast<double>(up(up(rows, kTileM) * up(x.ntokens, x.tile_n), kCUs) * (up(x.width, x.step) + 8)) +
+           split_cost(gradient_tiles(x, x.ntokens, x.tile_n), rows, x.step, 0, splits) +
+           split_cost(gradient_tiles(x, rows, x.tile_w), x.ntokens, x.step, 8, weight_splits) + 24;  // four launches
+}
+
+// Whether tiles of 64 x 64 (a few hundred of them) end sooner than the few
+// large ones of the logits: a step of a 64 x 64 tile takes about 0.35 us, of
+// fp32 0.45, where a step of a 256 x 256 tile takes 0.85 us and of 256 x 128
+// in pieces 1.28.
+bool small_tiles(uint64_t ntokens, uint64_t vocab, uint64_t width, bool f32, bool backward)
+{
+    if (ntokens <= 64) return true;
+    auto tiles = [](uint64_t m, uint64_t n) { return up(m, 64) * up(n, 64); };
+    if (tiles(vocab, ntokens) > 2 * kCUs) return false;
+    return !f32 || !backward || (tiles(width, ntokens) <= 2 * kCUs && tiles(width, vocab) <= 2 * kCUs);
 }
 
 }  // namespace
@@ -749,8 +866,9 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
 {
     CrossEntropyPlan p{};
     const bool f32 = dtype == AR_FLOAT32;
-    p.pieces = f32 && ntokens > 64;
-    p.tile_n = ntokens <= 16 ? 16 : ntokens <= 64 ? 64 : f32 ? kPiecesN : 256;
+    const bool small = small_tiles(ntokens, vocab, width, f32, backward);
+    p.pieces = f32 && !small;
+    p.tile_n = ntokens <= 16 ? 16 : small ? 64 : f32 ? kPiecesN : 256;
     const uint64_t ob = p.pieces ? kPieces * 2 : f32 ? 4 : 2, step = f32 ? 32 : kTileK;
     p.k_pad = round_up(width, step);
     p.t_pad = round_up(ntokens, p.tile_n == 16 ? 16 : kTileK);  // the tiles cover it: they write its zeros
@@ -763,7 +881,7 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     uint64_t most = kPieceBytes / (row_bytes * kTileM);
     if (most > 4096) most = 4096;  // the transposed piece's rows stay within a buffer's 2^31 bytes
     most = most < 1 ? 1 : most > whole ? whole : most;
-    p.splits = 1;
+    p.splits = p.weight_splits = 1;
     if (!backward) {
         const uint64_t pieces = (whole + most - 1) / most;
         p.piece = (whole + pieces - 1) / pieces * kTileM;
@@ -771,17 +889,19 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         // From half the largest size on, the one whose tiles fill the CUs best.
         // 8192 x 131072 x 4096: pieces of 16384 rows end in full rounds, of
         // 13312 the weight gradient's 832 tiles take four rounds for 3.25.
+        const Shape shape{ntokens, width, static_cast<uint64_t>(p.tile_n), tile_w, step, p.pieces};
         double best = 0;
         const uint64_t stride = most / 64 + 1;
         for (uint64_t m = most; m >= (most + 1) / 2 && m >= 1; m = m > stride ? m - stride : 0) {
             const uint64_t rows = m * kTileM, full = vocab / rows, rest = vocab - full * rows;
-            int splits = 1, unused;
-            double c = piece_cost(full ? rows : rest, ntokens, width, p.tile_n, tile_w, step, &splits) * (full ? full : 1);
-            if (full && rest) c += piece_cost(rest, ntokens, width, p.tile_n, tile_w, step, &unused);
+            int splits = 1, weight_splits = 1, unused;
+            double c = piece_cost(shape, full ? rows : rest, &splits, &weight_splits) * (full ? full : 1);
+            if (full && rest) c += piece_cost(shape, rest, &unused, &unused);
             if (best == 0 || c < best) {
                 best = c;
                 p.piece = rows;
                 p.splits = splits;
+                p.weight_splits = weight_splits;
             }
         }
     }
@@ -808,6 +928,7 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         p.weight_t = take(width * p.piece * ob);
         p.hidden_t = take(width * p.t_pad * ob);
         p.grad_hidden_acc = take(static_cast<uint64_t>(p.splits) * ntokens * width * 4);
+        if (p.weight_splits > 1) p.grad_weight_acc = take(static_cast<uint64_t>(p.weight_splits) * p.piece * width * 4);
         p.row_scale = take(sizeof(RowScale));
     }
     p.bytes = at;

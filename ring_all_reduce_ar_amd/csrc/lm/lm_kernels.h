@@ -134,9 +134,10 @@ struct CrossEntropyPlan {
     bool pack_hidden, pack_weight;
     int tile_n;            // token tile of the logits' product
     int splits;            // parts of the vocabulary axis in the hidden gradient's product
+    int weight_splits;     // parts of the token axis in the weight gradient's
     uint64_t stat_rows;    // rows of partial softmax statistics
     // offsets
-    uint64_t hidden, weight, stats, target_logit, d, dt, weight_t, hidden_t, grad_hidden_acc, row_scale, bytes;
+    uint64_t hidden, weight, stats, target_logit, d, dt, weight_t, hidden_t, grad_hidden_acc, grad_weight_acc, row_scale, bytes;
 };
 CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward);
 

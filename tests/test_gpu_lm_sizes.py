@@ -162,3 +162,11 @@ def test_clip_around_the_number_of_partials(comms, total):  # noqa: F811
             ar.ar_all_reduce_clip(comm, [[x]], [[y]], [total], 1.0, out, "f32")
         assert abs(float(out) - ref) <= ref * (U32 + 1e-12)
         close(y, x.double() / (ref + 1e-6), clip_bound(x.double() / (ref + 1e-6), "f32"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,vocab,width", [(4200, 300, 72), (2500, 700, 130), (6, 70_000, 40), (700, 6000, 136)])
+def test_loss_with_split_sums(comms, dtype, n, vocab, width):  # noqa: F811
+    """Gradients whose few tiles are summed in parts, along the tokens or the
+    vocabulary, in either order of the operands."""
+    check_loss(comms, n, vocab, width, dtype, 58)

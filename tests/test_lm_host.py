@@ -207,3 +207,14 @@ def test_lists_of_addresses():
     for bad in ([1, "2"], [1, 2.0], [1, None], ["1"]):
         with pytest.raises(TypeError):
             ar._ptrs(bad)
+
+
+def test_rows_of_matrices():
+    """A tensor's own pitch; rows that overlap or have gaps inside are refused."""
+    x = torch.zeros(6, 8)
+    assert ar._rows(x, 0) == (x.data_ptr(), 8) and ar._rows(x[:, 2:5], 0) == (x.data_ptr() + 8, 8)
+    assert ar._rows(x[1:2], 0) == (x.data_ptr() + 32, 0) and ar._rows(x[::2], 0) == (x.data_ptr(), 16)
+    assert ar._rows(x, 12) == (x.data_ptr(), 12) and ar._rows(64, 3) == (64, 3) and ar._rows(None, 0) == (None, 0)
+    for bad in (x[:, ::2], x.t(), torch.zeros(1, 8).expand(6, 8), x.as_strided((4, 8), (4, 1))):
+        with pytest.raises(ValueError):
+            ar._rows(bad, 0)
