@@ -608,7 +608,8 @@ GemmArgs swapped(GemmArgs g)
 
 // Whether the gradients' products have the model's columns as rows of B rather
 // than of A: tiles of pieces are 256 x 128, so that a width of 770 is padded to
-// 1024 as rows of A and to 896 as rows of B. MEASURED
+// 1024 as rows of A and to 896 as rows of B (1021 x 32003: 354 -> 293 and 280 ->
+// 243 us).
 bool columns_in_b(uint64_t width, uint64_t other)
 {
     return round_up(width, kPiecesN) * round_up(other, kTileM) < round_up(width, kTileM) * round_up(other, kPiecesN);
