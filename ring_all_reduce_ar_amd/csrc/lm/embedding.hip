@@ -7,6 +7,8 @@
 // contributions lie side by side in token order: each row is summed in fp32 in
 // one fixed order and written once, with no float atomics, and the rows that no
 // token meets are written as zeros in the same launch.
+#include <algorithm>
+
 #include "../kernels_impl.h"
 #include "lm_kernels.h"
 
@@ -82,25 +84,28 @@ hipError_t lookup_launch(const LookupArgs& a, bool vec, hipStream_t s)
 // ---------------------------------------------------------------------------
 // zeros for the rows that no token meets
 // ---------------------------------------------------------------------------
-// Rows [r0, r1) without a presence flag, by `blocks` workgroups of THREADS
+// Rows [r0, r1) for which `met` is false, by `blocks` workgroups of THREADS
 // threads, of which this is the `block`-th; `lanes` (a power of two) threads a
-// row, kFillRows neighbouring rows one after the other. Any alignment: 16-byte stores from the row's first boundary on.
+// row, kFillRows neighbouring rows one after the other. Any alignment: 16-byte
+// stores from the row's first boundary on. Beyond the last-level cache (NT)
+// non-temporal stores leave it to the gradient's rows: 131072 x 4096 bf16 with
+// 32768 tokens 289 us, with cached stores 305.
 constexpr int kFillRows = 4;
-template <class G, bool NT, int THREADS>
+template <class G, bool NT, int THREADS, class Met>
 __device__ __forceinline__ void fill_rows(const LookupGradArgs& a, uint64_t r0, uint64_t r1, uint32_t block,
-                                          uint32_t blocks, uint32_t lanes)
+                                          uint32_t blocks, uint32_t lanes, Met met)
 {
     constexpr uint32_t EB = 16 / G::kEpv;
     const uint32_t lane = threadIdx.x & (lanes - 1), per = THREADS / lanes;
-    constexpr int B = kFillRows;  // rows whose flags are loaded together
+    constexpr int B = kFillRows;
     for (uint64_t r = r0 + static_cast<uint64_t>(block) * per * B + threadIdx.x / lanes; r < r1;
          r += static_cast<uint64_t>(blocks) * per * B) {
-        uint8_t met[B];
+        bool skip[B];
 #pragma unroll
-        for (int k = 0; k < B; ++k) met[k] = r + k * per < r1 ? a.present[r + k * per] : 1;
+        for (int k = 0; k < B; ++k) skip[k] = r + k * per >= r1 || met(r + k * per);
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            if (met[k]) continue;
+            if (skip[k]) continue;
             char* row = static_cast<char*>(a.grad_weight) + (r + k * per) * a.ld_grad_weight * EB;
             const uint64_t bytes = a.width * EB, to_line = -reinterpret_cast<uintptr_t>(row) & 15;
             const uint64_t head = to_line < bytes ? to_line : bytes, body = (bytes - head) / 16, tail = head + body * 16;
@@ -153,7 +158,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_move(const LookupGradArgs a
     __shared__ uint32_t mine[W][kSortBins];
     __shared__ uint32_t sums[kSortBins / 64];
     if (blockIdx.x >= blocks) {
-        fill_rows<G, NT, kSortThreads>(a, r0, r1, blockIdx.x - blocks, gridDim.x - blocks, lanes);
+        fill_rows<G, NT, kSortThreads>(a, r0, r1, blockIdx.x - blocks, gridDim.x - blocks, lanes,
+                                       [&](uint64_t r) { return a.present[r] != 0; });
         return;
     }
     const int nb = 1 << bits, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, src = pass & 1;
@@ -231,6 +237,72 @@ __global__ __launch_bounds__(kSortThreads) void sort_move(const LookupGradArgs a
     }
 }
 
+// The same for at most kSortThreads tokens, one a thread: all passes in one
+// workgroup's LDS. 7 tokens into 2996 x 32: 22 us a call with the launches of the
+// general sort, 12 with this one and grad_small; 836 into 30274 x 32: 37 and 30.
+__global__ __launch_bounds__(kSortThreads) void sort_small(const LookupGradArgs a, int passes, int bits)
+{
+    constexpr int W = kSortThreads / 64;
+    __shared__ uint32_t mine[W][kSortBins];
+    __shared__ uint32_t base[kSortBins];
+    __shared__ uint32_t sums[kSortBins / 64];
+    __shared__ uint32_t keys[kSortThreads], places[kSortThreads];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, nb = 1 << bits;
+    const bool ok = static_cast<uint64_t>(t) < a.ntokens;
+    uint32_t key = ok ? static_cast<uint32_t>(row_of(a.tokens, t, a.first_row, a.rows)) : 0, pos = t;
+    for (int pass = 0; pass < passes; ++pass) {
+        for (int i = t; i < W * kSortBins; i += kSortThreads) (&mine[0][0])[i] = 0;
+        __syncthreads();
+        const uint32_t digit = (key >> (pass * bits)) & (nb - 1);
+        uint64_t same = __ballot(ok);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t m = __ballot((digit >> b) & 1);
+            same &= ((digit >> b) & 1) ? m : ~m;
+        }
+        const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
+        if (ok && rank == 0) mine[wave][digit] = __popcll(same);
+        __syncthreads();
+        uint32_t all = 0, upto = 0;
+        if (t < kSortBins) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const uint32_t c = mine[w][t];
+                mine[w][t] = all;
+                all += c;
+            }
+            upto = all;
+#pragma unroll
+            for (int k = 1; k < 64; k *= 2) {
+                const uint32_t o = __shfl_up(upto, k, 64);
+                if (lane >= k) upto += o;
+            }
+            if (lane == 63) sums[wave] = upto;
+        }
+        __syncthreads();
+        if (t < kSortBins) {
+            uint32_t before = upto - all;
+            for (int w = 0; w < wave; ++w) before += sums[w];
+            base[t] = before;
+        }
+        __syncthreads();
+        if (ok) {
+            const uint32_t to = base[digit] + mine[wave][digit] + rank;
+            keys[to] = key;
+            places[to] = pos;
+        }
+        __syncthreads();
+        if (ok) {
+            key = keys[t];
+            pos = places[t];
+        }
+        __syncthreads();
+    }
+    if (ok) {
+        a.key[0][t] = key;
+        a.pos[0][t] = pos;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // sums over runs of equal rows
 // ---------------------------------------------------------------------------
@@ -281,13 +353,14 @@ __device__ __forceinline__ void get_row(const LookupGradArgs& a, uint64_t t, uin
 // partial sum (slot 0: from the chunk's start; slot 1: to its end). Four rows
 // are loaded together and added in order.
 template <class F, class G, int U>
-__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
+__device__ __forceinline__ void sum_chunks(const LookupGradArgs& a, uint32_t chunks, int sorted, uint32_t lanes,
+                                           uint32_t block, uint32_t slice)
 {
     constexpr int K = kGradChunk, B = 4;
     __shared__ uint32_t keys[kBlock / kGradLanes][K + 2];  // the one before the chunk, its own, the one after
     __shared__ uint32_t places[kBlock / kGradLanes][K];
     const uint32_t rows = static_cast<uint32_t>(a.rows), per = kBlock / lanes;
-    const uint64_t first = static_cast<uint64_t>(blockIdx.x) * per * K;  // the workgroup's first position
+    const uint64_t first = static_cast<uint64_t>(block) * per * K;  // the workgroup's first position
     for (uint32_t i = threadIdx.x; i < per * (K + 2); i += kBlock) {
         const uint32_t g = i / (K + 2), k = i % (K + 2);
         const uint64_t p = first + static_cast<uint64_t>(g) * K + k;  // one past the place
@@ -296,8 +369,8 @@ __global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint3
         if (k >= 1 && k <= K) places[g][k - 1] = in ? a.pos[sorted][p - 1] : 0;
     }
     __syncthreads();
-    const uint32_t group = threadIdx.x / lanes, chunk = blockIdx.x * per + group;
-    const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * U;
+    const uint32_t group = threadIdx.x / lanes, chunk = block * per + group;
+    const uint64_t c = (static_cast<uint64_t>(slice) * lanes + (threadIdx.x & (lanes - 1))) * U;
     if (chunk >= chunks || c >= a.width) return;
     const uint32_t* key = &keys[group][1];
     const uint32_t* pos = places[group];
@@ -328,6 +401,37 @@ __global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint3
             from_start = false;
         }
     }
+}
+
+template <class F, class G, int U>
+__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
+{
+    sum_chunks<F, G, U>(a, chunks, sorted, lanes, blockIdx.x, blockIdx.y);
+}
+
+// The sums and the zeros of at most kSortThreads tokens: the first bx * by
+// workgroups sum, the others fill the rows that are not among the sorted keys.
+template <class F, class G, int U, bool NT>
+__global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uint32_t chunks, uint32_t lanes,
+                                                     uint32_t bx, uint32_t by, uint32_t fill_lanes)
+{
+    if (blockIdx.x < bx * by) {
+        sum_chunks<F, G, U>(a, chunks, 0, lanes, blockIdx.x % bx, blockIdx.x / bx);
+        return;
+    }
+    __shared__ uint32_t keys[kSortThreads];
+    const uint32_t n = static_cast<uint32_t>(a.ntokens);
+    for (uint32_t i = threadIdx.x; i < n; i += kBlock) keys[i] = a.key[0][i];
+    __syncthreads();
+    fill_rows<G, NT, kBlock>(a, 0, a.rows, blockIdx.x - bx * by, gridDim.x - bx * by, fill_lanes, [&](uint64_t r) {
+        uint32_t lo = 0, hi = n;  // the first key that is not below r
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi) / 2;
+            if (keys[mid] < r) lo = mid + 1;
+            else hi = mid;
+        }
+        return lo < n && keys[lo] == r;
+    });
 }
 
 // Joins the partial sums of a run that goes over chunk borders, in order:
@@ -384,7 +488,7 @@ __global__ __launch_bounds__(kBlock) void clear_words(uint32_t* words, uint64_t 
 template <class G, bool NT>
 __global__ __launch_bounds__(kSortThreads) void fill_all(const LookupGradArgs a, uint32_t lanes)
 {
-    fill_rows<G, NT, kSortThreads>(a, 0, a.rows, blockIdx.x, gridDim.x, lanes);
+    fill_rows<G, NT, kSortThreads>(a, 0, a.rows, blockIdx.x, gridDim.x, lanes, [](uint64_t) { return false; });
 }
 
 uint32_t lanes_for(uint64_t units, uint32_t least, uint32_t most)
@@ -394,20 +498,25 @@ uint32_t lanes_for(uint64_t units, uint32_t least, uint32_t most)
     return lanes;
 }
 
+// Workgroups that fill the rows of the matrix, THREADS threads each, and the
+// threads of one row.
+template <class G>
+void fill_shape(const LookupGradArgs& a, uint32_t threads, int num_cus, uint32_t* blocks, uint32_t* lanes)
+{
+    *lanes = lanes_for((a.width * (16 / G::kEpv) + 15) / 16, 1, 256);
+    const uint64_t each = threads / *lanes * kFillRows, wanted = (a.rows + each - 1) / each;
+    *blocks = static_cast<uint32_t>(std::min<uint64_t>(wanted, static_cast<uint64_t>(num_cus) * 8 * (kSortThreads / threads)));
+}
+
+// Sorts the tokens and fills; *sorted tells in which of the buffers they end.
 template <class G, bool NT>
 hipError_t sort_and_fill(const LookupGradArgs& a, int* sorted, int num_cus, hipStream_t s)
 {
-    const uint32_t lanes = lanes_for((a.width * (16 / G::kEpv) + 15) / 16, 1, 256);
-    const uint64_t each = kSortThreads / lanes * kFillRows, wanted = (a.rows + each - 1) / each, cap = static_cast<uint64_t>(num_cus) * 8;
-    const uint32_t fillers = static_cast<uint32_t>(wanted < cap ? wanted : cap);
-    const uint64_t words = a.clear_words;
-    const uint64_t clearers = (words + kBlock - 1) / kBlock;
-    hipLaunchKernelGGL(clear_words, dim3(static_cast<uint32_t>(clearers < 1024 ? clearers : 1024)), dim3(kBlock), 0, s,
-                       reinterpret_cast<uint32_t*>(a.present), words);
-    if (a.ntokens == 0) {
-        hipLaunchKernelGGL((fill_all<G, NT>), dim3(fillers), dim3(kSortThreads), 0, s, a, lanes);
-        return hipGetLastError();
-    }
+    uint32_t fillers, lanes;
+    fill_shape<G>(a, kSortThreads, num_cus, &fillers, &lanes);
+    const uint64_t clearers = (a.clear_words + kBlock - 1) / kBlock;
+    hipLaunchKernelGGL(clear_words, dim3(static_cast<uint32_t>(std::min<uint64_t>(clearers, 1024))), dim3(kBlock), 0, s,
+                       reinterpret_cast<uint32_t*>(a.present), a.clear_words);
     const uint64_t all = (a.ntokens + kSortThreads - 1) / kSortThreads;
     const uint32_t rounds = static_cast<uint32_t>((all + kSortBlocks - 1) / kSortBlocks);
     const uint32_t blocks = static_cast<uint32_t>((all + rounds - 1) / rounds);
@@ -422,13 +531,33 @@ hipError_t sort_and_fill(const LookupGradArgs& a, int* sorted, int num_cus, hipS
     return hipGetLastError();
 }
 
-template <class F, class G, int U>
-hipError_t grad_launch(const LookupGradArgs& a, uint32_t chunks, int sorted, hipStream_t s)
+template <class F, class G, int U, bool NT>
+hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
 {
+    if (a.ntokens == 0) {
+        uint32_t fillers, fill_lanes;
+        fill_shape<G>(a, kSortThreads, num_cus, &fillers, &fill_lanes);
+        hipLaunchKernelGGL((fill_all<G, NT>), dim3(fillers), dim3(kSortThreads), 0, s, a, fill_lanes);
+        return hipGetLastError();
+    }
+    const uint32_t chunks = static_cast<uint32_t>((a.ntokens + kGradChunk - 1) / kGradChunk);
     const uint64_t units = (a.width + U - 1) / U;
     const uint32_t lanes = lanes_for(units, kGradLanes, kBlock), per = kBlock / lanes;
     const dim3 grid((chunks + per - 1) / per, static_cast<uint32_t>((units + lanes - 1) / lanes));
-    hipLaunchKernelGGL((grad_sum<F, G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+    int sorted = 0;
+    if (a.ntokens <= kSortThreads) {
+        const int passes = sort_passes(a.rows), bits = (sort_bits(a.rows) + passes - 1) / passes;
+        hipLaunchKernelGGL(sort_small, dim3(1), dim3(kSortThreads), 0, s, a, passes, bits);
+        uint32_t fillers, fill_lanes;
+        fill_shape<G>(a, kBlock, num_cus, &fillers, &fill_lanes);
+        if (a.accumulate) fillers = 0;
+        hipLaunchKernelGGL((grad_small<F, G, U, NT>), dim3(grid.x * grid.y + fillers), dim3(kBlock), 0, s, a, chunks,
+                           lanes, grid.x, grid.y, fill_lanes);
+    } else {
+        const hipError_t e = sort_and_fill<G, NT>(a, &sorted, num_cus, s);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((grad_sum<F, G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+    }
     if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
     return hipGetLastError();
 }
@@ -437,11 +566,8 @@ template <class F, class G>
 hipError_t grad_call(const LookupGradArgs& a, bool vec, bool nt, int num_cus, hipStream_t s)
 {
     constexpr int U = F::kEpv > G::kEpv ? F::kEpv : G::kEpv;
-    int sorted = 0;
-    const hipError_t e = nt ? sort_and_fill<G, true>(a, &sorted, num_cus, s) : sort_and_fill<G, false>(a, &sorted, num_cus, s);
-    if (e != hipSuccess || a.ntokens == 0) return e;
-    const uint32_t chunks = static_cast<uint32_t>((a.ntokens + kGradChunk - 1) / kGradChunk);
-    return vec ? grad_launch<F, G, U>(a, chunks, sorted, s) : grad_launch<F, G, 1>(a, chunks, sorted, s);
+    if (nt) return vec ? grad_launch<F, G, U, true>(a, num_cus, s) : grad_launch<F, G, 1, true>(a, num_cus, s);
+    return vec ? grad_launch<F, G, U, false>(a, num_cus, s) : grad_launch<F, G, 1, false>(a, num_cus, s);
 }
 
 }  // namespace
