@@ -34,7 +34,9 @@ __device__ __forceinline__ uint64_t row_of(const Indices& x, uint64_t t, int64_t
 // lookup
 // ---------------------------------------------------------------------------
 // `lanes` (a power of two up to kBlock) threads a row, kBlock / lanes rows a
-// workgroup; VEC: 16-byte vectors, else elements.
+// workgroup; VEC: 16-byte vectors, else elements. Stores are cached: with
+// non-temporal ones 16384 x 4096 fp16 returns in 30 us rather than 44, but what
+// reads the rows next ends 11 us later (of 80), and so at every size from 32 MiB on.
 template <class F, bool VEC>
 __global__ __launch_bounds__(kBlock) void lookup(const LookupArgs a, int lanes)
 {
