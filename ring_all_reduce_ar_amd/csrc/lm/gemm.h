@@ -134,7 +134,8 @@ __device__ __forceinline__ void tile_of_workgroup(const GemmArgs& g, uint32_t* t
 // ---------------------------------------------------------------------------
 // A lane's results are four rows of one column; stored as they lie they make
 // pieces of 32 bytes. A 256 x 256 tile of 16-bit values fills the 128 KiB that
-// the product's stages held, and leaves in whole rows of 512 bytes.
+// the product's stages held, and leaves in whole rows of 512 bytes; `nt`:
+// non-temporal stores.
 struct NoStaging {
     static constexpr bool kOn = false;
 };
@@ -154,7 +155,7 @@ struct Staging {
     // out[n][m], `ld` apart, for the first `rows` n and `cols` m (a multiple of 8).
     template <class T, int MT, int NT>
     __device__ __forceinline__ void store_by_column(const Tile<MT, NT>& x, uint16_t* out, uint64_t ld, uint32_t rows,
-                                                    uint32_t cols) const
+                                                    uint32_t cols, bool nt) const
     {
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
         __syncthreads();
@@ -169,14 +170,14 @@ struct Staging {
             }
         }
         __syncthreads();
-        copy_rows(out, ld, n_base, rows, m_base, cols, 0);
+        copy_rows(out, ld, n_base, rows, m_base, cols, 0, nt);
     }
 
     // out[m][n]: neighbouring columns lie in neighbouring lanes, which
     // exchange halves, so that each has two columns of two rows.
     template <class T, int MT, int NT>
     __device__ __forceinline__ void store_by_row(const Tile<MT, NT>& x, const float (&factor)[NT], uint16_t* out,
-                                                 uint64_t ld, uint32_t rows, uint32_t cols) const
+                                                 uint64_t ld, uint32_t rows, uint32_t cols, bool nt) const
     {
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4, odd = lane & 1;
         __syncthreads();
@@ -196,19 +197,21 @@ struct Staging {
             }
         }
         __syncthreads();
-        copy_rows(out, ld, m_base, rows, n_base, cols, 1);
+        copy_rows(out, ld, m_base, rows, n_base, cols, 1, nt);
     }
 
 private:
     __device__ __forceinline__ void copy_rows(uint16_t* out, uint64_t ld, uint32_t row0, uint32_t rows, uint32_t col0,
-                                              uint32_t cols, int key_shift) const
+                                              uint32_t cols, int key_shift, bool nt) const
     {
         const uint32_t c = threadIdx.x & 31;
 #pragma unroll 4
         for (uint32_t r = threadIdx.x >> 5; r < 256; r += 16) {
             const u32x4 v = *reinterpret_cast<const u32x4*>(lds + at(r, c * 16, r >> key_shift));
-            if (row0 + r < rows && col0 + c * 8 < cols)
-                *reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(row0 + r) * ld + col0 + c * 8) = v;
+            if (row0 + r >= rows || col0 + c * 8 >= cols) continue;
+            u32x4* to = reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(row0 + r) * ld + col0 + c * 8);
+            if (nt) __builtin_nontemporal_store(v, to);
+            else *to = v;
         }
     }
 };
