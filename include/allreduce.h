@@ -366,7 +366,8 @@ ar_result_t ar_embedding(ar_comm_t comm, const void* weight, const void* tokens,
                          size_t ntokens, size_t rows, size_t width, size_t ld_weight, size_t ld_out,
                          long long first_row, float scale, ar_dtype_t dtype, hipStream_t stream);
 
-/* Workspace of ar_embedding_backward; (size_t)-1 for sizes it does not take. */
+/* Workspace of ar_embedding_backward, also for fewer tokens; (size_t)-1 for
+ * sizes it does not take. */
 size_t ar_embedding_workspace_bytes(size_t ntokens, size_t rows, size_t width);
 
 /* Its gradient: grad_weight[v] = scale * sum of grad_out[t] over the tokens t
@@ -381,7 +382,8 @@ ar_result_t ar_embedding_backward(ar_comm_t comm, const void* grad_out, const vo
                                   ar_dtype_t grad_dtype, int accumulate, hipStream_t stream);
 
 /* Workspace of ar_linear_cross_entropy (backward = 0) or its gradient
- * (backward != 0); (size_t)-1 for sizes they do not take. */
+ * (backward != 0), also for fewer tokens; (size_t)-1 for sizes they do not
+ * take. */
 size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, size_t width, ar_dtype_t dtype,
                                                int backward);
 

@@ -812,6 +812,7 @@ struct Call {
 // What a call's products cost with pieces of `rows` rows, in depth steps of the
 // busiest CU: a product takes whole rounds of one tile a CU.
 constexpr uint64_t kCUs = 256;
+constexpr uint64_t kMostSplits = 64;
 struct Shape {
     uint64_t ntokens, width, tile_n, tile_w, step;  // tile_w: columns of the weight gradient's tiles
     bool pieces;
@@ -836,7 +837,7 @@ double split_cost(uint64_t tiles, uint64_t depth, uint64_t step, double join, in
     for (uint64_t rounds = 0; rounds <= 2; ++rounds) {  // unsplit, or parts that fill one round or two
         uint64_t k = 1;
         if (rounds) {
-            k = std::min({rounds * kCUs / std::max<uint64_t>(tiles, 1), uint64_t(64), depth / 128});
+            k = std::min({rounds * kCUs / std::max<uint64_t>(tiles, 1), kMostSplits, depth / 128});
             if (k < 2) continue;
         }
         const double c = static_cast<double>(up(tiles * k, kCUs) * (up(up(depth, step), k) + 8)) +
@@ -870,6 +871,30 @@ bool small_tiles(uint64_t ntokens, uint64_t vocab, uint64_t width, bool f32, boo
 
 }  // namespace
 
+namespace {
+constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
+}  // namespace
+
+// Each buffer's largest size over the plans of up to `ntokens` tokens: they
+// differ in tiles, in the fp32 operands' form and in the parts of split sums,
+// which are at most two rounds of tiles or kMostSplits times a whole sum.
+uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward)
+{
+    const bool f32 = dtype == AR_FLOAT32;
+    const uint64_t ob = f32 ? kPieces * 2 : 2, k_pad = round_up(width, f32 ? 32 : kTileK), t_pad = round_up(ntokens, kTileK);
+    const uint64_t v_pad = round_up(vocab, kTileM), few = std::min<uint64_t>(ntokens, 64);
+    const uint64_t row_bytes = ob * (k_pad + (backward ? 2 * t_pad + width : 0));
+    const uint64_t piece = std::min(v_pad * row_bytes, std::max(kPieceBytes, kTileM * row_bytes));
+    uint64_t bytes = ntokens * k_pad * ob + piece + 16 * 256;
+    if (!backward)
+        // 2 or 4 rows of statistics a large tile, up to 8 for few tokens; small tiles come to less than 2^20 bytes
+        return bytes + (v_pad / kTileM + 1) * (ntokens * (f32 ? 4 : 2) + few * 8) * sizeof(Stats) + ntokens * 4 + (1u << 20);
+    constexpr uint64_t kRounds = 2 * kCUs * kTileM * 256 * 4;
+    const uint64_t hidden_sum = ntokens * width * 4, weight_sum = v_pad * width * 4;
+    return bytes + width * t_pad * ob + std::max(hidden_sum, std::min(hidden_sum * kMostSplits, kRounds)) +
+           std::min(weight_sum * kMostSplits, kRounds) + sizeof(RowScale);
+}
+
 CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward)
 {
     CrossEntropyPlan p{};
@@ -882,8 +907,7 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     p.t_pad = round_up(ntokens, p.tile_n == 16 ? 16 : kTileK);  // the tiles cover it: they write its zeros
     const uint64_t tile_w = p.pieces ? kPiecesN : f32 ? 64 : 256;
     p.pack_hidden = p.pack_weight = true;  // the caller clears these where the operands can be read as they lie
-    // A piece's buffers come to at most about kPieceBytes; pieces are whole tiles.
-    constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
+    // A piece's buffers come to at most kPieceBytes, or one tile's; pieces are whole tiles.
     const uint64_t row_bytes = ob * (p.k_pad + (backward ? 2 * p.t_pad + width : 0));
     const uint64_t whole = round_up(vocab, kTileM) / kTileM;
     uint64_t most = kPieceBytes / (row_bytes * kTileM);

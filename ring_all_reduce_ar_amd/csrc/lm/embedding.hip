@@ -349,16 +349,16 @@ __device__ __forceinline__ void get_row(const LookupGradArgs& a, uint64_t t, uin
     }
 }
 
-// `lanes` threads (a power of two, at least kGradLanes) sum kGradChunk
-// positions of the sorted order each over U columns: a run inside the chunk is
+// `lanes` threads (a power of two, at least kGradLanes) sum a chunk of K
+// positions of the sorted order over U columns: a run inside the chunk is
 // written to its row, a run that began before it or goes on after it leaves a
-// partial sum (slot 0: from the chunk's start; slot 1: to its end). Four rows
+// partial sum (slot 0: from the chunk's start; slot 1: to its end). Eight rows
 // are loaded together and added in order.
-template <class F, class G, int U>
+template <class F, class G, int U, int K>
 __device__ __forceinline__ void sum_chunks(const LookupGradArgs& a, uint32_t chunks, int sorted, uint32_t lanes,
                                            uint32_t block, uint32_t slice)
 {
-    constexpr int K = kGradChunk, B = 4;
+    constexpr int B = 8;
     __shared__ uint32_t keys[kBlock / kGradLanes][K + 2];  // the one before the chunk, its own, the one after
     __shared__ uint32_t places[kBlock / kGradLanes][K];
     const uint32_t rows = static_cast<uint32_t>(a.rows), per = kBlock / lanes;
@@ -379,13 +379,15 @@ __device__ __forceinline__ void sum_chunks(const LookupGradArgs& a, uint32_t chu
     float acc[U] = {};
     bool from_start = true;  // the run began at the chunk's first position
     for (int p = 0; p < K && key[p] < rows; p += B) {  // tokens of no row come last
-        float x[B][U] = {};
+        float x[B][U];  // loaded whether they count or not: under a branch each load would be waited for by itself
 #pragma unroll
-        for (int k = 0; k < B; ++k)
-            if (key[p + k] < rows) get_row<F, U>(a, pos[p + k], c, x[k]);
+        for (int k = 0; k < B; ++k) get_row<F, U>(a, pos[p + k], c, x[k]);
+        uint32_t at[B + 1];
+#pragma unroll
+        for (int k = 0; k <= B; ++k) at[k] = key[p + k];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            const uint32_t cur = key[p + k], nxt = key[p + k + 1];
+            const uint32_t cur = at[k], nxt = at[k + 1];
             if (cur >= rows) break;
 #pragma unroll
             for (int j = 0; j < U; ++j) acc[j] += x[k][j];
@@ -405,10 +407,10 @@ __device__ __forceinline__ void sum_chunks(const LookupGradArgs& a, uint32_t chu
     }
 }
 
-template <class F, class G, int U>
+template <class F, class G, int U, int K>
 __global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
 {
-    sum_chunks<F, G, U>(a, chunks, sorted, lanes, blockIdx.x, blockIdx.y);
+    sum_chunks<F, G, U, K>(a, chunks, sorted, lanes, blockIdx.x, blockIdx.y);
 }
 
 // The sums and the zeros of at most kSortThreads tokens: the first bx * by
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uin
                                                      uint32_t bx, uint32_t by, uint32_t fill_lanes)
 {
     if (blockIdx.x < bx * by) {
-        sum_chunks<F, G, U>(a, chunks, 0, lanes, blockIdx.x % bx, blockIdx.x / bx);
+        sum_chunks<F, G, U, kGradChunkFew>(a, chunks, 0, lanes, blockIdx.x % bx, blockIdx.x / bx);
         return;
     }
     __shared__ uint32_t keys[kSortThreads];
@@ -437,16 +439,19 @@ __global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uin
 }
 
 // Joins the partial sums of a run that goes over chunk borders, in order:
-// `lanes` threads for each chunk in which such a run begins, sixteen loads
-// together (the most frequent token of a text has a tenth of all positions).
+// `lanes` threads for each chunk of `len` positions in which such a run begins.
+// Sixteen chunks' keys and sums are loaded together, whether the run goes on
+// over all of them or not (the most frequent token of a text has a tenth of all
+// positions).
 template <class G, int U>
-__global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
+__global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t chunks, uint32_t len, int sorted,
+                                                    uint32_t lanes)
 {
     constexpr int B = 16;
     const uint32_t* key = a.key[sorted];
     const uint32_t chunk = blockIdx.x * (kBlock / lanes) + threadIdx.x / lanes;
     const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * U;
-    const uint64_t p0 = static_cast<uint64_t>(chunk) * kGradChunk, p1 = p0 + kGradChunk;
+    const uint64_t p0 = static_cast<uint64_t>(chunk) * len, p1 = p0 + len;
     if (p1 >= a.ntokens || c >= a.width) return;
     const uint32_t row = key[p1 - 1];
     if (row >= a.rows || key[p1] != row) return;                 // no run goes on
@@ -455,26 +460,24 @@ __global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint
     const float* from = a.partial + (2ull * chunk + 1) * a.width + c;
 #pragma unroll
     for (int j = 0; j < U; ++j) acc[j] = from[j];
-    auto goes_on = [&](uint64_t b) { return b < chunks && key[b * kGradChunk] == row; };
-    uint64_t b = chunk + 1;
-    while (goes_on(b + B - 1)) {  // and so do the chunks before it
+    for (uint32_t b = chunk + 1, on = 1; on; b += B) {
+        uint32_t at[B];
         float x[B][U];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            from = a.partial + 2ull * (b + k) * a.width + c;
+            const uint32_t q = min(b + k, chunks - 1);
+            at[k] = key[static_cast<uint64_t>(q) * len];
+            from = a.partial + 2ull * q * a.width + c;
 #pragma unroll
             for (int j = 0; j < U; ++j) x[k][j] = from[j];
         }
 #pragma unroll
-        for (int k = 0; k < B; ++k)
+        for (int k = 0; k < B; ++k) {
+            on = on && b + k < chunks && at[k] == row;
+            if (!on) continue;
 #pragma unroll
             for (int j = 0; j < U; ++j) acc[j] += x[k][j];
-        b += B;
-    }
-    for (; goes_on(b); ++b) {
-        from = a.partial + 2ull * b * a.width + c;
-#pragma unroll
-        for (int j = 0; j < U; ++j) acc[j] += from[j];
+        }
     }
     put_row<G, U>(a, row, c, acc);
 }
@@ -542,7 +545,7 @@ hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
         hipLaunchKernelGGL((fill_all<G, NT>), dim3(fillers), dim3(kSortThreads), 0, s, a, fill_lanes);
         return hipGetLastError();
     }
-    const uint32_t chunks = static_cast<uint32_t>((a.ntokens + kGradChunk - 1) / kGradChunk);
+    const uint32_t len = grad_chunk(a.ntokens), chunks = static_cast<uint32_t>((a.ntokens + len - 1) / len);
     const uint64_t units = (a.width + U - 1) / U;
     const uint32_t lanes = lanes_for(units, kGradLanes, kBlock), per = kBlock / lanes;
     const dim3 grid((chunks + per - 1) / per, static_cast<uint32_t>((units + lanes - 1) / lanes));
@@ -558,9 +561,12 @@ hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
     } else {
         const hipError_t e = sort_and_fill<G, NT>(a, &sorted, num_cus, s);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((grad_sum<F, G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+        if (len == kGradChunkFew)
+            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunkFew>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+        else
+            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunk>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
     }
-    if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+    if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, len, sorted, lanes);
     return hipGetLastError();
 }
 

@@ -355,7 +355,10 @@ bool grad_layout(uint64_t ntokens, uint64_t rows, uint64_t width, GradLayout* l)
     for (int k = 0; k < 2; ++k) l->pos[k] = take(ntokens, 4);
     l->present = take(rows, 1);
     l->hist = take(ar::lm::sort_passes(rows), ntokens ? ar::lm::kSortBlocks * ar::lm::kSortBins * 4 : 0);
-    l->partial = take(ceil_div(ntokens, ar::lm::kGradChunk) * 2, width * 4);
+    // (chunks of few tokens are short: what serves a number of tokens serves fewer)
+    const uint64_t few = std::min(ntokens, ar::lm::kGradFew);
+    l->partial = take(2 * std::max(ceil_div(ntokens, ar::lm::grad_chunk(ntokens)), ceil_div(few, ar::lm::grad_chunk(few))),
+                      width * 4);
     l->bytes = std::max<size_t>(at, 16);
     return ok;
 }
@@ -545,7 +548,7 @@ AR_EXPORT size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t 
 {
     if (!valid_dtype(dtype) || dtype == AR_INT32 || width == 0 || !plan_fits(ntokens, vocab, width, dtype))
         return static_cast<size_t>(-1);
-    return ar::lm::plan_cross_entropy(ntokens, vocab, width, dtype, backward != 0).bytes;
+    return ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, backward != 0);
 }
 
 namespace {
@@ -572,7 +575,7 @@ ar_result_t cross_entropy_common(ar_comm* comm, const void* hidden, const void* 
     *plan = ar::lm::plan_cross_entropy(ntokens, vocab, width, dtype, backward);
     plan->pack_hidden = !direct(hidden, *ld_hidden, width, e, plan->pieces);
     plan->pack_weight = !direct(weight, *ld_weight, width, e, plan->pieces);
-    return check_workspace(comm, plan->bytes);
+    return check_workspace(comm, ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, backward));
 }
 
 }  // namespace

@@ -2,6 +2,7 @@
 which come before the first HIP call (a communicator with no device behind it
 serves: a refused call reads its first fields only)."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -218,3 +219,29 @@ def test_rows_of_matrices():
     for bad in (x[:, ::2], x.t(), torch.zeros(1, 8).expand(6, 8), x.as_strided((4, 8), (4, 1))):
         with pytest.raises(ValueError):
             ar._rows(bad, 0)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses are not for a GPU")
+def test_a_workspace_serves_fewer_tokens():
+    """What the size function gives for n tokens passes the check of every call
+    with fewer: such a call gets as far as HIP."""
+    rng = random.Random(1)
+
+    def passes(fn, *args, **kw):
+        with pytest.raises(ar.ArError) as e:
+            fn(*args, **kw, stream=0)
+        assert e.value.code == ar.AR_ERR_HIP, str(e.value)
+
+    for _ in range(150):
+        n, vocab, width = (int(2 ** rng.uniform(0, k)) for k in (14, 18, 13))
+        dtype = rng.choice(["f32", "f16", "bf16"])
+        ws = [ar.ar_linear_cross_entropy_workspace_bytes(n, vocab, width, dtype, backward=b) for b in (False, True)]
+        emb = ar.ar_embedding_workspace_bytes(n, vocab, width)
+        for m in {n, max(1, n - 1), (n + 1) // 2, min(n, 64), min(n, 65), min(n, 16), min(n, 17), 1, rng.randint(1, n)}:
+            far = [(1 << 45) * k for k in range(1, 8)]
+            passes(ar.ar_linear_cross_entropy, host_comm(ws_bytes=ws[0]), far[0], far[1], far[2], far[3], far[4], m, vocab,
+                   width, dtype, index="i64")
+            passes(ar.ar_linear_cross_entropy_backward, host_comm(ws_bytes=ws[1]), far[0], far[1], far[2], far[3],
+                   far[4], far[5], far[6], m, vocab, width, dtype, index="i64")
+            passes(ar.ar_embedding_backward, host_comm(ws_bytes=emb), far[0], far[1], far[2], m, vocab, width, dtype,
+                   index="i32")
