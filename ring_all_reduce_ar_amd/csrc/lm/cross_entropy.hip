@@ -132,7 +132,8 @@ __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64
                                                           int64_t ignore, uint64_t vocab)
 {
     __shared__ Raw tile[64][sizeof(Raw) == 2 ? 66 : 65];
-    const uint64_t r0 = static_cast<uint64_t>(blockIdx.x) * 64, c0 = static_cast<uint64_t>(blockIdx.y) * 64;
+    const uint32_t high = static_cast<uint32_t>((pad + 63) / 64);
+    const uint64_t r0 = static_cast<uint64_t>(blockIdx.x % high) * 64, c0 = static_cast<uint64_t>(blockIdx.x / high) * 64;
     const int slot = threadIdx.x & 7;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -577,7 +578,7 @@ hipError_t transpose(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
                      const CrossEntropyArgs& a, int masked, hipStream_t s)
 {
     const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * sizeof(Raw) % 16 == 0;
-    const dim3 grid(static_cast<uint32_t>((pad + 63) / 64), static_cast<uint32_t>((width + 63) / 64));
+    const dim3 grid(static_cast<uint32_t>((pad + 63) / 64 * ((width + 63) / 64)));
     auto launch = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked,
                            a.ignore_index, a.vocab);
@@ -630,6 +631,13 @@ uint64_t stat_rows_of(uint64_t rows, uint64_t ntokens, int tile_n)
 // What is larger than the last-level cache is stored around it: 8192 x 131072 x
 // 4096 bf16, loss and gradients, 25.3 -> 25.0 ms.
 constexpr uint64_t kStreamBytes = uint64_t(256) << 20;
+
+// Rows of large tiles in one launch: work-items are counted in 32 bits.
+uint64_t most_tiles(uint64_t ntokens, uint64_t tile_n)
+{
+    const uint64_t across = (ntokens + tile_n - 1) / tile_n;
+    return (uint64_t(1) << 22) / (across ? across : 1);
+}
 
 // F: the storage type; T: the matrix instruction's.
 template <class F, class T, int PARTS>
@@ -716,7 +724,7 @@ struct Call {
         if (e != hipSuccess) return e;
         Stats* stats = reinterpret_cast<Stats*>(ws + p.stats);
         float* target_logit = reinterpret_cast<float*>(ws + p.target_logit);
-        const uint64_t piece = p.pack_weight ? p.piece : a.vocab;  // pieces bound what is packed
+        const uint64_t piece = p.pack_weight ? p.piece : most_tiles(a.ntokens, p.tile_n) * kTileM;  // pieces bound what is packed
         for (uint64_t v0 = 0; v0 < a.vocab; v0 += piece) {
             const uint64_t rows = a.vocab - v0 < piece ? a.vocab - v0 : piece;
             if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
@@ -887,8 +895,9 @@ uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, a
     const uint64_t piece = std::min(v_pad * row_bytes, std::max(kPieceBytes, kTileM * row_bytes));
     uint64_t bytes = ntokens * k_pad * ob + piece + 16 * 256;
     if (!backward)
-        // 2 or 4 rows of statistics a large tile, up to 8 for few tokens; small tiles come to less than 2^20 bytes
-        return bytes + (v_pad / kTileM + 1) * (ntokens * (f32 ? 4 : 2) + few * 8) * sizeof(Stats) + ntokens * 4 + (1u << 20);
+        // 2 or 4 rows of statistics for 256 of the vocabulary, up to 16 for few
+        // tokens; small tiles of more tokens come to less than 2^20 bytes
+        return bytes + (v_pad / kTileM + 1) * (ntokens * (f32 ? 4 : 2) + few * 16) * sizeof(Stats) + ntokens * 4 + (1u << 20);
     constexpr uint64_t kRounds = 2 * kCUs * kTileM * 256 * 4;
     const uint64_t hidden_sum = ntokens * width * 4, weight_sum = v_pad * width * 4;
     return bytes + width * t_pad * ob + std::max(hidden_sum, std::min(hidden_sum * kMostSplits, kRounds)) +
@@ -912,6 +921,7 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     const uint64_t whole = round_up(vocab, kTileM) / kTileM;
     uint64_t most = kPieceBytes / (row_bytes * kTileM);
     if (most > 4096) most = 4096;  // the transposed piece's rows stay within a buffer's 2^31 bytes
+    most = std::min(most, most_tiles(ntokens, p.tile_n));
     most = most < 1 ? 1 : most > whole ? whole : most;
     p.splits = p.weight_splits = 1;
     if (!backward) {
@@ -937,11 +947,11 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
             }
         }
     }
-    {  // in pieces, or, where the weight is read as it lies, at once
-        const uint64_t full = vocab / p.piece, rest = vocab % p.piece;
-        const uint64_t pieces = full * stat_rows_of(p.piece, ntokens, p.tile_n) + stat_rows_of(rest, ntokens, p.tile_n);
-        const uint64_t once = stat_rows_of(vocab, ntokens, p.tile_n);
-        p.stat_rows = pieces > once ? pieces : once;
+    // in pieces, or, where the weight is read as it lies, in as few launches as there can be
+    for (const uint64_t rows : {p.piece, most_tiles(ntokens, p.tile_n) * kTileM}) {
+        const uint64_t full = vocab / rows, rest = vocab % rows;
+        p.stat_rows = std::max(p.stat_rows, full * stat_rows_of(rows, ntokens, p.tile_n) +
+                                                (rest ? stat_rows_of(rest, ntokens, p.tile_n) : 0));
     }
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {

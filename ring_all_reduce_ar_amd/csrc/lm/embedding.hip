@@ -408,9 +408,10 @@ __device__ __forceinline__ void sum_chunks(const LookupGradArgs& a, uint32_t chu
 }
 
 template <class F, class G, int U, int K>
-__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes)
+__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes,
+                                                   uint32_t bx)
 {
-    sum_chunks<F, G, U, K>(a, chunks, sorted, lanes, blockIdx.x, blockIdx.y);
+    sum_chunks<F, G, U, K>(a, chunks, sorted, lanes, blockIdx.x % bx, blockIdx.x / bx);
 }
 
 // The sums and the zeros of at most kSortThreads tokens: the first bx * by
@@ -445,12 +446,12 @@ __global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uin
 // positions).
 template <class G, int U>
 __global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t chunks, uint32_t len, int sorted,
-                                                    uint32_t lanes)
+                                                    uint32_t lanes, uint32_t bx)
 {
     constexpr int B = 16;
     const uint32_t* key = a.key[sorted];
-    const uint32_t chunk = blockIdx.x * (kBlock / lanes) + threadIdx.x / lanes;
-    const uint64_t c = (static_cast<uint64_t>(blockIdx.y) * lanes + (threadIdx.x & (lanes - 1))) * U;
+    const uint32_t chunk = blockIdx.x % bx * (kBlock / lanes) + threadIdx.x / lanes;
+    const uint64_t c = (static_cast<uint64_t>(blockIdx.x / bx) * lanes + (threadIdx.x & (lanes - 1))) * U;
     const uint64_t p0 = static_cast<uint64_t>(chunk) * len, p1 = p0 + len;
     if (p1 >= a.ntokens || c >= a.width) return;
     const uint32_t row = key[p1 - 1];
@@ -548,7 +549,9 @@ hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
     const uint32_t len = grad_chunk(a.ntokens), chunks = static_cast<uint32_t>((a.ntokens + len - 1) / len);
     const uint64_t units = (a.width + U - 1) / U;
     const uint32_t lanes = lanes_for(units, kGradLanes, kBlock), per = kBlock / lanes;
-    const dim3 grid((chunks + per - 1) / per, static_cast<uint32_t>((units + lanes - 1) / lanes));
+    // bx workgroups along the chunks, times the slices of a row
+    const uint32_t bx = (chunks + per - 1) / per, by = static_cast<uint32_t>((units + lanes - 1) / lanes);
+    const dim3 grid(bx * by);
     int sorted = 0;
     if (a.ntokens <= kSortThreads) {
         const int passes = sort_passes(a.rows), bits = (sort_bits(a.rows) + passes - 1) / passes;
@@ -556,17 +559,17 @@ hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
         uint32_t fillers, fill_lanes;
         fill_shape<G>(a, kBlock, num_cus, &fillers, &fill_lanes);
         if (a.accumulate) fillers = 0;
-        hipLaunchKernelGGL((grad_small<F, G, U, NT>), dim3(grid.x * grid.y + fillers), dim3(kBlock), 0, s, a, chunks,
-                           lanes, grid.x, grid.y, fill_lanes);
+        hipLaunchKernelGGL((grad_small<F, G, U, NT>), dim3(grid.x + fillers), dim3(kBlock), 0, s, a, chunks,
+                           lanes, bx, by, fill_lanes);
     } else {
         const hipError_t e = sort_and_fill<G, NT>(a, &sorted, num_cus, s);
         if (e != hipSuccess) return e;
         if (len == kGradChunkFew)
-            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunkFew>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunkFew>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes, bx);
         else
-            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunk>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes);
+            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunk>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes, bx);
     }
-    if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, len, sorted, lanes);
+    if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, len, sorted, lanes, bx);
     return hipGetLastError();
 }
 

@@ -170,3 +170,38 @@ def test_loss_with_split_sums(comms, dtype, n, vocab, width):  # noqa: F811
     """Gradients whose few tiles are summed in parts, along the tokens or the
     vocabulary, in either order of the operands."""
     check_loss(comms, n, vocab, width, dtype, 58)
+
+
+def test_loss_of_more_tiles_than_a_launch_counts(comms):  # noqa: F811
+    """2^20 tokens over 600 000 rows: 9.6 million tiles of 512 threads. A
+    sample of the tokens against 64 bits, all of them against each other: tokens
+    with equal rows have equal results."""
+    n, vocab, width, kinds = 1 << 20, 600_000, 8, 64
+    try:
+        comm = comms(1, ar.ar_linear_cross_entropy_workspace_bytes(n, vocab, width, "bf16"))
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("needs about 40 GB of workspace")
+    g = gen(59)
+    x = normal(g, kinds, width, dtype="bf16").repeat(n // kinds, 1)
+    w = normal(g, vocab, width, dtype="bf16")
+    y = torch.randint(0, vocab, (kinds,), generator=g, device="cuda").repeat(n // kinds)
+    losses, lse = nan_like(n, dtype="f32"), nan_like(n, dtype="f32")
+    ar.ar_linear_cross_entropy(comm, x, w, y, losses, lse, n, vocab, width, "bf16")
+    z, ez, rl, el, rloss, eloss, kept, at = loss_ref(x[:kinds], w, y[:kinds], -100)
+    close(lse[:kinds], rl, el)
+    close(losses[:kinds], rloss, eloss)
+    assert torch.equal(losses, losses[:kinds].repeat(n // kinds)) and torch.equal(lse, lse[:kinds].repeat(n // kinds))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_wide_rows(comms, dtype):  # noqa: F811
+    """Widths beyond 65535 blocks of a launch's second dimension."""
+    width = 4_200_072
+    check_loss(comms, 3, 20, 262_144 + 8, dtype, 60)
+    comm = comms(1, ar.ar_embedding_workspace_bytes(40, 6, width))
+    t = torch.randint(0, 6, (40,), generator=gen(61), device="cuda")
+    dout = normal(gen(62), 40, width, dtype=dtype)
+    ref, mags, most = embedding_grad_ref(t, dout, 6, 0, 1.0)
+    dw = nan_like(6, width, dtype=dtype)
+    ar.ar_embedding_backward(comm, dout, t, dw, 40, 6, width, dtype)
+    close(dw, ref, mags * ((most + 2) * U32) + ref.abs() * U[dtype] + TINY[dtype])
