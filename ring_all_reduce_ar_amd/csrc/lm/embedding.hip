@@ -214,15 +214,28 @@ __global__ __launch_bounds__(kSortThreads) void sort_move(const LookupGradArgs a
         const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
         if (ok && rank == 0) mine[wave][digit] = __popcll(same);
         __syncthreads();
+        uint32_t to = 0;
         if (ok) {
-            uint32_t to = next[digit] + rank;
+            to = next[digit] + rank;
             for (int w = 0; w < wave; ++w) to += mine[w][digit];
             a.key[src ^ 1][to] = key;
             a.pos[src ^ 1][to] = pos;
-            if (!last) {
-                const uint32_t block = to / (rounds * kSortThreads);
-                atomicAdd(&hist_next[block * kSortBins + ((key >> (shift + bits)) & (nb - 1))], 1u);
+        }
+        if (!last) {
+            // Counts for the next pass, one addition for a wave's keys of equal
+            // digits that go to one workgroup's range: a frequent token's keys
+            // would meet at one address one by one.
+            const uint32_t digit_next = (key >> (shift + bits)) & (nb - 1), block = to / (rounds * kSortThreads);
+            for (int b = 0; b < bits; ++b) {
+                const uint64_t m = __ballot((digit_next >> b) & 1);
+                same &= ((digit_next >> b) & 1) ? m : ~m;
             }
+            const int leader = same ? __builtin_ctzll(same) : lane;
+            const bool with = __shfl(block, leader, 64) == block;
+            const uint64_t group = __ballot(with) & same;
+            uint32_t* at = &hist_next[block * kSortBins + digit_next];
+            if (ok && lane == leader) atomicAdd(at, static_cast<uint32_t>(__popcll(group)));
+            else if (ok && !with) atomicAdd(at, 1u);
         }
         if (k + 1 == rounds) break;
         __syncthreads();
