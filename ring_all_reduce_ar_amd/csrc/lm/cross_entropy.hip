@@ -620,24 +620,22 @@ bool columns_in_b(uint64_t width, uint64_t other)
 
 // Rows of statistics that the logits of `rows` vocabulary rows leave: one for
 // each wave along a tile.
-uint64_t stat_rows_of(uint64_t rows, uint64_t ntokens, int tile_n)
+uint64_t stat_rows_of(uint64_t rows, int tile_n)
 {
     if (tile_n > 64) return (rows + kTileM - 1) / kTileM * (tile_n == 256 ? 2 : 4);
-    const uint64_t tile_m = few_tile_m(rows, ntokens, 1, tile_n);
-    const uint64_t waves = (tile_m == kTileM ? 8 : 4) / (tile_n == 16 ? 1 : 2);
-    return (rows + tile_m - 1) / tile_m * waves;
+    return (rows + kFewM - 1) / kFewM * (tile_n == 16 ? 4 : 2);
+}
+
+// Tiles along the vocabulary that one launch takes: work-items are counted in 32 bits.
+uint64_t most_tiles(uint64_t ntokens, uint64_t tile_n)
+{
+    const uint64_t across = (ntokens + tile_n - 1) / tile_n;
+    return (uint64_t(1) << 21) / (across ? across : 1);
 }
 
 // What is larger than the last-level cache is stored around it: 8192 x 131072 x
 // 4096 bf16, loss and gradients, 25.3 -> 25.0 ms.
 constexpr uint64_t kStreamBytes = uint64_t(256) << 20;
-
-// Rows of large tiles in one launch: work-items are counted in 32 bits.
-uint64_t most_tiles(uint64_t ntokens, uint64_t tile_n)
-{
-    const uint64_t across = (ntokens + tile_n - 1) / tile_n;
-    return (uint64_t(1) << 22) / (across ? across : 1);
-}
 
 // F: the storage type; T: the matrix instruction's.
 template <class F, class T, int PARTS>
@@ -730,7 +728,7 @@ struct Call {
             if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
             const StatsEpilogue epi{stats, target_logit, a.targets, a.ignore_index, a.vocab, v0, row0};
             if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
-            row0 += stat_rows_of(rows, a.ntokens, p.tile_n);
+            row0 += stat_rows_of(rows, p.tile_n);
         }
         auto join = [&](auto kernel, uint32_t tokens) {
             hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>((a.ntokens + tokens - 1) / tokens)), dim3(kJoinBlock), 0,
@@ -950,8 +948,8 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     // in pieces, or, where the weight is read as it lies, in as few launches as there can be
     for (const uint64_t rows : {p.piece, most_tiles(ntokens, p.tile_n) * kTileM}) {
         const uint64_t full = vocab / rows, rest = vocab % rows;
-        p.stat_rows = std::max(p.stat_rows, full * stat_rows_of(rows, ntokens, p.tile_n) +
-                                                (rest ? stat_rows_of(rest, ntokens, p.tile_n) : 0));
+        p.stat_rows = std::max(p.stat_rows, full * stat_rows_of(rows, p.tile_n) +
+                                                (rest ? stat_rows_of(rest, p.tile_n) : 0));
     }
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {

@@ -269,9 +269,7 @@ template <int MT, int NT>
 __device__ __forceinline__ void read_few(i32x4 (&a)[MT][2], i32x4 (&b)[NT][2], uint32_t a0, uint32_t a1, uint32_t b0,
                                          uint32_t b1)
 {
-    if constexpr (MT == 4 && NT == 2) {
-        read_fragments<0, 0>(a, b[0], b[1], a0, a1, b0, b1);
-    } else if constexpr (MT == 2 && NT == 2) {
+    if constexpr (MT == 2 && NT == 2) {
         asm volatile(
             "ds_read_b128 %0, %8\n"
             "ds_read_b128 %1, %9\n"
@@ -284,19 +282,6 @@ __device__ __forceinline__ void read_few(i32x4 (&a)[MT][2], i32x4 (&b)[NT][2], u
             "s_waitcnt lgkmcnt(0)"
             : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(b[0][0]), "=&v"(b[0][1]),
               "=&v"(b[1][0]), "=&v"(b[1][1])
-            : "v"(a0), "v"(a1), "v"(b0), "v"(b1)
-            : "memory");
-    } else if constexpr (MT == 2) {
-        static_assert(NT == 1, "");
-        asm volatile(
-            "ds_read_b128 %0, %6\n"
-            "ds_read_b128 %1, %7\n"
-            "ds_read_b128 %2, %6 offset:2048\n"
-            "ds_read_b128 %3, %7 offset:2048\n"
-            "ds_read_b128 %4, %8\n"
-            "ds_read_b128 %5, %9\n"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(a[0][0]), "=&v"(a[0][1]), "=&v"(a[1][0]), "=&v"(a[1][1]), "=&v"(b[0][0]), "=&v"(b[0][1])
             : "v"(a0), "v"(a1), "v"(b0), "v"(b1)
             : "memory");
     } else {
@@ -432,31 +417,33 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
 // ---------------------------------------------------------------------------
 // few rows of B
 // ---------------------------------------------------------------------------
-// The time is that of reading A once: stages of 128 bytes a row, all but one of
-// them in flight, each waited for when it is due. 256 rows of A and 16 or 64 of
-// B with four stages (120 KiB in flight a CU), or 64 rows of A with six, where
-// the larger tiles are fewer than the CUs. fp32 rows are read as they are:
-// their matrix instructions' 157 TFLOP/s keep up with the memory here. 65536 x
-// 2048 fp16 for 3 rows of B: 43 us from the last-level cache, about 52 from HBM.
+// The time is that of reading A once: 64 rows of A and 16 or 64 of B, stages of
+// 128 bytes a row, all but one of them in flight, each waited for when it is
+// due; two workgroups a CU, so that one starts or ends while the other reads.
+// fp32 rows are read as they are: their matrix instructions' 157 TFLOP/s keep
+// up with the memory here. From HBM, microseconds a loss, against tiles of 256
+// rows (and four stages, one workgroup a CU): 3 tokens x 65536 x 2048 fp16 57
+// against 67, 1 x 128256 x 2048 bf16 101 against 123, 40 x 65536 x 2048 fp16 65
+// against 70; 16 x 131072 x 4096 bf16 185 against 179.
 constexpr int kFewM = 64;
 
-template <int BM, int BN>
+template <int BN>
 struct FewShape {
-    static_assert((BM == kTileM || BM == kFewM) && (BN == 16 || BN == 64), "tiles");
-    static constexpr int kThreads = BM == kTileM ? 512 : 256, kWaves = kThreads / 64;
-    static constexpr int kRows = kThreads / 8;                    // of one load
-    static constexpr int kRowsB = BN > kRows ? BN : kRows;        // every wave has as many loads in flight
-    static constexpr int kLoadsA = BM / kRows, kLoadsB = kRowsB / kRows;
-    static constexpr int kStages = BM == kTileM ? 4 : 6;
-    static constexpr uint32_t kB = BM * 128, kStage = kB + kRowsB * 128;
-    static constexpr int WN = BN == 16 ? 1 : 2, WM = kWaves / WN;  // waves
-    static constexpr int MT = BM / (16 * WM), NT = BN / (16 * WN);
+    static_assert(BN == 16 || BN == 64, "tiles");
+    static constexpr int kThreads = 256;
+    static constexpr int kRows = kThreads / 8;              // of one load
+    static constexpr int kRowsB = BN > kRows ? BN : kRows;  // every wave has as many loads in flight
+    static constexpr int kLoadsA = kFewM / kRows, kLoadsB = kRowsB / kRows;
+    static constexpr int kStages = BN == 16 ? 6 : 4;
+    static constexpr uint32_t kB = kFewM * 128, kStage = kB + kRowsB * 128;
+    static constexpr int WN = BN == 16 ? 1 : 2, WM = 4 / WN;  // waves
+    static constexpr int MT = kFewM / (16 * WM), NT = BN / (16 * WN);
 };
 
-template <class T, int BM, int BN, int THREADS, class Epilogue>
-__global__ __launch_bounds__(THREADS) void gemm_few(const GemmArgs g, const Epilogue epi)
+template <class T, int BN, class Epilogue>
+__global__ __launch_bounds__(256, 2) void gemm_few(const GemmArgs g, const Epilogue epi)
 {
-    using S = FewShape<BM, BN>;
+    using S = FewShape<BN>;
     constexpr int MT = S::MT, NT = S::NT;
     __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStage];
     uint32_t tm, tn, split;
@@ -465,7 +452,7 @@ __global__ __launch_bounds__(THREADS) void gemm_few(const GemmArgs g, const Epil
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t wm = wave / S::WN, wn = wave % S::WN;
-    const uint32_t m_base = tm * BM, n_base = tn * BN;
+    const uint32_t m_base = tm * kFewM, n_base = tn * BN;
     const uint32_t k0 = split * g.k;
     const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
     constexpr uint32_t EB = sizeof(typename T::Elem), kDepth = 128 / EB;
@@ -774,29 +761,14 @@ hipError_t launch_gemm_pieces(GemmArgs g, const Epilogue& epi, hipStream_t strea
     return hipGetLastError();
 }
 
-// Rows of A a tile: small ones where the large ones would leave CUs idle.
-inline uint32_t few_tile_m(uint64_t m, uint64_t n, uint64_t splits, uint64_t tile_n)
-{
-    constexpr uint64_t kCUs = 256;
-    return (m + kTileM - 1) / kTileM * ((n + tile_n - 1) / tile_n) * splits < kCUs ? kFewM : kTileM;
-}
-
-template <class T, int BM, int BN, class Epilogue>
-hipError_t launch_few_tiles(GemmArgs g, const Epilogue& epi, hipStream_t stream)
-{
-    g.tiles_m = (g.m + BM - 1) / BM;
-    g.tiles_n = (g.n + BN - 1) / BN;
-    constexpr int kThreads = FewShape<BM, BN>::kThreads;
-    hipLaunchKernelGGL((gemm_few<T, BM, BN, kThreads, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits),
-                       dim3(kThreads), 0, stream, g, epi);
-    return hipGetLastError();
-}
-
 template <class T, int BN, class Epilogue>
-hipError_t launch_gemm_few(const GemmArgs& g, const Epilogue& epi, hipStream_t stream)
+hipError_t launch_gemm_few(GemmArgs g, const Epilogue& epi, hipStream_t stream)
 {
-    return few_tile_m(g.m, g.n, g.splits, BN) == kFewM ? launch_few_tiles<T, kFewM, BN>(g, epi, stream)
-                                                       : launch_few_tiles<T, kTileM, BN>(g, epi, stream);
+    g.tiles_m = (g.m + kFewM - 1) / kFewM;
+    g.tiles_n = (g.n + BN - 1) / BN;
+    hipLaunchKernelGGL((gemm_few<T, BN, Epilogue>), dim3(g.tiles_m * g.tiles_n * g.splits), dim3(FewShape<BN>::kThreads),
+                       0, stream, g, epi);
+    return hipGetLastError();
 }
 
 template <class T, class Epilogue>
