@@ -221,7 +221,7 @@ private:
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (at == 16 * i + r) target_logit[t] = acc.v[i][j][r];
+                    if (at == static_cast<uint32_t>(16 * i + r)) target_logit[t] = acc.v[i][j][r];
         }
     }
 };
@@ -337,7 +337,7 @@ struct DEpilogue {
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] -= at == 16 * i + r ? kDScale : 0.0f;
+                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] -= at == static_cast<uint32_t>(16 * i + r) ? kDScale : 0.0f;
             }
             if (m0 + MT * 16 > g.m) {  // zeros below the vocabulary
 #pragma unroll
