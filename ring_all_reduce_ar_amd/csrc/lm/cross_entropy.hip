@@ -85,16 +85,17 @@ __device__ __forceinline__ void put8(char* row, uint64_t k, const Raw (&x)[8])
     }
 }
 
-// Eight elements from a 16-byte boundary, or one by one as far as they go.
-template <class Raw, bool VEC>
+// Eight elements by loads of A bytes (the rows' alignment), as far as they go.
+template <class Raw, int A>
 __device__ __forceinline__ void get8(const void* in, uint64_t at, uint64_t left, Raw (&x)[8])
 {
-    if constexpr (VEC) {
+    if constexpr (A > static_cast<int>(sizeof(Raw))) {
         if (left >= 8) {
-            constexpr int N = sizeof(Raw) / 2;
-            u32x4 v[N];
+            using Unit = typename std::conditional<A == 16, u32x4, u32x2>::type;
+            constexpr int N = sizeof(x) / A;
+            Unit v[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = ldv_at<false>(in, at * sizeof(Raw) + i * 16);
+            for (int i = 0; i < N; ++i) v[i] = gptr<Unit>(static_cast<const char*>(in) + at * sizeof(Raw))[i];
             __builtin_memcpy(x, v, sizeof(x));
             return;
         }
@@ -109,7 +110,7 @@ constexpr uint64_t operand_bytes() { return PARTS == 1 ? sizeof(Raw) : kPieces *
 
 // out[r] = in[r] in pieces (or as it is, on a 16-byte boundary), zeros from
 // `width` up to `pad`. `lanes` (a power of two) threads a row.
-template <int PARTS, class Raw, bool VEC>
+template <int PARTS, class Raw, int A>
 __global__ __launch_bounds__(kBlock) void pack_rows(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
                                                     uint64_t pad, char* out, int lanes)
 {
@@ -117,7 +118,7 @@ __global__ __launch_bounds__(kBlock) void pack_rows(const void* in, uint64_t ld,
     if (r >= rows) return;
     for (uint64_t c = (threadIdx.x & (lanes - 1)) * 8ull; c < pad; c += lanes * 8ull) {
         Raw x[8];
-        get8<Raw, VEC>(in, r * ld + c, c < width ? width - c : 0, x);
+        get8<Raw, A>(in, r * ld + c, c < width ? width - c : 0, x);
         put8<PARTS>(out + r * pad * operand_bytes<PARTS, Raw>(), c, x);
     }
 }
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(kBlock) void pack_rows(const void* in, uint64_t ld,
 // multiple of 8) and in rows whose target is ignored (whatever they hold).
 // 64 x 64 tiles through LDS; a lane takes eight rows of one column, eight lanes
 // 128 bytes of 16-bit elements.
-template <int PARTS, class Raw, bool VEC>
+template <int PARTS, class Raw, int A>
 __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64_t ld, uint64_t rows, uint64_t width,
                                                           uint64_t pad, char* out, Indices targets, int masked,
                                                           int64_t ignore, uint64_t vocab)
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(kBlock) void pack_transposed(const void* in, uint64
         const uint64_t r = r0 + row, c = c0 + slot * 8;
         Raw x[8] = {};
         if (r < rows && c < width && (!masked || load_target(targets, r, ignore, vocab) >= 0))
-            get8<Raw, VEC>(in, r * ld + c, width - c, x);
+            get8<Raw, A>(in, r * ld + c, width - c, x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) tile[row][slot * 8 + k] = x[k];
     }
@@ -564,27 +565,31 @@ dim3 grid_for(uint64_t rows, int lanes)
 template <int PARTS, class Raw>
 hipError_t pack(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, char* out, hipStream_t s)
 {
-    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * sizeof(Raw) % 16 == 0;
+    const uintptr_t mis = reinterpret_cast<uintptr_t>(in) | ld * sizeof(Raw);
     const int lanes = lanes_for(pad / 8);
     auto launch = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid_for(rows, lanes), dim3(kBlock), 0, s, in, ld, rows, width, pad, out, lanes);
         return hipGetLastError();
     };
-    return vec ? launch(pack_rows<PARTS, Raw, true>) : launch(pack_rows<PARTS, Raw, false>);
+    return mis % 16 == 0  ? launch(pack_rows<PARTS, Raw, 16>)
+           : mis % 8 == 0 ? launch(pack_rows<PARTS, Raw, 8>)
+                          : launch(pack_rows<PARTS, Raw, sizeof(Raw)>);
 }
 
 template <int PARTS, class Raw>
 hipError_t transpose(const void* in, uint64_t ld, uint64_t rows, uint64_t width, uint64_t pad, char* out,
                      const CrossEntropyArgs& a, int masked, hipStream_t s)
 {
-    const bool vec = reinterpret_cast<uintptr_t>(in) % 16 == 0 && ld * sizeof(Raw) % 16 == 0;
+    const uintptr_t mis = reinterpret_cast<uintptr_t>(in) | ld * sizeof(Raw);
     const dim3 grid(static_cast<uint32_t>((pad + 63) / 64 * ((width + 63) / 64)));
     auto launch = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, s, in, ld, rows, width, pad, out, a.targets, masked,
                            a.ignore_index, a.vocab);
         return hipGetLastError();
     };
-    return vec ? launch(pack_transposed<PARTS, Raw, true>) : launch(pack_transposed<PARTS, Raw, false>);
+    return mis % 16 == 0  ? launch(pack_transposed<PARTS, Raw, 16>)
+           : mis % 8 == 0 ? launch(pack_transposed<PARTS, Raw, 8>)
+                          : launch(pack_transposed<PARTS, Raw, sizeof(Raw)>);
 }
 
 template <class T, int PARTS, class Epilogue>
