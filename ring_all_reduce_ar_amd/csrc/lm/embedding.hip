@@ -30,56 +30,65 @@ __device__ __forceinline__ uint64_t row_of(const Indices& x, uint64_t t, int64_t
     return r < rows ? r : rows;
 }
 
+// Sixteen bytes at any address (a row of odd width starts anywhere): the
+// hardware takes a vector access at an element's alignment.
+__device__ __forceinline__ u32x4 load16(const void* base, uint64_t byte)
+{
+    u32x4 v;
+    __builtin_memcpy(&v, gptr<char>(base) + byte, 16);
+    return v;
+}
+__device__ __forceinline__ void store16(void* base, uint64_t byte, u32x4 v)
+{
+    __builtin_memcpy(gptr<char>(base) + byte, &v, 16);
+}
+
 // ---------------------------------------------------------------------------
 // lookup
 // ---------------------------------------------------------------------------
 // `lanes` (a power of two up to kBlock) threads a row, kBlock / lanes rows a
-// workgroup; VEC: 16-byte vectors, else elements. Stores are cached: with
-// non-temporal ones 16384 x 4096 fp16 returns in 30 us rather than 44, but what
-// reads the rows next ends 11 us later (of 80), and so at every size from 32 MiB on.
-template <class F, bool VEC>
+// workgroup, 16 bytes a thread and what is left of a row by elements. Stores are
+// cached: with non-temporal ones 16384 x 4096 fp16 returns in 30 us rather than
+// 44, but what reads the rows next ends 11 us later (of 80), and so at every size
+// from 32 MiB on. Rows that do not lie on 16 bytes: 16384 x 4093 fp16 in 58 us,
+// where elements take 101.
+template <class F>
 __global__ __launch_bounds__(kBlock) void lookup(const LookupArgs a, int lanes)
 {
-    constexpr int E = F::kEpv;
+    constexpr int E = F::kEpv, EB = 16 / E;
     const int per = kBlock / lanes;
-    const uint64_t units = VEC ? a.width / E : a.width;
     const int lane = threadIdx.x & (lanes - 1);
     for (uint64_t t = static_cast<uint64_t>(blockIdx.x) * per + threadIdx.x / lanes; t < a.ntokens;
          t += static_cast<uint64_t>(gridDim.x) * per) {
         const uint64_t row = row_of(a.tokens, t, a.first_row, a.rows);
         const bool here = row < a.rows;
         const uint64_t src = (here ? row : 0) * a.ld_weight, dst = t * a.ld_out;
-        for (uint64_t c = lane; c < units; c += lanes) {
-            if constexpr (VEC) {
+        for (uint64_t c = static_cast<uint64_t>(lane) * E; c < a.width; c += static_cast<uint64_t>(lanes) * E) {
+            if (c + E <= a.width) {
                 float x[E];
                 u32x4 v = {0, 0, 0, 0};
-                if (here) v = ldv_at<false>(a.weight, src * (16 / E) + c * 16);
+                if (here) v = load16(a.weight, (src + c) * EB);
                 F::unpack(v, x);
 #pragma unroll
-                for (int j = 0; j < E; ++j) x[j] *= a.scale;
-                if (!here) {
-#pragma unroll
-                    for (int j = 0; j < E; ++j) x[j] = 0.0f;
-                }
-                stv_at<false>(a.out, dst * (16 / E) + c * 16, F::pack(x));
+                for (int j = 0; j < E; ++j) x[j] = here ? x[j] * a.scale : 0.0f;
+                store16(a.out, (dst + c) * EB, F::pack(x));
             } else {
-                F::st(a.out, dst + c, here ? F::ld(a.weight, src + c) * a.scale : 0.0f);
+                for (uint64_t k = c; k < a.width; ++k) F::st(a.out, dst + k, here ? F::ld(a.weight, src + k) * a.scale : 0.0f);
             }
         }
     }
 }
 
 template <class F>
-hipError_t lookup_launch(const LookupArgs& a, bool vec, hipStream_t s)
+hipError_t lookup_launch(const LookupArgs& a, hipStream_t s)
 {
-    const uint64_t units = vec ? a.width / F::kEpv : a.width;
+    const uint64_t units = (a.width + F::kEpv - 1) / F::kEpv;
     int lanes = 1;
     while (lanes < kBlock && static_cast<uint64_t>(lanes) < units) lanes *= 2;
     const uint64_t per = kBlock / lanes;
     const uint64_t want = (a.ntokens + per - 1) / per;
     const int grid = static_cast<int>(want < (1u << 20) ? want : (1u << 20));
-    if (vec) hipLaunchKernelGGL((lookup<F, true>), dim3(grid), dim3(kBlock), 0, s, a, lanes);
-    else hipLaunchKernelGGL((lookup<F, false>), dim3(grid), dim3(kBlock), 0, s, a, lanes);
+    hipLaunchKernelGGL((lookup<F>), dim3(grid), dim3(kBlock), 0, s, a, lanes);
     return hipGetLastError();
 }
 
@@ -596,13 +605,12 @@ hipError_t grad_call(const LookupGradArgs& a, bool vec, bool nt, int num_cus, hi
 
 }  // namespace
 
-hipError_t launch_lookup(const LookupArgs& a, ar_dtype_t dtype, bool vec, int num_cus, hipStream_t stream)
+hipError_t launch_lookup(const LookupArgs& a, ar_dtype_t dtype, hipStream_t stream)
 {
-    (void)num_cus;
     switch (dtype) {
-    case AR_FLOAT32: return lookup_launch<F32>(a, vec, stream);
-    case AR_FLOAT16: return lookup_launch<F16>(a, vec, stream);
-    case AR_BFLOAT16: return lookup_launch<BF16>(a, vec, stream);
+    case AR_FLOAT32: return lookup_launch<F32>(a, stream);
+    case AR_FLOAT16: return lookup_launch<F16>(a, stream);
+    case AR_BFLOAT16: return lookup_launch<BF16>(a, stream);
     default: return hipErrorInvalidValue;
     }
 }

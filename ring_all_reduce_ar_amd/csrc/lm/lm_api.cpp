@@ -470,8 +470,7 @@ AR_EXPORT ar_result_t ar_embedding(ar_comm_t comm, const void* weight, const voi
         if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");
         const ar::lm::LookupArgs a{weight, out,       {tokens, index == AR_INDEX_INT64}, ntokens, rows, width,
                                    ld_weight, ld_out, first_row,                         scale};
-        const bool vec = width * e % 16 == 0 && rows16(out, ld_out, e) && (rows == 0 || rows16(weight, ld_weight, e));
-        const hipError_t err = ar::lm::launch_lookup(a, dtype, vec, comm->num_cus, stream);
+        const hipError_t err = ar::lm::launch_lookup(a, dtype, stream);
         return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
     });
 }

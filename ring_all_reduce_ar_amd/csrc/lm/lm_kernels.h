@@ -64,7 +64,7 @@ struct LookupArgs {
     int64_t first_row;
     float scale;
 };
-hipError_t launch_lookup(const LookupArgs& a, ar_dtype_t dtype, bool vec, int num_cus, hipStream_t stream);
+hipError_t launch_lookup(const LookupArgs& a, ar_dtype_t dtype, hipStream_t stream);
 
 // The sort: at most kSortBlocks workgroups of kSortThreads threads, digits of
 // at most 9 bits. The sum: a chunk of positions of the sorted order for at least
