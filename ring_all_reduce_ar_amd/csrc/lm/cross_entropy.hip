@@ -228,7 +228,7 @@ __device__ __forceinline__ Stats join_parts(Stats a, Stats b)
 // Joins the parts of each token's row: X tokens a workgroup, kJoinBlock / X
 // threads for each. Neighbouring tokens lie side by side, so many tokens take
 // 16 (128 bytes) and few tokens as few as there are, for more threads to a
-// row: 3 tokens with 2048 parts in 5 us rather than 38.
+// row: the loss of 3 x 65536 x 2048 fp16 takes 71 us rather than 110 with 16.
 constexpr int kJoinBlock = 512;
 template <int X>
 __global__ __launch_bounds__(kJoinBlock) void join_stats(const Stats* stats, uint64_t stat_rows,
@@ -693,7 +693,7 @@ struct Call {
     template <bool WEIGHT>
     hipError_t finish(const float* sums, int splits, const RowScale* scale, uint64_t rows, void* out, uint64_t ld) const
     {
-        // (few results take a thread each: 6 x 256 of 128 splits in 8 us rather than 37)
+        // (few results take a thread each: 6 x 256 of 64 parts in 5 us, by vectors and of 128 parts in 37)
         const bool vec = a.width % F::kEpv == 0 && ld % F::kEpv == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                          rows * a.width >= (1u << 18);
         const int lanes = lanes_for(vec ? a.width / F::kEpv : a.width);

@@ -595,6 +595,9 @@ hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
     return hipGetLastError();
 }
 
+// Rows that do not lie on 16 bytes are summed by elements: by vectors at any
+// address 23784 x 3549 bf16 takes 108 us rather than 99, 8191 x 1027 74 rather
+// than 69.
 template <class F, class G>
 hipError_t grad_call(const LookupGradArgs& a, bool vec, bool nt, int num_cus, hipStream_t s)
 {
