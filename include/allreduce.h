@@ -394,7 +394,10 @@ size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, siz
  * A token whose target is ignore_index or outside [0, vocab) is ignored: its
  * loss is 0 (its lse is still given). Products of fp16 and bf16 are summed in
  * fp32; fp32 products are exact to 2^-24 (fp32 matrix instructions up to 64
- * tokens, else bf16 pieces that hold all 24 bits). losses and lse are fp32.
+ * tokens, else bf16 pieces that hold all 24 bits; 2^-21 where both factors are
+ * of 256 or more). Products with an infinity, and beyond fp32's range, are the
+ * infinity of their sign: a logit of -infinity adds nothing to lse, one of
+ * +infinity, or a NaN, makes the token's lse and loss NaN. losses and lse are fp32.
  * ntokens and width are below 2^24, of fp32 below 2^20. Operands whose rows are
  * on 16-byte boundaries and whole multiples of 16 bytes long are read as they
  * lie (fp32 only up to 64 tokens); others are first laid out in the workspace,

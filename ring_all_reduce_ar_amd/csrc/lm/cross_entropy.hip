@@ -60,9 +60,16 @@ __device__ __forceinline__ void put8(char* row, uint64_t k, const Raw (&x)[8])
 #pragma unroll
         for (uint32_t i = 0; i < sizeof(x) / 16; ++i) *reinterpret_cast<u32x4*>(row + k * sizeof(Raw) + i * 16) = v[i];
     } else {
-        uint32_t p[4][3];
+        uint32_t p[4][3], top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_pair(x[2 * i], x[2 * i + 1], p[i]);
+        for (int i = 0; i < 8; ++i) top = max(top, as_u(x[i]) & 0x7FFFFFFFu);
+        if (top < as_u(kCutFrom)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_pair(x[2 * i], x[2 * i + 1], p[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_pair_any(x[2 * i], x[2 * i + 1], p[i]);
+        }
         char* at = row + (k / kPieceDepth) * (kPieceDepth * kPieces * 2) + k % kPieceDepth * 2;
 #pragma unroll
         for (int q = 0; q < kPieces; ++q)

@@ -520,23 +520,47 @@ __global__ __launch_bounds__(256, 2) void gemm_few(const GemmArgs g, const Epilo
 // ---------------------------------------------------------------------------
 // x = x1 + x2 + x3 with 8 significant bits each. A row holds, for each 32 of
 // its depth, 32 first pieces, 32 second and 32 third ones (192 bytes). Six of
-// the nine products of pieces are summed: the other three are below 2^-24 of
-// the whole.
+// the nine products of pieces are summed, smallest first: 3 1, 2 2, 1 3, 2 1, 1 2,
+// 1 1. The other three are below 2^-24 of the whole.
 constexpr int kPieces = 3;
 constexpr int kPieceDepth = 32;
 constexpr int kPiecesN = 128;  // columns of a tile
 
-// The pieces of two floats, the first in the low halves; a value that is no
-// number stays in its first piece.
+// The first or the second of two 16-bit pieces, as floats.
+__device__ __forceinline__ float low_piece(uint32_t w) { return detail::as_f(w << 16); }
+__device__ __forceinline__ float high_piece(uint32_t w) { return detail::as_f(w & 0xFFFF0000u); }
+
+// The pieces of two floats below kCutFrom (or of d, whose other factors these
+// are), the first in the low halves.
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&p)[3])
 {
-    auto low = [](uint32_t w) { return detail::as_f(w << 16); };
-    auto high = [](uint32_t w) { return detail::as_f(w & 0xFFFF0000u); };
     p[0] = MmaBF16::pack2(x, y);
-    const float rx = __builtin_isfinite(low(p[0])) ? x - low(p[0]) : 0.0f;
-    const float ry = __builtin_isfinite(high(p[0])) ? y - high(p[0]) : 0.0f;
+    const float rx = x - low_piece(p[0]), ry = y - high_piece(p[0]);
     p[1] = MmaBF16::pack2(rx, ry);
-    p[2] = MmaBF16::pack2(rx - low(p[1]), ry - high(p[1]));
+    p[2] = MmaBF16::pack2(rx - low_piece(p[1]), ry - high_piece(p[1]));
+}
+
+// The pieces of any two floats. From kCutFrom on a number is cut rather than
+// rounded to its pieces: the largest ones would round to an infinity, and pieces
+// of one sign leave no product beyond fp32's range with infinities of both (x1
+// y2 of a y below kCutFrom stays within the range). The products left out are
+// then below 2^-21 where both factors are cut. An infinity is the third piece,
+// which meets the other factor's first alone, beside a first piece of +-1: its
+// products are the infinity of their sign, and no number with a zero.
+constexpr float kCutFrom = 256.0f;
+__device__ __forceinline__ void split_pair_any(float x, float y, uint32_t (&p)[3])
+{
+    auto cut = [](float v) { return detail::as_f(detail::as_u(v) & 0xFFFF0000u); };
+    auto first = [&](float v) {
+        return __builtin_isinf(v) ? __builtin_copysignf(1.0f, v) : __builtin_fabsf(v) >= kCutFrom ? cut(v) : v;
+    };
+    auto second = [&](float v, float rest) {
+        return __builtin_isinf(rest) ? 0.0f : __builtin_fabsf(v) >= kCutFrom ? cut(rest) : rest;
+    };
+    p[0] = MmaBF16::pack2(first(x), first(y));
+    const float rx = x - low_piece(p[0]), ry = y - high_piece(p[0]);
+    p[1] = MmaBF16::pack2(second(x, rx), second(y, ry));
+    p[2] = MmaBF16::pack2(rx - low_piece(p[1]), ry - high_piece(p[1]));
 }
 
 // Twelve fragments: two groups of 16 rows at x and two at y, three pieces each.
