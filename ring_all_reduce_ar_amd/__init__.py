@@ -176,10 +176,12 @@ def _ptrs(bufs):
     t = _PTR_ARRAY_TYPES.get(n)
     if t is None:
         t = _PTR_ARRAY_TYPES[n] = ctypes.c_void_p * n
-    if n and type(bufs[0]) is int and type(bufs) in (list, tuple):
-        try:  # addresses alone: many times faster than one ctypes object each
+    # Addresses alone: many times faster than one ctypes object each. Every element
+    # is looked at: an array takes an integer tensor of one element by its value.
+    if set(map(type, bufs)) == {int}:
+        try:
             return t.from_buffer(array.array("Q", bufs))
-        except (TypeError, OverflowError):
+        except OverflowError:
             pass
     return t(*[b if type(b) is int else _addr(b) for b in bufs])
 
