@@ -137,12 +137,28 @@ private:
     std::vector<ar::MultiArgs> list_;
 };
 
-// Tensor t of rank r, checked: pointers, alignment, sizes, overlaps.
-// `recv` may be null (a norm alone); `rank0_only`: only rank 0's send
-// pointers are read.
+// What is written may overlap neither what else is written nor what is read;
+// inputs may overlap each other.
+ar_result_t check_disjoint(const std::vector<Interval>& reads, const std::vector<Interval>& writes)
+{
+    for (size_t i = 0; i < writes.size(); ++i) {
+        auto hits = [&](const Interval& x) {
+            return x.hi > x.lo && writes[i].hi > writes[i].lo && x.lo < writes[i].hi && writes[i].lo < x.hi;
+        };
+        for (const Interval& x : reads)
+            if (hits(x)) return fail(AR_ERR_INVALID_ARGUMENT, "%s overlaps %s", writes[i].what, x.what);
+        for (size_t k = i + 1; k < writes.size(); ++k)
+            if (hits(writes[k])) return fail(AR_ERR_INVALID_ARGUMENT, "%s overlaps %s", writes[i].what, writes[k].what);
+    }
+    return AR_SUCCESS;
+}
+
+// Tensor t of rank r, checked: pointers, alignment, sizes, overlaps (with
+// norm_out and the workspace too). `recv` may be null (a norm alone);
+// `rank0_only`: only rank 0's send pointers are read.
 ar_result_t check_tensors(const ar_comm* comm, int ntensors, const void* const send[], void* const recv[],
-                          const size_t counts[], ar_dtype_t dtype, bool rank0_only, uint64_t* total,
-                          uint64_t* touched)
+                          const size_t counts[], ar_dtype_t dtype, bool rank0_only, const float* norm_out,
+                          uint64_t* total, uint64_t* touched)
 {
     if (ntensors < 0 || ntensors > AR_MAX_TENSORS)
         return fail(AR_ERR_INVALID_ARGUMENT, "ntensors %d is outside 0..%d", ntensors, AR_MAX_TENSORS);
@@ -168,6 +184,7 @@ ar_result_t check_tensors(const ar_comm* comm, int ntensors, const void* const s
             // What is only read may be read twice; what is written may
             // overlap nothing but its own send tensor.
             if (!recv) {
+                if (!rank0_only || r == 0) iv.push_back({s, s + bytes, "gradient", t});
                 *touched += bytes;
                 continue;
             }
@@ -179,15 +196,16 @@ ar_result_t check_tensors(const ar_comm* comm, int ntensors, const void* const s
             }
         }
     }
-    if (recv) {
-        for (const Interval& x : iv) *touched += x.hi - x.lo;
-        size_t oa, ob;
-        const uintptr_t w = reinterpret_cast<uintptr_t>(comm->ws);
-        iv.push_back({w, w + sizeof(ar::lm::ClipWorkspace), "workspace", -1});
-        if (find_overlap(iv, &oa, &ob))
-            return fail(AR_ERR_INVALID_ARGUMENT, "%s %d overlaps %s %d (only send == recv may alias)", iv[oa].what,
-                        iv[oa].rank, iv[ob].what, iv[ob].rank);
-    }
+    const uintptr_t w = reinterpret_cast<uintptr_t>(comm->ws), norm = reinterpret_cast<uintptr_t>(norm_out);
+    std::vector<Interval> own = {{w, w + sizeof(ar::lm::ClipWorkspace), "workspace", -1}};
+    if (norm_out) own.push_back({norm, norm + sizeof(float), "norm_out", -1});
+    if (!recv) return check_disjoint(iv, own);
+    for (const Interval& x : iv) *touched += x.hi - x.lo;
+    iv.insert(iv.end(), own.begin(), own.end());
+    size_t oa, ob;
+    if (find_overlap(iv, &oa, &ob))
+        return fail(AR_ERR_INVALID_ARGUMENT, "%s %d overlaps %s %d (only send == recv may alias)", iv[oa].what,
+                    iv[oa].rank, iv[ob].what, iv[ob].rank);
     return AR_SUCCESS;
 }
 
@@ -252,7 +270,8 @@ ar_result_t clip_impl(ar_comm* comm, int ntensors, const void* const send[], voi
     if (!writes && !norm_out) return fail(AR_ERR_INVALID_ARGUMENT, "norm_out is NULL");
     uint64_t total, touched;
     const bool replicated = layout == AR_GRADS_REPLICATED;
-    rc = check_tensors(comm, ntensors, send, writes ? recv : nullptr, counts, dtype, replicated, &total, &touched);
+    rc = check_tensors(comm, ntensors, send, writes ? recv : nullptr, counts, dtype, replicated, norm_out, &total,
+                       &touched);
     if (rc != AR_SUCCESS) return rc;
     const int n = comm->nranks;
     const size_t e = elem_size(dtype);
@@ -295,22 +314,6 @@ ar_result_t check_matrix(const char* what, const void* p, uint64_t rows, uint64_
     if (a % elem) return fail(AR_ERR_INVALID_ARGUMENT, "%s is not aligned to %zu bytes", what, elem);
     if (a > UINTPTR_MAX - bytes) return fail(AR_ERR_INVALID_ARGUMENT, "%s wraps the address space", what);
     if (iv) iv->push_back({a, a + bytes, what, 0});
-    return AR_SUCCESS;
-}
-
-// What is written may overlap neither what else is written nor what is read;
-// inputs may overlap each other.
-ar_result_t check_disjoint(const std::vector<Interval>& reads, const std::vector<Interval>& writes)
-{
-    for (size_t i = 0; i < writes.size(); ++i) {
-        auto hits = [&](const Interval& x) {
-            return x.hi > x.lo && writes[i].hi > writes[i].lo && x.lo < writes[i].hi && writes[i].lo < x.hi;
-        };
-        for (const Interval& x : reads)
-            if (hits(x)) return fail(AR_ERR_INVALID_ARGUMENT, "%s overlaps %s", writes[i].what, x.what);
-        for (size_t k = i + 1; k < writes.size(); ++k)
-            if (hits(writes[k])) return fail(AR_ERR_INVALID_ARGUMENT, "%s overlaps %s", writes[i].what, writes[k].what);
-    }
     return AR_SUCCESS;
 }
 
@@ -425,7 +428,7 @@ AR_EXPORT ar_result_t ar_all_reduce_clip(ar_comm_t comm, int ntensors, const voi
         if (!valid_op(op)) return fail(AR_ERR_INVALID_ARGUMENT, "invalid op %d", static_cast<int>(op));
         if (op != AR_SUM && op != AR_AVG) return fail(AR_ERR_UNSUPPORTED, "gradients are clipped after AR_SUM or AR_AVG");
         uint64_t total, touched;
-        rc = check_tensors(comm, ntensors, sendbufs, recvbufs, counts, dtype, false, &total, &touched);
+        rc = check_tensors(comm, ntensors, sendbufs, recvbufs, counts, dtype, false, norm_out, &total, &touched);
         if (rc != AR_SUCCESS) return rc;
         const int n = comm->nranks;
         const size_t e = elem_size(dtype);
