@@ -342,8 +342,9 @@ ar_result_t ar_grad_norm(ar_comm_t comm, int ntensors, const void* const grads[]
  * 1e-6)), the factor rounded once to fp32 and the product once to dtype. An
  * infinite norm gives the factor 0 (finite elements become 0, infinite ones
  * NaN), a NaN norm makes every element NaN; norm_out (device, may be NULL)
- * tells. max_norm: at least 0, may be infinite. In place per tensor and rank
- * (send == recv) is allowed. */
+ * tells. max_norm: at least 0; an infinite one clips nothing (the factor is 1,
+ * of an infinite norm too). In place per tensor and rank (send == recv) is
+ * allowed. */
 ar_result_t ar_clip_grads(ar_comm_t comm, int ntensors, const void* const sendbufs[], void* const recvbufs[],
                           const size_t counts[], ar_dtype_t dtype, ar_grads_t layout, ar_norm_t norm, double max_norm,
                           float* norm_out, hipStream_t stream);

@@ -71,6 +71,7 @@ __device__ __forceinline__ double norm_of(double joined, int inf) { return inf ?
 
 __device__ __forceinline__ float scale_of(double total, double max_norm)
 {
+    if (__builtin_isinf(max_norm) && !__builtin_isnan(total)) return 1.0f;  // no limit, also of an infinite norm
     const double s = max_norm / (total + kClipEps);
     return static_cast<float>(s > 1.0 ? 1.0 : s);  // a NaN stays one
 }

@@ -115,3 +115,34 @@ def test_products_of_large_fp32_numbers(comms, n, vocab):  # noqa: F811
     z, ez, rl, el, rloss, eloss, kept, at = loss_ref(x, w, y, -100)
     close(lse, rl, el, "lse")
     close(losses, rloss, eloss, "losses")
+
+
+# ---------------------------------------------------------------------------
+# clip
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("norm", ["l2", "inf"])
+@pytest.mark.parametrize("size", [1000, 2_000_001])  # partial norms joined by every workgroup, and by a launch
+def test_no_limit_clips_nothing(comms, dtype, norm, size):  # noqa: F811
+    """An infinite max_norm leaves every element as it is, whatever the norm; of a
+    NaN norm it is NaN as by any limit."""
+    comm = comms(2)
+    out = torch.zeros(1, device="cuda")
+    for value in (1.0, math.inf, -math.inf, math.nan):
+        x = [[normal(gen(73), size, dtype=dtype) for _ in range(2)]]
+        x[0][1][77] = value
+        for call in ("sharded", "replicated", "reduce"):
+            y = [[nan_like(size, dtype=dtype) for _ in range(2)]]
+            if call == "reduce":
+                want = [[nan_like(size, dtype=dtype) for _ in range(2)]]
+                ar.ar_all_reduce_multi(comm, x, want, [size], dtype, "sum")
+                ar.ar_all_reduce_clip(comm, x, y, [size], math.inf, out, dtype, "sum", norm)
+            else:
+                want = x if call == "sharded" else [[x[0][0], x[0][0]]]
+                ar.ar_clip_grads(comm, x, y, [size], math.inf, out, dtype, call, norm)
+            for a, b in zip(y[0], want[0]):
+                if math.isnan(value) and call != "replicated":
+                    assert torch.isnan(a).all() and torch.isnan(out).all()
+                else:
+                    assert torch.equal(a, b)
+                    assert math.isinf(float(out)) == (math.isinf(value) and call != "replicated")
