@@ -818,23 +818,29 @@ struct Call {
 constexpr uint64_t kCUs = 256;
 constexpr uint64_t kMostSplits = 64;
 struct Shape {
-    uint64_t ntokens, width, tile_n, tile_w, step;  // tile_w: columns of the weight gradient's tiles
+    uint64_t ntokens, width;
+    uint64_t tile_m, tile_n;          // tiles of the logits' and the hidden gradient's product
+    uint64_t weight_m, weight_n;      // and of the weight gradient's
+    uint64_t step;
     bool pieces;
 };
 
 uint64_t up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // Tiles of a gradient's product with `other` rows.
-uint64_t gradient_tiles(const Shape& x, uint64_t other, uint64_t tile)
+uint64_t gradient_tiles(const Shape& x, uint64_t other, uint64_t tile_m, uint64_t tile_n)
 {
     return x.pieces && columns_in_b(x.width, other) ? up(x.width, kPiecesN) * up(other, kTileM)
-                                                    : up(x.width, kTileM) * up(other, tile);
+                                                    : up(x.width, tile_m) * up(other, tile_n);
 }
 
 // The best number of parts for a sum over `depth` with so many tiles, and its
 // cost. A round costs about eight steps to start and to end in; parts are
 // written and read again, about two steps each; `join` is the cost of a launch
-// that only a split sum needs.
+// that only a split sum needs. One round of tiles of 64 rows is best too, though
+// two workgroups of them fit a CU: both gradients of 16 tokens x 32000 x 2048 bf16
+// take 163 us in 8 parts (256 workgroups), 181 in 4, 168 in 16, 174 in 32 and 230
+// unsplit, of 64 x 32000 x 4096 333 in 4 parts, 351 in 16, 432 unsplit.
 double split_cost(uint64_t tiles, uint64_t depth, uint64_t step, double join, int* splits)
 {
     double best = 0;
@@ -856,9 +862,10 @@ double split_cost(uint64_t tiles, uint64_t depth, uint64_t step, double join, in
 
 double piece_cost(const Shape& x, uint64_t rows, int* splits, int* weight_splits)
 {
-    return static_cast<double>(up(up(rows, kTileM) * up(x.ntokens, x.tile_n), kCUs) * (up(x.width, x.step) + 8)) +
-           split_cost(gradient_tiles(x, x.ntokens, x.tile_n), rows, x.step, 0, splits) +
-           split_cost(gradient_tiles(x, rows, x.tile_w), x.ntokens, x.step, 8, weight_splits) + 24;  // four launches
+    return static_cast<double>(up(up(rows, x.tile_m) * up(x.ntokens, x.tile_n), kCUs) * (up(x.width, x.step) + 8)) +
+           split_cost(gradient_tiles(x, x.ntokens, x.tile_m, x.tile_n), rows, x.step, 0, splits) +
+           split_cost(gradient_tiles(x, rows, x.weight_m, x.weight_n), x.ntokens, x.step, 8, weight_splits) +
+           24;  // four launches
 }
 
 // Whether tiles of 64 x 64 (a few hundred of them) end sooner than the few
@@ -910,7 +917,6 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     const uint64_t ob = p.pieces ? kPieces * 2 : f32 ? 4 : 2, step = f32 ? 32 : kTileK;
     p.k_pad = round_up(width, step);
     p.t_pad = round_up(ntokens, p.tile_n == 16 ? 16 : kTileK);  // the tiles cover it: they write its zeros
-    const uint64_t tile_w = p.pieces ? kPiecesN : f32 ? 64 : 256;
     p.pack_hidden = p.pack_weight = true;  // the caller clears these where the operands can be read as they lie
     // A piece's buffers come to at most kPieceBytes, or one tile's; pieces are whole tiles.
     const uint64_t row_bytes = ob * (p.k_pad + (backward ? 2 * p.t_pad + width : 0));
@@ -927,7 +933,9 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         // From half the largest size on, the one whose tiles fill the CUs best.
         // 8192 x 131072 x 4096: pieces of 16384 rows end in full rounds, of
         // 13312 the weight gradient's 832 tiles take four rounds for 3.25.
-        const Shape shape{ntokens, width, static_cast<uint64_t>(p.tile_n), tile_w, step, p.pieces};
+        const uint64_t tile_m = small ? kFewM : kTileM, tile_n = static_cast<uint64_t>(p.tile_n);
+        const Shape shape = f32 ? Shape{ntokens, width, tile_m, tile_n, tile_m, small ? 64u : tile_n, step, p.pieces}
+                                : Shape{ntokens, width, tile_m, tile_n, kTileM, 256, step, false};
         double best = 0;
         const uint64_t stride = most / 64 + 1;
         for (uint64_t m = most; m >= (most + 1) / 2 && m >= 1; m = m > stride ? m - stride : 0) {
