@@ -429,28 +429,32 @@ __device__ __forceinline__ void sum_chunks(const LookupGradArgs& a, uint32_t chu
     }
 }
 
+// `base`: the workgroups of earlier launches, here and below (see in_launches).
 template <class F, class G, int U, int K>
-__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t chunks, int sorted, uint32_t lanes,
-                                                   uint32_t bx)
+__global__ __launch_bounds__(kBlock) void grad_sum(const LookupGradArgs a, uint32_t base, uint32_t chunks, int sorted,
+                                                   uint32_t lanes, uint32_t bx)
 {
-    sum_chunks<F, G, U, K>(a, chunks, sorted, lanes, blockIdx.x % bx, blockIdx.x / bx);
+    const uint32_t id = base + blockIdx.x;
+    sum_chunks<F, G, U, K>(a, chunks, sorted, lanes, id % bx, id / bx);
 }
 
 // The sums and the zeros of at most kSortThreads tokens: the first bx * by
 // workgroups sum, the others fill the rows that are not among the sorted keys.
 template <class F, class G, int U, bool NT>
-__global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uint32_t chunks, uint32_t lanes,
-                                                     uint32_t bx, uint32_t by, uint32_t fill_lanes)
+__global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uint32_t base, uint32_t chunks,
+                                                     uint32_t lanes, uint32_t bx, uint32_t by, uint32_t fillers,
+                                                     uint32_t fill_lanes)
 {
-    if (blockIdx.x < bx * by) {
-        sum_chunks<F, G, U, kGradChunkFew>(a, chunks, 0, lanes, blockIdx.x % bx, blockIdx.x / bx);
+    const uint32_t id = base + blockIdx.x;
+    if (id < bx * by) {
+        sum_chunks<F, G, U, kGradChunkFew>(a, chunks, 0, lanes, id % bx, id / bx);
         return;
     }
     __shared__ uint32_t keys[kSortThreads];
     const uint32_t n = static_cast<uint32_t>(a.ntokens);
     for (uint32_t i = threadIdx.x; i < n; i += kBlock) keys[i] = a.key[0][i];
     __syncthreads();
-    fill_rows<G, NT, kBlock>(a, 0, a.rows, blockIdx.x - bx * by, gridDim.x - bx * by, fill_lanes, [&](uint64_t r) {
+    fill_rows<G, NT, kBlock>(a, 0, a.rows, id - bx * by, fillers, fill_lanes, [&](uint64_t r) {
         uint32_t lo = 0, hi = n;  // the first key that is not below r
         while (lo < hi) {
             const uint32_t mid = (lo + hi) / 2;
@@ -467,13 +471,13 @@ __global__ __launch_bounds__(kBlock) void grad_small(const LookupGradArgs a, uin
 // over all of them or not (the most frequent token of a text has a tenth of all
 // positions).
 template <class G, int U>
-__global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t chunks, uint32_t len, int sorted,
-                                                    uint32_t lanes, uint32_t bx)
+__global__ __launch_bounds__(kBlock) void grad_join(const LookupGradArgs a, uint32_t base, uint32_t chunks, uint32_t len,
+                                                    int sorted, uint32_t lanes, uint32_t bx)
 {
     constexpr int B = 16;
     const uint32_t* key = a.key[sorted];
-    const uint32_t chunk = blockIdx.x % bx * (kBlock / lanes) + threadIdx.x / lanes;
-    const uint64_t c = (static_cast<uint64_t>(blockIdx.x / bx) * lanes + (threadIdx.x & (lanes - 1))) * U;
+    const uint32_t id = base + blockIdx.x, chunk = id % bx * (kBlock / lanes) + threadIdx.x / lanes;
+    const uint64_t c = (static_cast<uint64_t>(id / bx) * lanes + (threadIdx.x & (lanes - 1))) * U;
     const uint64_t p0 = static_cast<uint64_t>(chunk) * len, p1 = p0 + len;
     if (p1 >= a.ntokens || c >= a.width) return;
     const uint32_t row = key[p1 - 1];
@@ -559,6 +563,18 @@ hipError_t sort_and_fill(const LookupGradArgs& a, int* sorted, int num_cus, hipS
     return hipGetLastError();
 }
 
+// Launches `blocks` workgroups in parts whose work-items are counted in 32 bits:
+// launch(base, part).
+template <class Launch>
+hipError_t in_launches(uint64_t blocks, const Launch& launch)
+{
+    constexpr uint64_t most = (uint64_t(1) << 32) / kBlock - 1;
+    if (blocks > UINT32_MAX) return hipErrorInvalidValue;  // more bytes of partial sums than a device has
+    for (uint64_t base = 0; base < blocks; base += most)
+        launch(static_cast<uint32_t>(base), dim3(static_cast<uint32_t>(std::min(blocks - base, most))));
+    return hipGetLastError();
+}
+
 template <class F, class G, int U, bool NT>
 hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
 {
@@ -573,26 +589,34 @@ hipError_t grad_launch(const LookupGradArgs& a, int num_cus, hipStream_t s)
     const uint32_t lanes = lanes_for(units, kGradLanes, kBlock), per = kBlock / lanes;
     // bx workgroups along the chunks, times the slices of a row
     const uint32_t bx = (chunks + per - 1) / per, by = static_cast<uint32_t>((units + lanes - 1) / lanes);
-    const dim3 grid(bx * by);
+    const uint64_t blocks = static_cast<uint64_t>(bx) * by;
     int sorted = 0;
+    hipError_t e;
     if (a.ntokens <= kSortThreads) {
         const int passes = sort_passes(a.rows), bits = (sort_bits(a.rows) + passes - 1) / passes;
         hipLaunchKernelGGL(sort_small, dim3(1), dim3(kSortThreads), 0, s, a, passes, bits);
         uint32_t fillers, fill_lanes;
         fill_shape<G>(a, kBlock, num_cus, &fillers, &fill_lanes);
         if (a.accumulate) fillers = 0;
-        hipLaunchKernelGGL((grad_small<F, G, U, NT>), dim3(grid.x + fillers), dim3(kBlock), 0, s, a, chunks,
-                           lanes, bx, by, fill_lanes);
+        e = in_launches(blocks + fillers, [&](uint32_t base, dim3 part) {
+            hipLaunchKernelGGL((grad_small<F, G, U, NT>), part, dim3(kBlock), 0, s, a, base, chunks, lanes, bx, by, fillers,
+                               fill_lanes);
+        });
     } else {
-        const hipError_t e = sort_and_fill<G, NT>(a, &sorted, num_cus, s);
-        if (e != hipSuccess) return e;
-        if (len == kGradChunkFew)
-            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunkFew>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes, bx);
-        else
-            hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunk>), grid, dim3(kBlock), 0, s, a, chunks, sorted, lanes, bx);
+        if ((e = sort_and_fill<G, NT>(a, &sorted, num_cus, s)) != hipSuccess) return e;
+        e = in_launches(blocks, [&](uint32_t base, dim3 part) {
+            if (len == kGradChunkFew)
+                hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunkFew>), part, dim3(kBlock), 0, s, a, base, chunks, sorted,
+                                   lanes, bx);
+            else
+                hipLaunchKernelGGL((grad_sum<F, G, U, kGradChunk>), part, dim3(kBlock), 0, s, a, base, chunks, sorted,
+                                   lanes, bx);
+        });
     }
-    if (chunks > 1) hipLaunchKernelGGL((grad_join<G, U>), grid, dim3(kBlock), 0, s, a, chunks, len, sorted, lanes, bx);
-    return hipGetLastError();
+    if (e != hipSuccess || chunks == 1) return e;
+    return in_launches(blocks, [&](uint32_t base, dim3 part) {
+        hipLaunchKernelGGL((grad_join<G, U>), part, dim3(kBlock), 0, s, a, base, chunks, len, sorted, lanes, bx);
+    });
 }
 
 // Rows that do not lie on 16 bytes are summed by elements: by vectors at any

@@ -146,3 +146,30 @@ def test_no_limit_clips_nothing(comms, dtype, norm, size):  # noqa: F811
                 else:
                     assert torch.equal(a, b)
                     assert math.isinf(float(out)) == (math.isinf(value) and call != "replicated")
+
+
+# ---------------------------------------------------------------------------
+# embedding
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("n,rows,width", [(9, 1, (1 << 31) - 1),     # sorted by one workgroup
+                                          (1025, 5, 33_500_001)])
+def test_embedding_grad_of_more_blocks_than_a_launch_counts(comms, n, rows, width):  # noqa: F811
+    """2^24 workgroups of 256 threads and more, which are 2^32 work-items. Whole
+    numbers, so that every sum is exact."""
+    try:
+        comm = comms(1, ar.ar_embedding_workspace_bytes(n, rows, width))
+        dout = torch.empty(n, width, dtype=torch.bfloat16, device="cuda")
+        dw = torch.full((rows, width), math.nan, device="cuda")
+        column = (torch.arange(width, dtype=torch.int32, device="cuda") % 97).to(torch.bfloat16)
+    except torch.cuda.OutOfMemoryError:
+        pytest.skip("needs about 110 GB")
+    for t in range(n):
+        torch.add(column, float(t % 7), out=dout[t])
+    tokens = torch.arange(n, device="cuda") % rows
+    ar.ar_embedding_backward(comm, dout, tokens, dw, n, rows, width, "bf16", "f32")
+    for r in range(rows):
+        mine = range(r, n, rows)
+        want = float(sum(t % 7 for t in mine))
+        for lo in range(0, width, 1 << 27):
+            part = column[lo:lo + (1 << 27)].float() * len(mine) + want
+            assert torch.equal(dw[r, lo:lo + (1 << 27)], part), (r, lo)
