@@ -178,7 +178,7 @@ def _ptrs(bufs):
         t = _PTR_ARRAY_TYPES[n] = ctypes.c_void_p * n
     # Addresses alone: many times faster than one ctypes object each. Every element
     # is looked at: an array takes an integer tensor of one element by its value.
-    if set(map(type, bufs)) == {int}:
+    if n and type(bufs[0]) is int and set(map(type, bufs)) == {int}:
         try:
             return t.from_buffer(array.array("Q", bufs))
         except OverflowError:
