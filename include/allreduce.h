@@ -395,14 +395,14 @@ size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, siz
  * A token whose target is ignore_index or outside [0, vocab) is ignored: its
  * loss is 0 (its lse is still given). Products of fp16 and bf16 are summed in
  * fp32; fp32 products are exact to 2^-24 (fp32 matrix instructions up to 64
- * tokens, else bf16 pieces that hold all 24 bits; 2^-21 where both factors are
- * of 256 or more). Products with an infinity, and beyond fp32's range, are the
+ * tokens and for small problems, else bf16 pieces that hold all 24 bits; 2^-21
+ * where both factors are of 256 or more). Products with an infinity, and beyond fp32's range, are the
  * infinity of their sign: a logit of -infinity adds nothing to lse, one of
  * +infinity, or a NaN, makes the token's lse and loss NaN. losses and lse are fp32.
  * ntokens and width are below 2^24, of fp32 below 2^20. Operands whose rows are
  * on 16-byte boundaries and whole multiples of 16 bytes long are read as they
- * lie (fp32 only up to 64 tokens); others are first laid out in the workspace,
- * at most 1 GiB of the weight at a time. */
+ * lie (fp32 ones by fp32 matrix instructions only); others are first laid out in
+ * the workspace, at most 1 GiB of the weight at a time. */
 ar_result_t ar_linear_cross_entropy(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
                                     ar_index_t index, float* losses, float* lse, size_t ntokens, size_t vocab,
                                     size_t width, size_t ld_hidden, size_t ld_weight, long long ignore_index,
@@ -414,9 +414,11 @@ ar_result_t ar_linear_cross_entropy(ar_comm_t comm, const void* hidden, const vo
  *   grad_hidden = d weight,  grad_weight = d^T hidden,
  * both of dtype and either may be NULL. Ignored tokens have zero grad_hidden
  * and add nothing to grad_weight, whatever their hidden row holds. For fp16
- * and bf16, d is rounded to that type once (scaled by a power of two and, for
- * grad_weight, by the largest |grad_losses|, so that small probabilities do
- * not underflow); sums are fp32. */
+ * and bf16, d is rounded to that type once (scaled by 2^14 and, for grad_weight,
+ * by the largest |grad_losses|, so that small probabilities do not underflow: in
+ * fp16 steps of 2^-38, of the largest |grad_losses| for grad_weight, are left);
+ * sums are fp32 and hold the 2^14. An infinite grad_losses of a token that
+ * counts makes grad_weight NaN. */
 ar_result_t ar_linear_cross_entropy_backward(ar_comm_t comm, const void* hidden, const void* weight,
                                              const void* targets, ar_index_t index, const float* lse,
                                              const float* grad_losses, void* grad_hidden, void* grad_weight,

@@ -11,10 +11,10 @@
 // are gemm.h's, with both operands contiguous along the summed axis, so W and
 // X are also laid out transposed, and d is written in both orders.
 //
-// fp32 operands of more than 64 tokens are laid out as three bf16 pieces each:
-// six bf16 products give the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the
-// fp32 matrix instructions end at 0.16. With fewer tokens the time is that of
-// reading the weight, which then stays as it is.
+// fp32 operands are laid out as three bf16 pieces each: six bf16 products give
+// the fp32 product to 2^-24 at 2.5 PFLOP/s / 6, where the fp32 matrix instructions
+// end at 0.16. Up to 64 tokens the time is that of reading the weight, which then
+// stays as it is, and so it does where there are few tiles (small_tiles).
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -931,8 +931,9 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         p.piece = (whole + pieces - 1) / pieces * kTileM;
     } else {
         // From half the largest size on, the one whose tiles fill the CUs best.
-        // 8192 x 131072 x 4096: pieces of 16384 rows end in full rounds, of
-        // 13312 the weight gradient's 832 tiles take four rounds for 3.25.
+        // 8192 x 131072 x 4096: the tiles of pieces of 20224 rows take ten, two and
+        // five rounds for 9.9, 2 and 4.9; of 13312 rows the weight gradient's 832
+        // take four for 3.25.
         const uint64_t tile_m = small ? kFewM : kTileM, tile_n = static_cast<uint64_t>(p.tile_n);
         const Shape shape = f32 ? Shape{ntokens, width, tile_m, tile_n, tile_m, small ? 64u : tile_n, step, p.pieces}
                                 : Shape{ntokens, width, tile_m, tile_n, kTileM, 256, step, false};

@@ -48,10 +48,10 @@ __device__ __forceinline__ void store16(void* base, uint64_t byte, u32x4 v)
 // ---------------------------------------------------------------------------
 // `lanes` (a power of two up to kBlock) threads a row, kBlock / lanes rows a
 // workgroup, 16 bytes a thread and what is left of a row by elements. Stores are
-// cached: with non-temporal ones 16384 x 4096 fp16 returns in 30 us rather than
-// 44, but what reads the rows next ends 11 us later (of 80), and so at every size
-// from 32 MiB on. Rows that do not lie on 16 bytes: 16384 x 4093 fp16 in 58 us,
-// where elements take 101.
+// cached: with non-temporal ones 16384 x 4096 fp16 returns in 26 us rather than
+// 43, but what reads the rows next takes the time instead, 79 against 81 us for
+// both. Rows that do not lie on 16 bytes: 16384 x 4093 fp16 in 58 us, where
+// elements take 101.
 template <class F>
 __global__ __launch_bounds__(kBlock) void lookup(const LookupArgs a, int lanes)
 {
