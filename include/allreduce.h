@@ -398,11 +398,11 @@ size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t vocab, siz
  * tokens and for small problems, else bf16 pieces that hold all 24 bits; 2^-21
  * where both factors are of 256 or more). Products with an infinity, and beyond fp32's range, are the
  * infinity of their sign: a logit of -infinity adds nothing to lse, one of
- * +infinity, or a NaN, makes the token's lse and loss NaN. losses and lse are fp32.
- * ntokens and width are below 2^24, of fp32 below 2^20. Operands whose rows are
- * on 16-byte boundaries and whole multiples of 16 bytes long are read as they
- * lie (fp32 ones by fp32 matrix instructions only); others are first laid out in
- * the workspace, at most 1 GiB of the weight at a time. */
+ * +infinity, or a NaN, makes the token's lse and loss NaN. losses and lse are
+ * fp32. ntokens and width are below 2^24, of fp32 below 2^20, vocab below 2^28.
+ * Operands whose rows are on 16-byte boundaries and whole multiples of 16 bytes
+ * long are read as they lie (fp32 ones by fp32 matrix instructions only); others
+ * are first laid out in the workspace, at most 1 GiB of the weight at a time. */
 ar_result_t ar_linear_cross_entropy(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
                                     ar_index_t index, float* losses, float* lse, size_t ntokens, size_t vocab,
                                     size_t width, size_t ld_hidden, size_t ld_weight, long long ignore_index,
