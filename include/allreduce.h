@@ -426,6 +426,52 @@ ar_result_t ar_linear_cross_entropy_backward(ar_comm_t comm, const void* hidden,
                                              size_t ld_weight, size_t ld_grad_hidden, size_t ld_grad_weight,
                                              long long ignore_index, ar_dtype_t dtype, hipStream_t stream);
 
+/* Workspace of ar_linear_log_probs with `top` alternatives (backward = 0) or of
+ * its gradient (backward != 0; top is not looked at), also for fewer tokens and
+ * fewer alternatives (but for at least one, if those are to be found);
+ * (size_t)-1 for sizes they do not take. */
+size_t ar_linear_log_probs_workspace_bytes(size_t ntokens, size_t vocab, size_t width, ar_dtype_t dtype, int top,
+                                           int backward);
+
+/* Log probabilities of given tokens under the linear head of
+ * ar_linear_cross_entropy, at the inverse temperature `scale` (finite, above 0):
+ *   z[t][v] = scale * (hidden[t] . weight[v]),  lse[t] = log sum_v exp z[t][v],
+ *   log_probs[t] = z[t][targets[t]] - lse[t],
+ *   entropy[t] = -sum_v p log p with p = exp(z[t][v] - lse[t])   (may be NULL).
+ * The `top` (0 to 64, at most vocab) largest z of every token go to
+ * top_log_probs[t][k] = z - lse[t] and top_ids[t][k], the largest first and of
+ * equal ones the smaller id first; a NaN counts as -infinity among them.
+ * Both may be NULL if top is 0. A token whose target is ignore_index or outside
+ * [0, vocab) has the log probability 0; its other results are given. Products,
+ * infinities, NaN and limits are as in ar_linear_cross_entropy (a logit of
+ * -infinity adds nothing to the entropy; one of +infinity, or a NaN, makes all
+ * results of its token but top_ids NaN); with alternatives vocab is below 2^24, and the
+ * workspace holds the logits of up to 1 GiB worth of tokens (of 256 tokens at
+ * the least). */
+ar_result_t ar_linear_log_probs(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
+                                ar_index_t index, float* log_probs, float* entropy, float* lse, int top,
+                                float* top_log_probs, int* top_ids, size_t ntokens, size_t vocab, size_t width,
+                                size_t ld_hidden, size_t ld_weight, float scale, long long ignore_index,
+                                ar_dtype_t dtype, hipStream_t stream);
+
+/* Its gradients, given lse and entropy of the forward call and the gradients of
+ * each log probability and entropy (grad_entropy may be NULL: none comes
+ * through it, and entropy is not read):
+ *   dz[t][v] = grad_log_probs[t] ([v = targets[t]] - p) - grad_entropy[t] p (log p + entropy[t]),
+ *   grad_hidden = scale dz weight,  grad_weight = scale dz^T hidden,
+ * both of dtype and either may be NULL. A token whose target is ignore_index or
+ * outside [0, vocab) has zero grad_hidden and adds nothing to grad_weight,
+ * whatever its hidden row and gradients hold. For fp16 and bf16, dz over the
+ * larger of the token's two gradients is rounded to that type once (times 2^12:
+ * in fp16 steps of 2^-36 are left); sums are fp32. */
+ar_result_t ar_linear_log_probs_backward(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
+                                         ar_index_t index, const float* lse, const float* entropy,
+                                         const float* grad_log_probs, const float* grad_entropy, void* grad_hidden,
+                                         void* grad_weight, size_t ntokens, size_t vocab, size_t width,
+                                         size_t ld_hidden, size_t ld_weight, size_t ld_grad_hidden,
+                                         size_t ld_grad_weight, float scale, long long ignore_index, ar_dtype_t dtype,
+                                         hipStream_t stream);
+
 /* Static description of a result code. */
 const char* ar_result_string(ar_result_t result);
 

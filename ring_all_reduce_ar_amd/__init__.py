@@ -68,6 +68,7 @@ EXPORTED_SYMBOLS = (
     "ar_clip_workspace_bytes", "ar_grad_norm", "ar_clip_grads", "ar_all_reduce_clip",
     "ar_embedding", "ar_embedding_workspace_bytes", "ar_embedding_backward",
     "ar_linear_cross_entropy_workspace_bytes", "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward",
+    "ar_linear_log_probs_workspace_bytes", "ar_linear_log_probs", "ar_linear_log_probs_backward",
     "ar_result_string", "ar_last_error",
 )
 
@@ -109,6 +110,12 @@ _lib.ar_linear_cross_entropy_workspace_bytes.restype = _c_size
 _lib.ar_linear_cross_entropy.argtypes = [_vp, _vp, _vp, _vp, _c_int, _vp, _vp] + [_c_size] * 5 + [_c_i64, _c_int, _vp]
 _lib.ar_linear_cross_entropy_backward.argtypes = ([_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _vp] + [_c_size] * 7 +
                                                   [_c_i64, _c_int, _vp])
+_lib.ar_linear_log_probs_workspace_bytes.argtypes = [_c_size] * 3 + [_c_int] * 3
+_lib.ar_linear_log_probs_workspace_bytes.restype = _c_size
+_lib.ar_linear_log_probs.argtypes = ([_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _vp, _vp] + [_c_size] * 5 +
+                                     [ctypes.c_float, _c_i64, _c_int, _vp])
+_lib.ar_linear_log_probs_backward.argtypes = ([_vp, _vp, _vp, _vp, _c_int] + [_vp] * 6 + [_c_size] * 7 +
+                                              [ctypes.c_float, _c_i64, _c_int, _vp])
 _lib.ar_result_string.argtypes = [_c_int]
 _lib.ar_result_string.restype = ctypes.c_char_p
 _lib.ar_last_error.argtypes = []
@@ -118,7 +125,8 @@ for _name in ("ar_comm_create", "ar_comm_destroy", "ar_comm_set_workspace", "ar_
               "ar_all_gather", "ar_all_to_all", "ar_all_reduce_multi", "ar_comm_set_step_timing",
               "ar_comm_set_streaming", "ar_comm_set_access", "ar_last_step_times_ms",
               "ar_grad_norm", "ar_clip_grads", "ar_all_reduce_clip", "ar_embedding", "ar_embedding_backward",
-              "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward"):
+              "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward", "ar_linear_log_probs",
+              "ar_linear_log_probs_backward"):
     getattr(_lib, _name).restype = _c_int
 
 
@@ -490,3 +498,48 @@ def ar_linear_cross_entropy_backward(comm, hidden, weight, targets, lse, grad_lo
                                                  ld_weight, ld_grad_hidden, ld_grad_weight, ignore_index,
                                                  _enum(dtype, DTYPE_NAMES, "dtype"), _stream(stream, _device(comm))),
            "ar_linear_cross_entropy_backward")
+
+
+def ar_linear_log_probs_workspace_bytes(ntokens: int, vocab: int, width: int, dtype, top: int = 0,
+                                        backward: bool = False) -> int:
+    return _check_size(_lib.ar_linear_log_probs_workspace_bytes(ntokens, vocab, width,
+                                                                _enum(dtype, DTYPE_NAMES, "dtype"), top,
+                                                                1 if backward else 0),
+                       "ar_linear_log_probs_workspace_bytes")
+
+
+def ar_linear_log_probs(comm, hidden, weight, targets, log_probs, entropy, lse, ntokens: int, vocab: int, width: int,
+                        dtype, top: int = 0, top_log_probs=None, top_ids=None, scale: float = 1.0,
+                        ignore_index: int = -100, ld_hidden: int = 0, ld_weight: int = 0, index=None, stream=None):
+    """log_probs[t] = z[t][targets[t]] - lse[t] with z = scale * hidden weight^T,
+    its entropy (or None), and the ``top`` likeliest tokens' log probabilities
+    and ids (int32)."""
+    x, ld_hidden = _rows(hidden, ld_hidden)
+    w, ld_weight = _rows(weight, ld_weight)
+    if not isinstance(top_ids, (int, type(None))) and top_ids.dtype != torch.int32:
+        raise TypeError(f"top_ids are int32, not {top_ids.dtype}")
+    _check(_lib.ar_linear_log_probs(_h(comm), x, w, _addr(targets), _index(index, targets), _addr(log_probs),
+                                    None if entropy is None else _addr(entropy), _addr(lse), top,
+                                    None if top_log_probs is None else _addr(top_log_probs),
+                                    None if top_ids is None else _addr(top_ids), ntokens, vocab, width, ld_hidden,
+                                    ld_weight, scale, ignore_index, _enum(dtype, DTYPE_NAMES, "dtype"),
+                                    _stream(stream, _device(comm))), "ar_linear_log_probs")
+
+
+def ar_linear_log_probs_backward(comm, hidden, weight, targets, lse, entropy, grad_log_probs, grad_entropy,
+                                 grad_hidden, grad_weight, ntokens: int, vocab: int, width: int, dtype,
+                                 scale: float = 1.0, ignore_index: int = -100, ld_hidden: int = 0, ld_weight: int = 0,
+                                 ld_grad_hidden: int = 0, ld_grad_weight: int = 0, index=None, stream=None):
+    """grad_hidden and grad_weight (either may be None) from lse, entropy and the
+    gradients of each log probability and entropy (grad_entropy may be None, and
+    entropy then too)."""
+    x, ld_hidden = _rows(hidden, ld_hidden)
+    w, ld_weight = _rows(weight, ld_weight)
+    gx, ld_grad_hidden = _rows(grad_hidden, ld_grad_hidden)
+    gw, ld_grad_weight = _rows(grad_weight, ld_grad_weight)
+    _check(_lib.ar_linear_log_probs_backward(_h(comm), x, w, _addr(targets), _index(index, targets), _addr(lse),
+                                             None if entropy is None else _addr(entropy), _addr(grad_log_probs),
+                                             None if grad_entropy is None else _addr(grad_entropy), gx, gw, ntokens,
+                                             vocab, width, ld_hidden, ld_weight, ld_grad_hidden, ld_grad_weight, scale,
+                                             ignore_index, _enum(dtype, DTYPE_NAMES, "dtype"),
+                                             _stream(stream, _device(comm))), "ar_linear_log_probs_backward")

@@ -1,5 +1,6 @@
 // cross_entropy.hip -- softmax cross entropy of a linear head, in pieces of
-// the vocabulary, without keeping the logits.
+// the vocabulary, without keeping the logits; log probabilities with their
+// entropy and alternatives take the same way with the epilogues of log_probs.h.
 //
 //   z[t][v] = x[t] . w[v],  lse[t] = log sum_v exp z[t][v],  loss[t] = lse[t] - z[t][y[t]]
 //   d[t][v] = g[t] (exp(z[t][v] - lse[t]) - [v = y[t]]),  dX = d W,  dW = d^T X
@@ -19,33 +20,12 @@
 #include <type_traits>
 #include <utility>
 
-#include "gemm.h"
+#include "log_probs.h"
 
 namespace ar {
 namespace lm {
-using namespace detail;
 
 namespace {
-
-// d is held times 2^14: a probability of 1e-8 is still a normal fp16, and
-// |p - 1| 2^14 is far below its largest.
-constexpr float kDBits = 14.0f, kDScale = 16384.0f;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ int64_t load_target(const Indices& x, uint64_t t, int64_t ignore, uint64_t vocab)
-{
-    const int64_t y = x.is64 ? gptr<int64_t>(x.p)[t] : static_cast<int64_t>(gptr<int32_t>(x.p)[t]);
-    return y == ignore || static_cast<uint64_t>(y) >= vocab ? -1 : y;
-}
-
-// Where target y lies among a lane's rows v, v + 1 .. of MT groups of 16.
-constexpr uint32_t kNoTarget = UINT32_MAX;
-template <int MT>
-__device__ __forceinline__ uint32_t target_at(int64_t y, uint64_t v)
-{
-    const uint64_t at = static_cast<uint64_t>(y) - v;
-    return y >= 0 && at < MT * 16 ? static_cast<uint32_t>(at) : kNoTarget;
-}
 
 // ---------------------------------------------------------------------------
 // laying out operands
@@ -236,7 +216,6 @@ __device__ __forceinline__ Stats join_parts(Stats a, Stats b)
 // threads for each. Neighbouring tokens lie side by side, so many tokens take
 // 16 (128 bytes) and few tokens as few as there are, for more threads to a
 // row: the loss of 3 x 65536 x 2048 fp16 takes 71 us rather than 110 with 16.
-constexpr int kJoinBlock = 512;
 template <int X>
 __global__ __launch_bounds__(kJoinBlock) void join_stats(const Stats* stats, uint64_t stat_rows,
                                                          const float* target_logit, Indices targets, int64_t ignore,
@@ -268,10 +247,6 @@ __global__ __launch_bounds__(kJoinBlock) void join_stats(const Stats* stats, uin
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-struct RowScale {
-    float top;  // the largest |g| of the rows that count, at least the least normal number
-};
-
 __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices targets, int64_t ignore, uint64_t vocab,
                                                   uint64_t ntokens, RowScale* out)
 {
@@ -289,15 +264,14 @@ __global__ __launch_bounds__(1024) void row_scale(const float* g, Indices target
     }
 }
 
-// d of one piece of the vocabulary, in both orders: d[t][v] = 2^14 (p - [v =
-// y]) for the hidden gradient (whose rows take g[t] at the end) and dt[v][t]
-// the same times g[t] / max |g| for the weight's.
-template <class T>
+// d of one piece of the vocabulary, in both orders: d[t][v] by the rule (LossD
+// or LogProbD) for the hidden gradient, whose rows take g[t] at the end, and
+// dt[v][t] the same times g[t] / max |g| for the weight's.
+template <class T, class Rule>
 struct DEpilogue {
     typename T::Elem* d;
     typename T::Elem* dt;
-    const float* lse;
-    const float* g_losses;
+    Rule rule;
     const RowScale* scale;
     Indices targets;
     int64_t ignore;
@@ -318,21 +292,18 @@ struct DEpilogue {
             const int64_t y = t < g.n ? load_target(targets, t, ignore, vocab) : -1;
             const uint32_t at = target_at<MT>(y, v0 + mine);
             const uint32_t keep = y >= 0 ? ~0u : 0u;  // zeros for an ignored token, even from a NaN
-            const float l = y >= 0 ? lse[t] : 0.0f;
-            factor[j] = y >= 0 ? g_losses[t] * inv : 0.0f;
+            const typename Rule::Row row = rule.row(t, y >= 0);
+            factor[j] = y >= 0 ? row.g * inv : 0.0f;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc.v[i][j][r] - l, kLog2e, kDBits));
-                    acc.v[i][j][r] = as_f(as_u(p) & keep);
-                }
+                for (int r = 0; r < 4; ++r) acc.v[i][j][r] = as_f(as_u(rule(row, acc.v[i][j][r])) & keep);
             __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
             if (__any(at != kNoTarget)) {       // few tiles hold a target
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] -= at == static_cast<uint32_t>(16 * i + r) ? kDScale : 0.0f;
+                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] += at == static_cast<uint32_t>(16 * i + r) ? rule.at_target(row) : 0.0f;
             }
             if (m0 + MT * 16 > g.m) {  // zeros below the vocabulary
 #pragma unroll
@@ -445,18 +416,18 @@ struct SumEpilogue {
     }
 };
 
-// out[row][h] = round(scale 2^-14 * the splits' sum), U elements a thread, `lanes`
+// out[row][h] = round(scale unit * the splits' sum), U elements a thread, `lanes`
 // threads a row. The hidden gradient's scale is g[t], and 0 for ignored tokens;
 // the weight's is max |g|. 8192 x 4096 into bf16 in 37 us, 5.4 TB/s.
 template <class F, int U, bool WEIGHT>
 __global__ __launch_bounds__(kBlock) void finish_sum(const float* acc, int splits, const float* g, Indices targets,
-                                                     int64_t ignore, uint64_t vocab, const RowScale* top, uint64_t rows,
-                                                     uint64_t width, void* out, uint64_t ld, int lanes)
+                                                     int64_t ignore, uint64_t vocab, const RowScale* top, float unit,
+                                                     uint64_t rows, uint64_t width, void* out, uint64_t ld, int lanes)
 {
     const uint64_t row = static_cast<uint64_t>(blockIdx.x) * (kBlock / lanes) + threadIdx.x / lanes;
     if (row >= rows) return;
     const bool on = WEIGHT || load_target(targets, row, ignore, vocab) >= 0;
-    const float scale = (WEIGHT ? top->top : on ? g[row] : 0.0f) * (1.0f / kDScale);
+    const float scale = (WEIGHT ? top->top : on ? g[row] : 0.0f) * unit;
     for (uint64_t c = (threadIdx.x & (lanes - 1)) * static_cast<uint64_t>(U); c < width;
          c += lanes * static_cast<uint64_t>(U)) {
         float s[U] = {};
@@ -481,13 +452,14 @@ __global__ __launch_bounds__(kBlock) void finish_sum(const float* acc, int split
     }
 }
 
-// grad_weight[v][h] = round(max |g| 2^-14 * sum). The product's rows are the
+// grad_weight[v][h] = round(max |g| unit * sum). The product's rows are the
 // columns h, or (BY_VOCAB) the vocabulary's.
 template <class F, class T, bool BY_VOCAB>
 struct WeightEpilogue {
     void* out;
     uint64_t ld;
     const RowScale* scale;
+    float unit;  // the inverse of what d is held times
     int vec;  // the elements that can be stored together: 1, 4, or 8 of 16 bits
     int nt;   // the gradient is more than the last-level cache holds
 
@@ -496,7 +468,7 @@ struct WeightEpilogue {
                                                uint32_t, const S& stage) const
     {
         const int lane = threadIdx.x & 63, quad = lane >> 4;
-        const float s = scale->top * (1.0f / kDScale);
+        const float s = scale->top * unit;
         if constexpr (BY_VOCAB) {
             each_result(c, m0, n0, g, [&](uint32_t v, uint32_t h, float x) { F::st(out, v * ld + h, x * s); });
             return;
@@ -631,6 +603,10 @@ uint64_t most_tiles(uint64_t ntokens, uint64_t tile_n)
     return (uint64_t(1) << 21) / (across ? across : 1);
 }
 
+// Up to so many tokens eight waves find the alternatives of one, since there
+// are CUs to spare.
+constexpr uint64_t kSelectFew = 512;
+
 // What is larger than the last-level cache is stored around it: 8192 x 131072 x
 // 4096 bf16, loss and gradients, 25.3 -> 25.0 ms.
 constexpr uint64_t kStreamBytes = uint64_t(256) << 20;
@@ -670,7 +646,7 @@ struct Call {
         *ld = p.k_pad * OB;
         return pack<PARTS, Raw>(from, a.ld_weight, rows, a.width, p.k_pad, ws + p.weight, s);
     }
-    GemmArgs logits_args(const char* w, uint64_t ldw, const char* x, uint64_t ldx, uint64_t rows) const
+    GemmArgs logits_args(const char* w, uint64_t ldw, const char* x, uint64_t ldx, uint64_t rows, uint64_t tokens) const
     {
         GemmArgs g{};
         g.a = w;
@@ -678,7 +654,7 @@ struct Call {
         g.lda = ldw;
         g.ldb = ldx;
         g.m = static_cast<uint32_t>(rows);
-        g.n = static_cast<uint32_t>(a.ntokens);
+        g.n = static_cast<uint32_t>(tokens);
         // an operand that lies as given ends at the width, then whole 16-byte columns
         g.k = g.k_all = static_cast<uint32_t>(p.pack_hidden && p.pack_weight ? p.k_pad : a.width);
         g.splits = 1;
@@ -698,15 +674,16 @@ struct Call {
     }
 
     template <bool WEIGHT>
-    hipError_t finish(const float* sums, int splits, const RowScale* scale, uint64_t rows, void* out, uint64_t ld) const
+    hipError_t finish(const float* sums, int splits, const RowScale* scale, float unit, const float* row_g, uint64_t rows,
+                      void* out, uint64_t ld) const
     {
         // (few results take a thread each: 6 x 256 of 64 parts in 5 us, by vectors and of 128 parts in 37)
         const bool vec = a.width % F::kEpv == 0 && ld % F::kEpv == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
                          rows * a.width >= (1u << 18);
         const int lanes = lanes_for(vec ? a.width / F::kEpv : a.width);
         auto launch = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid_for(rows, lanes), dim3(kBlock), 0, s, sums, splits, a.grad_losses, a.targets,
-                               a.ignore_index, a.vocab, scale, rows, a.width, out, ld, lanes);
+            hipLaunchKernelGGL(kernel, grid_for(rows, lanes), dim3(kBlock), 0, s, sums, splits, row_g, a.targets,
+                               a.ignore_index, a.vocab, scale, unit, rows, a.width, out, ld, lanes);
             return hipGetLastError();
         };
         return vec ? launch(finish_sum<F, F::kEpv, WEIGHT>) : launch(finish_sum<F, 1, WEIGHT>);
@@ -725,7 +702,7 @@ struct Call {
             const uint64_t rows = a.vocab - v0 < piece ? a.vocab - v0 : piece;
             if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
             const StatsEpilogue epi{stats, target_logit, a.targets, a.ignore_index, a.vocab, v0, row0};
-            if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
+            if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows, a.ntokens), p.tile_n, epi, s)) != hipSuccess) return e;
             row0 += stat_rows_of(rows, p.tile_n);
         }
         auto join = [&](auto kernel, uint32_t tokens) {
@@ -739,7 +716,75 @@ struct Call {
         return join(join_stats<16>, 16);
     }
 
+    // The same for log probabilities, a chunk of tokens after the other where
+    // their logits are kept for alternatives.
+    hipError_t forward_log_probs() const
+    {
+        const char *x, *w;
+        uint64_t ldx, ldw;
+        hipError_t e = hidden(&x, &ldx);
+        if (e != hipSuccess) return e;
+        LogParts* parts = reinterpret_cast<LogParts*>(ws + p.stats);
+        float* target_logit = reinterpret_cast<float*>(ws + p.target_logit);
+        float* logits = a.top ? reinterpret_cast<float*>(ws + p.logits) : nullptr;
+        const uint64_t piece = p.pack_weight ? p.piece : most_tiles(p.chunk, p.tile_n) * kTileM;
+        for (uint64_t t0 = 0; t0 < a.ntokens; t0 += p.chunk) {
+            const uint64_t tokens = std::min(a.ntokens - t0, p.chunk);
+            uint64_t row0 = 0;
+            for (uint64_t v0 = 0; v0 < a.vocab; v0 += piece) {
+                const uint64_t rows = std::min(a.vocab - v0, piece);
+                if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
+                const LogPartsEpilogue epi{parts, target_logit, logits, a.targets, a.ignore_index, a.vocab, v0, row0,
+                                           t0, a.scale};
+                if ((e = product<T, PARTS>(logits_args(w, ldw, x + t0 * ldx, ldx, rows, tokens), p.tile_n, epi, s)) !=
+                    hipSuccess)
+                    return e;
+                row0 += stat_rows_of(rows, p.tile_n);
+            }
+            const LogProbOut out{a.targets, a.ignore_index, a.vocab, t0, tokens, target_logit, a.losses, a.entropy, a.lse};
+            auto grid = [&](uint64_t per) { return dim3(static_cast<uint32_t>((tokens + per - 1) / per)); };
+            if (a.top) {
+                const uint32_t group = p.tile_n == 256 ? 128 : p.tile_n > 64 ? 64 : p.tile_n == 16 ? 16 : 32;
+                auto select = [&](auto kernel, uint64_t per, uint32_t threads) {
+                    hipLaunchKernelGGL(kernel, grid(per), dim3(threads), 0, s, parts, row0, logits, group, a.top, out,
+                                       a.top_log_probs, a.top_ids);
+                };
+                if (tokens <= kSelectFew) select(select_top<8>, 1, 512);
+                else select(select_top<1>, 4, 256);
+            } else {
+                auto join = [&](auto kernel, uint64_t per) {
+                    hipLaunchKernelGGL(kernel, grid(per), dim3(kJoinBlock), 0, s, parts, row0, out);
+                };
+                if (tokens <= 32) join(join_log_probs<1>, 1);
+                else if (tokens <= 512) join(join_log_probs<4>, 4);
+                else join(join_log_probs<16>, 16);
+            }
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+
     hipError_t backward() const
+    {
+        RowScale* scale = reinterpret_cast<RowScale*>(ws + p.row_scale);
+        if (a.log_probs) {
+            float* rows = reinterpret_cast<float*>(ws + p.row_gradients);
+            const RowGradients r{rows, rows + a.ntokens, rows + 2 * a.ntokens};
+            hipLaunchKernelGGL(row_gradients, dim3(1), dim3(1024), 0, s, a.grad_losses, a.grad_entropy, a.scale, a.targets,
+                               a.ignore_index, a.vocab, a.ntokens, r, scale);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            return backward_by(LogProbD{a.lse, a.grad_entropy ? a.entropy : nullptr, r, a.scale}, 1.0f / kLogProbScale, r.g);
+        }
+        hipLaunchKernelGGL(row_scale, dim3(1), dim3(1024), 0, s, a.grad_losses, a.targets, a.ignore_index, a.vocab,
+                           a.ntokens, scale);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        return backward_by(LossD{a.lse, a.grad_losses}, 1.0f / kDScale, a.grad_losses);
+    }
+
+    template <class Rule>
+    hipError_t backward_by(const Rule& rule, float unit, const float* row_g) const
     {
         const char *x = nullptr, *w = nullptr;
         uint64_t ldx = 0, ldw = 0;
@@ -749,10 +794,7 @@ struct Call {
         Elem* dt = a.grad_weight ? reinterpret_cast<Elem*>(ws + p.dt) : nullptr;
         char *wt = ws + p.weight_t, *xt = ws + p.hidden_t;
         float* acc = reinterpret_cast<float*>(ws + p.grad_hidden_acc);
-        RowScale* scale = reinterpret_cast<RowScale*>(ws + p.row_scale);
-        hipLaunchKernelGGL(row_scale, dim3(1), dim3(1024), 0, s, a.grad_losses, a.targets, a.ignore_index, a.vocab,
-                           a.ntokens, scale);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        const RowScale* scale = reinterpret_cast<const RowScale*>(ws + p.row_scale);
         if (dt && a.ntokens &&
             (e = transpose<PARTS, Raw>(a.hidden, a.ld_hidden, a.ntokens, a.width, p.t_pad, xt, a, 1, s)) != hipSuccess)
             return e;
@@ -761,9 +803,9 @@ struct Call {
             const uint64_t pad = round_up(rows, kTileK);
             if (a.ntokens) {  // no token: the weight's gradient is the empty sum
                 if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
-                const DEpilogue<T> epi{d, dt, a.lse, a.grad_losses, scale, a.targets, a.ignore_index, a.vocab, v0, pad,
-                                       p.t_pad, a.ntokens * pad * OB > kStreamBytes};
-                if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows), p.tile_n, epi, s)) != hipSuccess) return e;
+                const DEpilogue<T, Rule> epi{d, dt, rule, scale, a.targets, a.ignore_index, a.vocab, v0, pad, p.t_pad,
+                                             a.ntokens * pad * OB > kStreamBytes};
+                if ((e = product<T, PARTS>(logits_args(w, ldw, x, ldx, rows, a.ntokens), p.tile_n, epi, s)) != hipSuccess) return e;
             }
             if (d) {
                 const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * EB;
@@ -797,18 +839,18 @@ struct Call {
                     const SumEpilogue<false> by_column{sums, rows, a.width, 0};
                     const SumEpilogue<true> by_vocab{sums, rows, a.width, 0};
                     if ((e = in_order(g, rows, 256, by_column, by_vocab)) != hipSuccess) return e;
-                    if ((e = finish<true>(sums, p.weight_splits, scale, rows, out, a.ld_grad_weight)) != hipSuccess) return e;
+                    if ((e = finish<true>(sums, p.weight_splits, scale, unit, row_g, rows, out, a.ld_grad_weight)) != hipSuccess) return e;
                 } else {
                     const uintptr_t mis = reinterpret_cast<uintptr_t>(out) | a.ld_grad_weight * EB;
                     const int vec = EB == 2 && mis % 16 == 0 ? 8 : mis % (4 * EB) == 0 ? 4 : 1;
                     const int nt = a.vocab * a.width * EB > kStreamBytes;
-                    const WeightEpilogue<F, T, false> by_column{out, a.ld_grad_weight, scale, vec, nt};
-                    const WeightEpilogue<F, T, true> by_vocab{out, a.ld_grad_weight, scale, vec, nt};
+                    const WeightEpilogue<F, T, false> by_column{out, a.ld_grad_weight, scale, unit, vec, nt};
+                    const WeightEpilogue<F, T, true> by_vocab{out, a.ld_grad_weight, scale, unit, vec, nt};
                     if ((e = in_order(g, rows, 256, by_column, by_vocab)) != hipSuccess) return e;
                 }
             }
         }
-        if (d) e = finish<false>(acc, p.splits, scale, a.ntokens, a.grad_hidden, a.ld_grad_hidden);
+        if (d) e = finish<false>(acc, p.splits, scale, unit, row_g, a.ntokens, a.grad_hidden, a.ld_grad_hidden);
         return e;
     }
 };
@@ -884,13 +926,23 @@ bool small_tiles(uint64_t ntokens, uint64_t vocab, uint64_t width, bool f32, boo
 
 namespace {
 constexpr uint64_t kPieceBytes = uint64_t(1) << 30;
+
+// Tokens whose logits are kept at a time: 1 GiB of them, or one tile's.
+constexpr uint64_t kLogitBytes = uint64_t(1) << 30;
+uint64_t logit_chunk(uint64_t vocab)
+{
+    return std::max<uint64_t>(kLogitBytes / (round_up(vocab, kTileM) * 4) / 256, 1) * 256;
+}
+uint64_t logit_bytes(uint64_t tokens, uint64_t v_pad) { return round_up(tokens, 16) * v_pad * 4; }
+uint64_t stats_bytes(HeadKind kind) { return kind.log_probs ? sizeof(LogParts) : sizeof(Stats); }
 }  // namespace
 
 // Each buffer's largest size over the plans of up to `ntokens` tokens: they
 // differ in tiles, in the fp32 operands' form and in the parts of split sums,
 // which are at most two rounds of tiles or kMostSplits times a whole sum.
-uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward)
+uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, HeadKind kind)
 {
+    const bool backward = kind.backward;
     const bool f32 = dtype == AR_FLOAT32;
     const uint64_t ob = f32 ? kPieces * 2 : 2, k_pad = round_up(width, f32 ? 32 : kTileK), t_pad = round_up(ntokens, kTileK);
     const uint64_t v_pad = round_up(vocab, kTileM), few = std::min<uint64_t>(ntokens, 64);
@@ -899,17 +951,20 @@ uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, a
     uint64_t bytes = ntokens * k_pad * ob + piece + 16 * 256;
     if (!backward)
         // 2 or 4 rows of statistics for 256 of the vocabulary, up to 16 for few
-        // tokens; small tiles of more tokens come to less than 2^20 bytes
-        return bytes + (v_pad / kTileM + 1) * (ntokens * (f32 ? 4 : 2) + few * 16) * sizeof(Stats) + ntokens * 4 + (1u << 20);
+        // tokens; small tiles of more tokens come to less than 2^17 of them
+        return bytes + (v_pad / kTileM + 1) * (ntokens * (f32 ? 4 : 2) + few * 16) * stats_bytes(kind) + ntokens * 4 +
+               (1u << 17) * stats_bytes(kind) + (kind.top ? logit_bytes(std::min(ntokens, logit_chunk(vocab)), v_pad) : 0);
     constexpr uint64_t kRounds = 2 * kCUs * kTileM * 256 * 4;
     const uint64_t hidden_sum = ntokens * width * 4, weight_sum = v_pad * width * 4;
     return bytes + width * t_pad * ob + std::max(hidden_sum, std::min(hidden_sum * kMostSplits, kRounds)) +
-           std::min(weight_sum * kMostSplits, kRounds) + sizeof(RowScale);
+           std::min(weight_sum * kMostSplits, kRounds) + sizeof(RowScale) + (kind.log_probs ? ntokens * 12 + 256 : 0);
 }
 
-CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward)
+CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, HeadKind kind)
 {
+    const bool backward = kind.backward;
     CrossEntropyPlan p{};
+    p.chunk = kind.top ? std::min(ntokens, logit_chunk(vocab)) : ntokens;
     const bool f32 = dtype == AR_FLOAT32;
     const bool small = small_tiles(ntokens, vocab, width, f32, backward);
     p.pieces = f32 && !small;
@@ -967,8 +1022,9 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     p.hidden = take(ntokens * p.k_pad * ob);
     p.weight = take(p.piece * p.k_pad * ob);
     if (!backward) {
-        p.stats = take(p.stat_rows * ntokens * sizeof(Stats));
-        p.target_logit = take(ntokens * 4);
+        p.stats = take(p.stat_rows * p.chunk * stats_bytes(kind));
+        p.target_logit = take(p.chunk * 4);
+        if (kind.top) p.logits = take(logit_bytes(p.chunk, round_up(vocab, kTileM)));
     } else {
         p.d = take(ntokens * p.piece * ob);
         p.dt = take(p.piece * p.t_pad * ob);
@@ -977,35 +1033,39 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         p.grad_hidden_acc = take(static_cast<uint64_t>(p.splits) * ntokens * width * 4);
         if (p.weight_splits > 1) p.grad_weight_acc = take(static_cast<uint64_t>(p.weight_splits) * p.piece * width * 4);
         p.row_scale = take(sizeof(RowScale));
+        if (kind.log_probs) p.row_gradients = take(ntokens * 12);
     }
     p.bytes = at;
     return p;
 }
 
-hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPlan& p, ar_dtype_t dtype, char* ws,
-                                hipStream_t stream)
+namespace {
+// fn(call) by the operands' type and form.
+template <class Fn>
+hipError_t by_type(const CrossEntropyArgs& a, const CrossEntropyPlan& p, ar_dtype_t dtype, char* ws, hipStream_t stream,
+                   const Fn& fn)
 {
     switch (dtype) {
     case AR_FLOAT32:
-        return p.pieces ? Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.forward()
-                        : Call<F32, MmaF32, 1>{a, p, ws, stream}.forward();
-    case AR_FLOAT16: return Call<F16, MmaF16, 1>{a, p, ws, stream}.forward();
-    case AR_BFLOAT16: return Call<BF16, MmaBF16, 1>{a, p, ws, stream}.forward();
+        return p.pieces ? fn(Call<F32, MmaBF16, kPieces>{a, p, ws, stream}) : fn(Call<F32, MmaF32, 1>{a, p, ws, stream});
+    case AR_FLOAT16: return fn(Call<F16, MmaF16, 1>{a, p, ws, stream});
+    case AR_BFLOAT16: return fn(Call<BF16, MmaBF16, 1>{a, p, ws, stream});
     default: return hipErrorInvalidValue;
     }
+}
+}  // namespace
+
+hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPlan& p, ar_dtype_t dtype, char* ws,
+                                hipStream_t stream)
+{
+    return by_type(a, p, dtype, ws, stream,
+                   [&](const auto& call) { return a.log_probs ? call.forward_log_probs() : call.forward(); });
 }
 
 hipError_t launch_cross_entropy_backward(const CrossEntropyArgs& a, const CrossEntropyPlan& p, ar_dtype_t dtype,
                                          char* ws, hipStream_t stream)
 {
-    switch (dtype) {
-    case AR_FLOAT32:
-        return p.pieces ? Call<F32, MmaBF16, kPieces>{a, p, ws, stream}.backward()
-                        : Call<F32, MmaF32, 1>{a, p, ws, stream}.backward();
-    case AR_FLOAT16: return Call<F16, MmaF16, 1>{a, p, ws, stream}.backward();
-    case AR_BFLOAT16: return Call<BF16, MmaBF16, 1>{a, p, ws, stream}.backward();
-    default: return hipErrorInvalidValue;
-    }
+    return by_type(a, p, dtype, ws, stream, [](const auto& call) { return call.backward(); });
 }
 
 }  // namespace lm

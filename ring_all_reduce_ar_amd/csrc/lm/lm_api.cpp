@@ -552,15 +552,15 @@ AR_EXPORT size_t ar_linear_cross_entropy_workspace_bytes(size_t ntokens, size_t 
 {
     if (!valid_dtype(dtype) || dtype == AR_INT32 || width == 0 || !plan_fits(ntokens, vocab, width, dtype))
         return static_cast<size_t>(-1);
-    return ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, backward != 0);
+    return ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, {backward != 0, false, 0});
 }
 
 namespace {
 
 ar_result_t cross_entropy_common(ar_comm* comm, const void* hidden, const void* weight, const void* targets,
                                  ar_index_t index, size_t ntokens, size_t vocab, size_t width, size_t* ld_hidden,
-                                 size_t* ld_weight, ar_dtype_t dtype, bool backward, std::vector<Interval>* reads,
-                                 ar::lm::CrossEntropyPlan* plan)
+                                 size_t* ld_weight, ar_dtype_t dtype, ar::lm::HeadKind kind,
+                                 std::vector<Interval>* reads, ar::lm::CrossEntropyPlan* plan)
 {
     if (!comm) return fail(AR_ERR_INVALID_ARGUMENT, "comm is NULL");
     ar_result_t rc = check_float(dtype);
@@ -576,10 +576,10 @@ ar_result_t cross_entropy_common(ar_comm* comm, const void* hidden, const void* 
     if (rc == AR_SUCCESS) rc = check_matrix("weight", weight, vocab, width, ld_weight, e, reads);
     if (rc == AR_SUCCESS) rc = check_vector("targets", targets, ntokens, index_bytes(index), reads);
     if (rc != AR_SUCCESS) return rc;
-    *plan = ar::lm::plan_cross_entropy(ntokens, vocab, width, dtype, backward);
+    *plan = ar::lm::plan_cross_entropy(ntokens, vocab, width, dtype, kind);
     plan->pack_hidden = !direct(hidden, *ld_hidden, width, e, plan->pieces);
     plan->pack_weight = !direct(weight, *ld_weight, width, e, plan->pieces);
-    return check_workspace(comm, ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, backward));
+    return check_workspace(comm, std::max(ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, kind), plan->bytes));
 }
 
 }  // namespace
@@ -594,7 +594,7 @@ AR_EXPORT ar_result_t ar_linear_cross_entropy(ar_comm_t comm, const void* hidden
         std::vector<Interval> reads, writes;
         ar::lm::CrossEntropyPlan p;
         ar_result_t rc = cross_entropy_common(comm, hidden, weight, targets, index, ntokens, vocab, width, &ld_hidden,
-                                              &ld_weight, dtype, false, &reads, &p);
+                                              &ld_weight, dtype, {false, false, 0}, &reads, &p);
         if (rc == AR_SUCCESS) rc = check_vector("losses", losses, ntokens, 4, &writes);
         if (rc == AR_SUCCESS) rc = check_vector("lse", lse, ntokens, 4, &writes);
         if (rc != AR_SUCCESS) return rc;
@@ -631,7 +631,7 @@ AR_EXPORT ar_result_t ar_linear_cross_entropy_backward(ar_comm_t comm, const voi
         std::vector<Interval> reads, writes;
         ar::lm::CrossEntropyPlan p;
         ar_result_t rc = cross_entropy_common(comm, hidden, weight, targets, index, ntokens, vocab, width, &ld_hidden,
-                                              &ld_weight, dtype, true, &reads, &p);
+                                              &ld_weight, dtype, {true, false, 0}, &reads, &p);
         if (rc != AR_SUCCESS) return rc;
         const size_t e = elem_size(dtype);
         rc = check_vector("lse", lse, ntokens, 4, &reads);
@@ -665,6 +665,143 @@ AR_EXPORT ar_result_t ar_linear_cross_entropy_backward(ar_comm_t comm, const voi
         a.ld_grad_hidden = ld_grad_hidden;
         a.ld_grad_weight = ld_grad_weight;
         a.ignore_index = ignore_index;
+        const hipError_t err = ar::lm::launch_cross_entropy_backward(a, p, dtype, static_cast<char*>(comm->ws), stream);
+        return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
+    });
+}
+
+// ---------------------------------------------------------------------------
+// log probabilities
+// ---------------------------------------------------------------------------
+namespace {
+
+// Alternatives keep the logits of one tile's tokens at least.
+constexpr uint64_t kMostTopVocab = uint64_t(1) << 24;
+
+ar_result_t check_log_probs(size_t vocab, float scale, int top)
+{
+    if (!(scale > 0.0f) || std::isinf(scale))
+        return fail(AR_ERR_INVALID_ARGUMENT, "scale %g is not a finite number above 0", static_cast<double>(scale));
+    if (top < 0 || top > ar::lm::kMostTop || static_cast<size_t>(top) > vocab)
+        return fail(AR_ERR_INVALID_ARGUMENT, "top %d is outside 0..min(%d, vocab %zu)", top, ar::lm::kMostTop, vocab);
+    if (top && vocab >= kMostTopVocab)
+        return fail(AR_ERR_INVALID_ARGUMENT, "alternatives need a vocabulary below 2^24, not of %zu", vocab);
+    return AR_SUCCESS;
+}
+
+}  // namespace
+
+AR_EXPORT size_t ar_linear_log_probs_workspace_bytes(size_t ntokens, size_t vocab, size_t width, ar_dtype_t dtype,
+                                                     int top, int backward)
+{
+    if (!valid_dtype(dtype) || dtype == AR_INT32 || width == 0 || !plan_fits(ntokens, vocab, width, dtype) || top < 0 ||
+        top > ar::lm::kMostTop || (top && vocab >= kMostTopVocab))
+        return static_cast<size_t>(-1);
+    return ar::lm::cross_entropy_bytes(ntokens, vocab, width, dtype, {backward != 0, true, top});
+}
+
+AR_EXPORT ar_result_t ar_linear_log_probs(ar_comm_t comm, const void* hidden, const void* weight, const void* targets,
+                                          ar_index_t index, float* log_probs, float* entropy, float* lse, int top,
+                                          float* top_log_probs, int* top_ids, size_t ntokens, size_t vocab,
+                                          size_t width, size_t ld_hidden, size_t ld_weight, float scale,
+                                          long long ignore_index, ar_dtype_t dtype, hipStream_t stream)
+{
+    return guarded([&] {
+        std::vector<Interval> reads, writes;
+        ar::lm::CrossEntropyPlan p;
+        ar_result_t rc = check_log_probs(vocab, scale, top);
+        if (rc == AR_SUCCESS)
+            rc = cross_entropy_common(comm, hidden, weight, targets, index, ntokens, vocab, width, &ld_hidden, &ld_weight,
+                                      dtype, {false, true, top}, &reads, &p);
+        if (rc == AR_SUCCESS) rc = check_vector("log_probs", log_probs, ntokens, 4, &writes);
+        if (rc == AR_SUCCESS && entropy) rc = check_vector("entropy", entropy, ntokens, 4, &writes);
+        if (rc == AR_SUCCESS) rc = check_vector("lse", lse, ntokens, 4, &writes);
+        if (rc == AR_SUCCESS && top) rc = check_vector("top_log_probs", top_log_probs, ntokens * top, 4, &writes);
+        if (rc == AR_SUCCESS && top) rc = check_vector("top_ids", top_ids, ntokens * top, 4, &writes);
+        if (rc != AR_SUCCESS) return rc;
+        const uintptr_t w = reinterpret_cast<uintptr_t>(comm->ws);
+        writes.push_back({w, w + p.bytes, "workspace", 0});
+        if ((rc = check_disjoint(reads, writes)) != AR_SUCCESS || ntokens == 0) return rc;
+        DeviceGuard g(comm->device);
+        if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");
+        ar::lm::CrossEntropyArgs a{};
+        a.hidden = hidden;
+        a.weight = weight;
+        a.targets = {targets, index == AR_INDEX_INT64};
+        a.losses = log_probs;
+        a.entropy = entropy;
+        a.lse = lse;
+        a.top = top;
+        a.top_log_probs = top_log_probs;
+        a.top_ids = top_ids;
+        a.ntokens = ntokens;
+        a.vocab = vocab;
+        a.width = width;
+        a.ld_hidden = ld_hidden;
+        a.ld_weight = ld_weight;
+        a.ignore_index = ignore_index;
+        a.log_probs = true;
+        a.scale = scale;
+        const hipError_t err = ar::lm::launch_cross_entropy(a, p, dtype, static_cast<char*>(comm->ws), stream);
+        return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
+    });
+}
+
+AR_EXPORT ar_result_t ar_linear_log_probs_backward(ar_comm_t comm, const void* hidden, const void* weight,
+                                                   const void* targets, ar_index_t index, const float* lse,
+                                                   const float* entropy, const float* grad_log_probs,
+                                                   const float* grad_entropy, void* grad_hidden, void* grad_weight,
+                                                   size_t ntokens, size_t vocab, size_t width, size_t ld_hidden,
+                                                   size_t ld_weight, size_t ld_grad_hidden, size_t ld_grad_weight,
+                                                   float scale, long long ignore_index, ar_dtype_t dtype,
+                                                   hipStream_t stream)
+{
+    return guarded([&] {
+        std::vector<Interval> reads, writes;
+        ar::lm::CrossEntropyPlan p;
+        ar_result_t rc = check_log_probs(vocab, scale, 0);
+        if (rc == AR_SUCCESS)
+            rc = cross_entropy_common(comm, hidden, weight, targets, index, ntokens, vocab, width, &ld_hidden, &ld_weight,
+                                      dtype, {true, true, 0}, &reads, &p);
+        if (rc != AR_SUCCESS) return rc;
+        const size_t e = elem_size(dtype);
+        rc = check_vector("lse", lse, ntokens, 4, &reads);
+        if (rc == AR_SUCCESS) rc = check_vector("grad_log_probs", grad_log_probs, ntokens, 4, &reads);
+        if (rc == AR_SUCCESS && grad_entropy) rc = check_vector("grad_entropy", grad_entropy, ntokens, 4, &reads);
+        if (rc == AR_SUCCESS && grad_entropy) rc = check_vector("entropy", entropy, ntokens, 4, &reads);
+        if (rc == AR_SUCCESS && grad_hidden)
+            rc = check_matrix("grad_hidden", grad_hidden, ntokens, width, &ld_grad_hidden, e, &writes);
+        if (rc == AR_SUCCESS && grad_weight)
+            rc = check_matrix("grad_weight", grad_weight, vocab, width, &ld_grad_weight, e, &writes);
+        if (rc != AR_SUCCESS) return rc;
+        if (!grad_hidden && !grad_weight)
+            return fail(AR_ERR_INVALID_ARGUMENT, "grad_hidden and grad_weight are both NULL");
+        const uintptr_t w = reinterpret_cast<uintptr_t>(comm->ws);
+        writes.push_back({w, w + p.bytes, "workspace", 0});
+        if ((rc = check_disjoint(reads, writes)) != AR_SUCCESS) return rc;
+        if (ntokens == 0 && !grad_weight) return AR_SUCCESS;
+        DeviceGuard g(comm->device);
+        if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");
+        ar::lm::CrossEntropyArgs a{};
+        a.hidden = hidden;
+        a.weight = weight;
+        a.targets = {targets, index == AR_INDEX_INT64};
+        a.lse = const_cast<float*>(lse);
+        a.entropy = const_cast<float*>(entropy);
+        a.grad_losses = grad_log_probs;
+        a.grad_entropy = grad_entropy;
+        a.grad_hidden = grad_hidden;
+        a.grad_weight = grad_weight;
+        a.ntokens = ntokens;
+        a.vocab = vocab;
+        a.width = width;
+        a.ld_hidden = ld_hidden;
+        a.ld_weight = ld_weight;
+        a.ld_grad_hidden = ld_grad_hidden;
+        a.ld_grad_weight = ld_grad_weight;
+        a.ignore_index = ignore_index;
+        a.log_probs = true;
+        a.scale = scale;
         const hipError_t err = ar::lm::launch_cross_entropy_backward(a, p, dtype, static_cast<char*>(comm->ws), stream);
         return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
     });

@@ -1,5 +1,6 @@
 // lm_kernels.h -- internal interface between lm_api.cpp and the kernels of the
-// language-model operators (clip.hip, embedding.hip, cross_entropy.hip).
+// language-model operators (clip.hip, embedding.hip, cross_entropy.hip with
+// log_probs.h, orthogonalize.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -129,6 +130,22 @@ struct CrossEntropyArgs {
     uint64_t ntokens, vocab, width;
     uint64_t ld_hidden, ld_weight, ld_grad_hidden, ld_grad_weight;
     int64_t ignore_index;
+    // log probabilities: `losses` are those, grad_losses their gradients
+    bool log_probs;
+    float scale;
+    float* entropy;             // written forward (may be null), read backward
+    const float* grad_entropy;  // backward; may be null
+    int top;                    // alternatives, up to kMostTop
+    float* top_log_probs;
+    int32_t* top_ids;
+};
+constexpr int kMostTop = 64;
+
+// What a call of a linear head is.
+struct HeadKind {
+    bool backward;
+    bool log_probs;
+    int top;
 };
 
 // How one call goes through the vocabulary, and where its buffers lie in the
@@ -143,12 +160,14 @@ struct CrossEntropyPlan {
     int splits;            // parts of the vocabulary axis in the hidden gradient's product
     int weight_splits;     // parts of the token axis in the weight gradient's
     uint64_t stat_rows;    // rows of partial softmax statistics
+    uint64_t chunk;        // tokens of a forward pass; fewer than all where alternatives keep their logits
     // offsets
     uint64_t hidden, weight, stats, target_logit, d, dt, weight_t, hidden_t, grad_hidden_acc, grad_weight_acc, row_scale, bytes;
+    uint64_t logits, row_gradients;
 };
 // At least the bytes of the plans of `ntokens` and of fewer tokens.
-uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward);
-CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, bool backward);
+uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, HeadKind kind);
+CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, HeadKind kind);
 
 hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPlan& p, ar_dtype_t dtype, char* ws,
                                 hipStream_t stream);

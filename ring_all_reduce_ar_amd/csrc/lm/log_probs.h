@@ -1,0 +1,421 @@
+// log_probs.h -- log probabilities under a linear head: what cross_entropy.hip's
+// products need beyond the loss.
+//
+//   z[t][v] = s x[t] . w[v],  lse[t] = log sum_v exp z[t][v],  lp[t] = z[t][y[t]] - lse[t]
+//   H[t] = -sum_v p log p = log S - (sum_v e^u u) / S,  u = z - max z <= 0, S = sum_v e^u
+//   dz[t][v] = s (a[t] ([v = y[t]] - p) - b[t] p (log p + H[t])),  a, b the gradients of lp and H
+//
+// Both terms of H are at least 0, so nothing cancels. A wave's part of a row is
+// a group of neighbouring vocabulary rows, whose maximum the softmax needs
+// anyway: the `top` largest logits lie in the `top` groups of largest maxima
+// (the first of equal ones first), so alternatives cost one store of the logits
+// and a read of those groups alone.
+#pragma once
+
+#include <type_traits>
+
+#include "head.h"
+
+namespace ar {
+namespace lm {
+namespace {
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+struct LogParts {
+    float top, sum, dot;  // of u = z - top: the sums of e^u and of e^u u
+};
+
+// The logits of a chunk of tokens, kept for their alternatives: group after
+// group of 16 MT vocabulary rows, in it blocks of 16 tokens, in those MT blocks
+// of 16 x 16, so that one store of a wave is 1024 bytes on end.
+__host__ __device__ constexpr uint64_t logit_at(uint64_t group, uint64_t token_blocks, uint64_t token, uint32_t groups_of_16,
+                                                uint32_t row)
+{
+    return ((group * token_blocks + token / 16) * groups_of_16 + row / 16) * 256 + token % 16 * 16 + row % 16;
+}
+
+// A wave's part of each token's row, as StatsEpilogue, and its logits.
+struct LogPartsEpilogue {
+    LogParts* parts;      // [group][token of the chunk]
+    float* target_logit;  // [token of the chunk]
+    float* logits;        // or null
+    Indices targets;
+    int64_t ignore;
+    uint64_t vocab, v0, row0;
+    uint64_t first_token;
+    float scale;
+
+    template <int MT, int NT, class S>
+    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const GemmArgs& g,
+                                               uint32_t mrow, uint32_t, const S&) const
+    {
+        if (m0 + MT * 16 <= g.m) write<true>(acc, m0, n0, g, mrow);
+        else write<false>(acc, m0, n0, g, mrow);
+    }
+
+private:
+    template <bool FULL, int MT, int NT>
+    __device__ __forceinline__ void write(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const GemmArgs& g,
+                                          uint32_t mrow) const
+    {
+        const int lane = threadIdx.x & 63, quad = lane >> 4;
+        const uint32_t mine = m0 + quad * 4;
+        const uint64_t blocks = (g.n + 15) / 16;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            if (n0 + j * 16 >= g.n) break;
+            const uint32_t t = n0 + j * 16 + (lane & 15);
+            const bool ok = t < g.n;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                acc.v[i][j] *= scale;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (FULL || mine + 16 * i + r < g.m) top = fmaxf(top, acc.v[i][j][r]);
+            }
+            if (logits) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    __builtin_nontemporal_store(acc.v[i][j], reinterpret_cast<f32x4*>(
+                                                                 logits + logit_at(row0 + mrow, blocks, t, MT, 16 * i + quad * 4)));
+            }
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (FULL || mine + 16 * i + r < g.m) {
+                        const float u = acc.v[i][j][r] - base, e = __builtin_amdgcn_exp2f(u * kLog2e);
+                        sum += e;
+                        dot += e > 0.0f ? e * u : 0.0f;  // a logit of -infinity adds nothing
+                    }
+            sum += __shfl_xor(sum, 16, 64);
+            dot += __shfl_xor(dot, 16, 64);
+            sum += __shfl_xor(sum, 32, 64);
+            dot += __shfl_xor(dot, 32, 64);
+            if (ok && quad == 0) parts[(row0 + mrow) * g.n + t] = LogParts{top, sum, dot};
+            const uint32_t at =
+                ok ? target_at<MT>(load_target(targets, first_token + t, ignore, vocab), v0 + mine) : kNoTarget;
+            if (!__any(at != kNoTarget)) continue;  // few tiles hold a target
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (at == static_cast<uint32_t>(16 * i + r)) target_logit[t] = acc.v[i][j][r];
+        }
+    }
+};
+
+__device__ __forceinline__ LogParts join_parts(LogParts a, LogParts b)
+{
+    const float m = fmaxf(a.top, b.top);
+    if (m == -INFINITY) return LogParts{m, a.sum + b.sum, 0.0f};
+    // (the part of nothing has the top -infinity and sums of 0)
+    const float da = fmaxf(a.top - m, -1e4f), db = fmaxf(b.top - m, -1e4f);
+    const float fa = __builtin_amdgcn_exp2f(da * kLog2e), fb = __builtin_amdgcn_exp2f(db * kLog2e);
+    return LogParts{m, a.sum * fa + b.sum * fb, (a.dot + da * a.sum) * fa + (b.dot + db * b.sum) * fb};
+}
+
+struct LogProbOut {
+    Indices targets;
+    int64_t ignore;
+    uint64_t vocab, first_token, ntokens;  // the chunk's tokens
+    const float* target_logit;             // of the chunk
+    float *log_probs, *entropy, *lse;      // of the call; entropy may be null
+
+    __device__ __forceinline__ float put(uint64_t t, const LogParts& s) const
+    {
+        const uint64_t at = first_token + t;
+        const float log_sum = logf(s.sum), l = s.top + log_sum;
+        lse[at] = l;
+        log_probs[at] = load_target(targets, at, ignore, vocab) >= 0 ? target_logit[t] - l : 0.0f;
+        if (entropy) entropy[at] = log_sum - s.dot / s.sum;
+        return l;
+    }
+};
+
+// Joins the parts of each token's row, as join_stats.
+template <int X>
+__global__ __launch_bounds__(kJoinBlock) void join_log_probs(const LogParts* parts, uint64_t groups, LogProbOut out)
+{
+    constexpr int Y = kJoinBlock / X;
+    __shared__ LogParts part[Y][X];
+    const int x = threadIdx.x % X, y = threadIdx.x / X;
+    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * X + x;
+    LogParts s{-INFINITY, 0.0f, 0.0f};
+    if (t < out.ntokens) {
+#pragma unroll 4
+        for (uint64_t r = y; r < groups; r += Y) s = join_parts(s, parts[r * out.ntokens + t]);
+    }
+    part[y][x] = s;
+#pragma unroll
+    for (int h = Y / 2; h >= 1; h /= 2) {
+        __syncthreads();
+        if (y < h) part[y][x] = join_parts(part[y][x], part[y + h][x]);
+    }
+    if (y == 0 && t < out.ntokens) out.put(t, part[0][x]);
+}
+
+// ---------------------------------------------------------------------------
+// alternatives
+// ---------------------------------------------------------------------------
+// The order of alternatives as one number: the larger value first, of equal ones
+// the smaller id. NaN counts as -infinity, -0 as 0; 0 is below every key.
+__device__ __forceinline__ uint64_t order_key(float z, uint32_t id)
+{
+    const uint32_t bits = as_u(z != z ? -INFINITY : z + 0.0f);
+    const uint32_t high = bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+    return static_cast<uint64_t>(high) << 32 | ~id;
+}
+__device__ __forceinline__ float key_value(uint64_t key)
+{
+    const uint32_t high = static_cast<uint32_t>(key >> 32);
+    return as_f(high & 0x80000000u ? high ^ 0x80000000u : ~high);
+}
+__device__ __forceinline__ uint32_t key_id(uint64_t key) { return ~static_cast<uint32_t>(key); }
+
+// The largest value of a wave, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+    auto step = [&](auto dpp, auto rows) {
+        const uint32_t y = __builtin_amdgcn_update_dpp(0, x, decltype(dpp)::value, decltype(rows)::value, 0xF, false);
+        x = x > y ? x : y;
+    };
+    step(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});  // the lane below in a row of 16
+    step(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
+    step(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
+    step(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row 0 to 1, 2 to 3
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // row 1 to 2 and 3
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// A wave's list of the `top` (at most 64) largest keys that it has met, lane l
+// holding the l-th.
+constexpr int kTopBatch = 8;
+struct TopList {
+    uint64_t mine = 0;   // this lane's place
+    uint64_t last = 0;   // the list's last key: what is not above it has no place
+    // Keys of one batch (0: none), each met once.
+    __device__ __forceinline__ void add(uint64_t (&key)[kTopBatch], int top)
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < kTopBatch; ++i) best = key[i] > best ? key[i] : best;
+        if (!__any(best > last)) return;
+        best = mine > best ? mine : best;
+        uint64_t held = mine, list = 0;
+        for (int k = 0; k < top; ++k) {
+            const uint32_t high = wave_max(static_cast<uint32_t>(best >> 32));
+            if (high == 0) break;  // no more keys
+            const bool first = static_cast<uint32_t>(best >> 32) == high;
+            const uint32_t low = wave_max(first ? static_cast<uint32_t>(best) : 0u);
+            const uint64_t won = static_cast<uint64_t>(high) << 32 | low;
+            if (lane == static_cast<uint32_t>(k)) list = won;
+            if (best == won) {  // one lane: it goes on with its next one
+                held = held == won ? 0 : held;
+                best = held;
+#pragma unroll
+                for (int i = 0; i < kTopBatch; ++i) {
+                    key[i] = key[i] == won ? 0 : key[i];
+                    best = key[i] > best ? key[i] : best;
+                }
+            }
+        }
+        mine = list;
+        last = __shfl(mine, top - 1, 64);
+    }
+};
+
+// The alternatives of a chunk's tokens, and with them the join of their parts.
+// W waves work on a token and join their lists through LDS: 8 for few tokens,
+// where the time is latency, 1 (4 tokens a workgroup) for many.
+template <int W>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogParts* parts, uint64_t groups,
+                                                                    const float* logits, uint32_t group_rows, int top,
+                                                                    LogProbOut out, float* top_log_probs,
+                                                                    int32_t* top_ids)
+{
+    constexpr int TOKENS = W == 1 ? 4 : 1;
+    __shared__ uint64_t lists[TOKENS][W][64];
+    __shared__ LogParts sums[TOKENS][W];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int slot = W == 1 ? wave : 0, w = W == 1 ? 0 : wave;
+    const uint64_t t = static_cast<uint64_t>(blockIdx.x) * TOKENS + slot, n = out.ntokens;
+    const bool on = t < n;  // (the same for a wave; all meet at the barriers)
+
+    // the waves' lists become one, in every wave
+    auto join_lists = [&](TopList& list) {
+        if constexpr (W > 1) {
+            __syncthreads();
+            lists[slot][w][lane] = list.mine;
+            __syncthreads();
+            list = TopList{};
+            uint64_t key[kTopBatch] = {};
+            static_assert(W <= kTopBatch, "one batch takes all lists");
+#pragma unroll
+            for (int i = 0; i < W; ++i) key[i] = lists[slot][i][lane];
+            list.add(key, top);
+        }
+    };
+
+    TopList best;
+    LogParts s{-INFINITY, 0.0f, 0.0f};
+    if (on) {
+        for (uint64_t g0 = static_cast<uint64_t>(w) * 64 * kTopBatch; g0 < groups; g0 += W * 64 * kTopBatch) {
+            uint64_t key[kTopBatch];
+#pragma unroll
+            for (int i = 0; i < kTopBatch; ++i) {
+                const uint64_t g = g0 + i * 64 + lane;
+                key[i] = 0;
+                if (g < groups) {
+                    const LogParts p = parts[g * n + t];
+                    key[i] = order_key(p.top, static_cast<uint32_t>(g));
+                    s = join_parts(s, p);
+                }
+            }
+            best.add(key, top);
+        }
+#pragma unroll
+        for (int m = 1; m <= 32; m *= 2)
+            s = join_parts(s, LogParts{__shfl_xor(s.top, m, 64), __shfl_xor(s.sum, m, 64), __shfl_xor(s.dot, m, 64)});
+    }
+    join_lists(best);
+    if constexpr (W > 1) {
+        if (lane == 0) sums[slot][w] = s;
+        __syncthreads();
+        s = sums[slot][0];
+#pragma unroll
+        for (int i = 1; i < W; ++i) s = join_parts(s, sums[slot][i]);
+    }
+
+    TopList found;
+    if (on) {
+        const uint64_t blocks = (n + 15) / 16;
+        const uint32_t per_batch = 64 * kTopBatch / group_rows;  // groups
+        for (uint32_t k0 = w * per_batch; k0 < static_cast<uint32_t>(top); k0 += W * per_batch) {
+            uint64_t key[kTopBatch];
+#pragma unroll
+            for (int i = 0; i < kTopBatch; ++i) {
+                const uint32_t e = i * 64 + lane, k = k0 + e / group_rows, row = e % group_rows;
+                const uint64_t group = __shfl(best.mine, k & 63, 64);
+                key[i] = 0;
+                if (k < static_cast<uint32_t>(top) && group != 0) {
+                    const uint64_t id = static_cast<uint64_t>(key_id(group)) * group_rows + row;
+                    if (id < out.vocab)
+                        key[i] = order_key(logits[logit_at(key_id(group), blocks, t, group_rows / 16, row)],
+                                           static_cast<uint32_t>(id));
+                }
+            }
+            found.add(key, top);
+        }
+    }
+    join_lists(found);
+    if (!on || w != 0) return;
+    const float l = s.top + logf(s.sum);
+    if (lane == 0) out.put(t, s);
+    if (lane < top) {
+        const uint64_t at = (out.first_token + t) * top + lane;
+        top_log_probs[at] = key_value(found.mine) - l;
+        top_ids[at] = static_cast<int32_t>(key_id(found.mine));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// d of a row is held over the row's larger gradient g = s max(|a|, |b|): |p
+// (log p + H)| is below 6 for a vocabulary of 2^28, so that 2^12 d stays within
+// fp16, where its steps are then 2^-36.
+constexpr float kLogProbBits = 12.0f, kLogProbScale = 4096.0f;
+
+struct RowGradients {
+    float* g;  // [token]
+    float* a;  // over g / s
+    float* b;
+};
+
+__global__ __launch_bounds__(1024) void row_gradients(const float* grad_log_probs, const float* grad_entropy,
+                                                      float scale, Indices targets, int64_t ignore, uint64_t vocab,
+                                                      uint64_t ntokens, RowGradients out, RowScale* top_out)
+{
+    __shared__ float waves[16];
+    float top = 0.0f;
+    for (uint64_t t = threadIdx.x; t < ntokens; t += 1024) {
+        float g = 0.0f, a = 0.0f, b = 0.0f;
+        if (load_target(targets, t, ignore, vocab) >= 0) {
+            const float x = grad_log_probs[t], y = grad_entropy ? grad_entropy[t] : 0.0f;
+            const float most = fmaxf(fabsf(x), fabsf(y));
+            g = scale * most;
+            // (subnormal gradients take a factor of their own: their reciprocal may be infinite)
+            const float up = most < 0x1p-100f ? 0x1p40f : 1.0f;
+            a = most == 0.0f ? 0.0f : x * up / (most * up);
+            b = most == 0.0f ? 0.0f : y * up / (most * up);
+            if (x != x || y != y) g = NAN;
+            top = fmaxf(top, g);
+        }
+        out.g[t] = g;
+        out.a[t] = a;
+        out.b[t] = b;
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) top = fmaxf(top, waves[w]);
+        top_out->top = fmaxf(top, 0x1p-126f);  // whose reciprocal is finite
+    }
+}
+
+// The part of d that a tile's epilogue computes before it is stored: 2^12 (a
+// [v = y] - p (a + b (log p + H))).
+struct LogProbD {
+    const float* lse;
+    const float* entropy;  // null where no gradient comes through it
+    RowGradients rows;
+    float scale;
+
+    struct Row {
+        float lse, entropy, a, b, g;
+    };
+    __device__ __forceinline__ Row row(uint64_t t, bool on) const
+    {
+        return on ? Row{lse[t], entropy ? entropy[t] : 0.0f, rows.a[t], rows.b[t], rows.g[t]} : Row{};
+    }
+    __device__ __forceinline__ float operator()(const Row& x, float product) const
+    {
+        float log_p = __builtin_fmaf(product, scale, -x.lse);
+        log_p = log_p < -200.0f ? -200.0f : log_p;  // finite, of probability 0
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(log_p, kLog2e, kLogProbBits));
+        return -p * __builtin_fmaf(x.b, log_p + x.entropy, x.a);
+    }
+    __device__ __forceinline__ float at_target(const Row& x) const { return x.a * kLogProbScale; }
+};
+
+// The same for the loss: 2^14 (p - [v = y]).
+struct LossD {
+    const float* lse;
+    const float* g;
+
+    struct Row {
+        float lse, g;
+    };
+    __device__ __forceinline__ Row row(uint64_t t, bool on) const { return on ? Row{lse[t], g[t]} : Row{}; }
+    __device__ __forceinline__ float operator()(const Row& x, float product) const
+    {
+        return __builtin_amdgcn_exp2f(__builtin_fmaf(product - x.lse, kLog2e, kDBits));
+    }
+    __device__ __forceinline__ float at_target(const Row&) const { return -kDScale; }
+};
+
+}  // namespace
+}  // namespace lm
+}  // namespace ar
