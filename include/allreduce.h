@@ -472,6 +472,47 @@ ar_result_t ar_linear_log_probs_backward(ar_comm_t comm, const void* hidden, con
                                          size_t ld_grad_weight, float scale, long long ignore_index, ar_dtype_t dtype,
                                          hipStream_t stream);
 
+/* Workspace of the two calls below for so many matrices, on any number of
+ * ranks; (size_t)-1 for sizes they do not take. */
+size_t ar_orthogonalize_workspace_bytes(int nmatrices, size_t rows, size_t cols);
+
+/* Makes matrices of one size nearly orthogonal by Newton-Schulz products, the
+ * update of the Muon optimiser:
+ *   X = in / max(|in|, eps)                        (|.| the root of the sum of squares)
+ *   X <- a X + (b A + c A A) X,  A = X X^T         (`steps` times, 1 to 32)
+ *   out = X,
+ * on the transposed matrix where it has more rows than columns, which gives the
+ * same. coefficients (host): a, b and c of every step, or NULL for 3.4445,
+ * -4.7750, 2.0315 in each; |a| is at most 16, |b| and |c| at most 32, and c is 0 or
+ * so large that |b| <= 16 |c| and b^2 <= 64 |c|. Sums are fp32 or fp64; X and what
+ * is made of it is held to 22 bits, within |x| < 32 (beyond, results are NaN).
+ * A matrix that holds a NaN or an infinity, or whose iteration diverges, gives
+ * NaN; one of zeros gives zeros. in and out are of dtype. In place (in[t] ==
+ * out[t] of one pitch) is allowed; what a matrix spans with its pitch overlaps no
+ * other that is written. Sides are below 2^20, the smaller up to 2^16, a matrix up to
+ * 2^34 elements. eps: at least 1e-30. nmatrices <= AR_MAX_TENSORS. */
+ar_result_t ar_orthogonalize(ar_comm_t comm, int nmatrices, const void* const in[], void* const out[], size_t rows,
+                             size_t cols, size_t ld_in, size_t ld_out, int steps, const double coefficients[],
+                             double eps, ar_dtype_t dtype, hipStream_t stream);
+
+/* The whole update of weight matrices of one size, given gradients that are the
+ * same on every rank, as after an all-reduce:
+ *   momentum_out = decay * momentum_in + (1 - decay) * grads,
+ *   U = nesterov ? decay * momentum_out + (1 - decay) * grads : momentum_out,
+ *   weights_out = (1 - lr * weight_decay) * weights_in - lr * update_scale * X,
+ * with X the orthogonalised U as above, in fp32. grads (dtype), momentum (fp32)
+ * and weights_in are one buffer a matrix; weights_out[t*nranks + r] is rank r's
+ * replica, all of which get the same. weights_in and weights_out are of
+ * weight_dtype: dtype or fp32. decay: in [0, 1). In place is allowed for the
+ * momentum (momentum_in[t] == momentum_out[t]) and for the weights (one of a
+ * matrix's replicas == weights_in[t]). */
+ar_result_t ar_muon_update(ar_comm_t comm, int nmatrices, const void* const grads[], const float* const momentum_in[],
+                           float* const momentum_out[], const void* const weights_in[], void* const weights_out[],
+                           size_t rows, size_t cols, size_t ld_grads, size_t ld_momentum, size_t ld_weights,
+                           double decay, int nesterov, double lr, double weight_decay, double update_scale, int steps,
+                           const double coefficients[], double eps, ar_dtype_t dtype, ar_dtype_t weight_dtype,
+                           hipStream_t stream);
+
 /* Static description of a result code. */
 const char* ar_result_string(ar_result_t result);
 

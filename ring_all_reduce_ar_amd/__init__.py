@@ -69,6 +69,7 @@ EXPORTED_SYMBOLS = (
     "ar_embedding", "ar_embedding_workspace_bytes", "ar_embedding_backward",
     "ar_linear_cross_entropy_workspace_bytes", "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward",
     "ar_linear_log_probs_workspace_bytes", "ar_linear_log_probs", "ar_linear_log_probs_backward",
+    "ar_orthogonalize_workspace_bytes", "ar_orthogonalize", "ar_muon_update",
     "ar_result_string", "ar_last_error",
 )
 
@@ -116,6 +117,13 @@ _lib.ar_linear_log_probs.argtypes = ([_vp, _vp, _vp, _vp, _c_int, _vp, _vp, _vp,
                                      [ctypes.c_float, _c_i64, _c_int, _vp])
 _lib.ar_linear_log_probs_backward.argtypes = ([_vp, _vp, _vp, _vp, _c_int] + [_vp] * 6 + [_c_size] * 7 +
                                               [ctypes.c_float, _c_i64, _c_int, _vp])
+_double_array = ctypes.POINTER(ctypes.c_double)
+_lib.ar_orthogonalize_workspace_bytes.argtypes = [_c_int] + [_c_size] * 2
+_lib.ar_orthogonalize_workspace_bytes.restype = _c_size
+_lib.ar_orthogonalize.argtypes = ([_vp, _c_int, _ptr_array, _ptr_array] + [_c_size] * 4 +
+                                  [_c_int, _double_array, ctypes.c_double, _c_int, _vp])
+_lib.ar_muon_update.argtypes = ([_vp, _c_int] + [_ptr_array] * 5 + [_c_size] * 5 + [ctypes.c_double, _c_int] +
+                                [ctypes.c_double] * 3 + [_c_int, _double_array, ctypes.c_double, _c_int, _c_int, _vp])
 _lib.ar_result_string.argtypes = [_c_int]
 _lib.ar_result_string.restype = ctypes.c_char_p
 _lib.ar_last_error.argtypes = []
@@ -126,7 +134,7 @@ for _name in ("ar_comm_create", "ar_comm_destroy", "ar_comm_set_workspace", "ar_
               "ar_comm_set_streaming", "ar_comm_set_access", "ar_last_step_times_ms",
               "ar_grad_norm", "ar_clip_grads", "ar_all_reduce_clip", "ar_embedding", "ar_embedding_backward",
               "ar_linear_cross_entropy", "ar_linear_cross_entropy_backward", "ar_linear_log_probs",
-              "ar_linear_log_probs_backward"):
+              "ar_linear_log_probs_backward", "ar_orthogonalize", "ar_muon_update"):
     getattr(_lib, _name).restype = _c_int
 
 
@@ -543,3 +551,77 @@ def ar_linear_log_probs_backward(comm, hidden, weight, targets, lse, entropy, gr
                                              vocab, width, ld_hidden, ld_weight, ld_grad_hidden, ld_grad_weight, scale,
                                              ignore_index, _enum(dtype, DTYPE_NAMES, "dtype"),
                                              _stream(stream, _device(comm))), "ar_linear_log_probs_backward")
+
+
+def ar_orthogonalize_workspace_bytes(nmatrices: int, rows: int, cols: int) -> int:
+    return _check_size(_lib.ar_orthogonalize_workspace_bytes(nmatrices, rows, cols), "ar_orthogonalize_workspace_bytes")
+
+
+def _matrices(bufs, ld: int):
+    """(addresses, row pitch) of a list of matrices of one size: the tensors' own
+    pitch, the same for all, where none is given."""
+    bufs = _flat(bufs)
+    if ld or not len(bufs) or isinstance(bufs[0], int):
+        return _ptrs([b if isinstance(b, int) else _rows(b, ld or 1)[0] for b in bufs] if ld else bufs), ld
+    rows = [_rows(b, 0) for b in bufs]
+    if any(pitch != rows[0][1] for _, pitch in rows):
+        raise ValueError("the matrices of a list have one row pitch")
+    return _ptrs([p for p, _ in rows]), rows[0][1]
+
+
+def _coefficients(coefficients, steps: int):
+    if coefficients is None:
+        return None
+    flat = [float(x) for step in coefficients for x in (step if isinstance(step, (list, tuple)) else [step])]
+    if len(flat) == 3:
+        flat *= steps
+    if len(flat) != 3 * steps:
+        raise ValueError(f"{steps} steps take 3 or {3 * steps} coefficients, not {len(flat)}")
+    return (ctypes.c_double * len(flat))(*flat)
+
+
+def _same_length(what: str, got: int, want: int):
+    if got != want:
+        raise ValueError(f"{what}: {got} matrices where there are {want}")
+
+
+def ar_orthogonalize(comm, ins, outs, rows: int, cols: int, dtype, steps: int = 5, coefficients=None, eps: float = 1e-7,
+                     ld_in: int = 0, ld_out: int = 0, stream=None):
+    """outs[t] = ins[t] / max(norm, eps) after ``steps`` Newton-Schulz steps, for
+    lists of matrices [rows][cols]. coefficients: (a, b, c), or three for each
+    step."""
+    _same_length("outs", len(outs), len(ins))
+    p, ld_in = _matrices(ins, ld_in)
+    q, ld_out = (p, ld_in) if outs is ins and not ld_out else _matrices(outs, ld_out)
+    _check(_lib.ar_orthogonalize(_h(comm), len(ins), p, q, rows, cols, ld_in, ld_out, steps,
+                                 _coefficients(coefficients, steps), eps, _enum(dtype, DTYPE_NAMES, "dtype"),
+                                 _stream(stream, _device(comm))), "ar_orthogonalize")
+
+
+def ar_muon_update(comm, grads, momentum_in, momentum_out, weights_in, weights_out, rows: int, cols: int, dtype,
+                   weight_dtype=None, decay: float = 0.95, nesterov: bool = True, lr: float = 0.02,
+                   weight_decay: float = 0.0, update_scale: float = 1.0, steps: int = 5, coefficients=None,
+                   eps: float = 1e-7, ld_grads: int = 0, ld_momentum: int = 0, ld_weights: int = 0, stream=None):
+    """The update of weight matrices [rows][cols] by orthogonalised momentum.
+    weights_out: one list of per-rank replicas per matrix (``weights_out[t][r]``),
+    or a flat matrix-major list; the others one buffer per matrix."""
+    n = len(grads)
+    flat = _flat(weights_out)
+    nranks = max(comm.nranks if isinstance(comm, Comm) else ar_comm_nranks(comm), 1)
+    for what, got, want in (("momentum_in", len(momentum_in), n), ("momentum_out", len(momentum_out), n),
+                            ("weights_in", len(weights_in), n),
+                            ("weights_out", len(flat), n * nranks)):
+        _same_length(what, got, want)
+    d = _enum(dtype, DTYPE_NAMES, "dtype")
+    g, ld_grads = _matrices(grads, ld_grads)
+    mi, ld_in = _matrices(momentum_in, ld_momentum)
+    mo, ld_momentum = (mi, ld_in) if momentum_out is momentum_in else _matrices(momentum_out, ld_momentum)
+    wi, ld_read = _matrices(weights_in, ld_weights)
+    wo, ld_weights = _matrices(flat, ld_weights)
+    if n and ((ld_in or cols) != (ld_momentum or cols) or (ld_read or cols) != (ld_weights or cols)):
+        raise ValueError("momentum_in and momentum_out, and weights_in and weights_out, have one row pitch each")
+    _check(_lib.ar_muon_update(_h(comm), n, g, mi, mo, wi, wo, rows, cols, ld_grads, ld_momentum, ld_weights, decay,
+                               1 if nesterov else 0, lr, weight_decay, update_scale, steps,
+                               _coefficients(coefficients, steps), eps, d,
+                               d if weight_dtype is None else _enum(weight_dtype, DTYPE_NAMES, "weight_dtype"),
+                               _stream(stream, _device(comm))), "ar_muon_update")

@@ -806,3 +806,211 @@ AR_EXPORT ar_result_t ar_linear_log_probs_backward(ar_comm_t comm, const void* h
         return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
     });
 }
+
+// ---------------------------------------------------------------------------
+// orthogonalised updates
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr uint64_t kMostSide = uint64_t(1) << 20;  // 128 rows of an operand lie within 2^31 bytes
+constexpr uint64_t kMostSmall = uint64_t(1) << 16, kMostElements = uint64_t(1) << 34;  // work-items are counted in 32 bits
+constexpr int kMostSteps = 32;
+constexpr double kLeastEps = 1e-30;
+
+bool orthogonalize_fits(int nmatrices, uint64_t rows, uint64_t cols)
+{
+    return nmatrices >= 0 && nmatrices <= AR_MAX_TENSORS && rows < kMostSide && cols < kMostSide &&
+           std::min(rows, cols) <= kMostSmall && rows * cols <= kMostElements;
+}
+
+// The coefficients of every step, checked.
+ar_result_t step_coefficients(int steps, const double* given, std::vector<double>* out)
+{
+    if (steps < 1 || steps > kMostSteps)
+        return fail(AR_ERR_INVALID_ARGUMENT, "steps %d is outside 1..%d", steps, kMostSteps);
+    out->resize(3 * static_cast<size_t>(steps));
+    for (int k = 0; k < steps; ++k) {
+        static const double quintic[3] = {3.4445, -4.7750, 2.0315};
+        const double *from = given ? given + 3 * k : quintic, a = from[0], b = from[1], c = from[2];
+        // the square's completion: its terms within the pieces' range, and not so
+        // large beside the sum that their difference loses it
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c) || std::fabs(a) > 16 || std::fabs(b) > 32 ||
+            std::fabs(c) > 32 || (c != 0 && (std::fabs(b) > 16 * std::fabs(c) || b * b > 64 * std::fabs(c))))
+            return fail(AR_ERR_INVALID_ARGUMENT, "coefficients %g %g %g of step %d are out of range", a, b, c, k);
+        std::copy(from, from + 3, out->begin() + 3 * k);
+    }
+    return AR_SUCCESS;
+}
+
+ar_result_t check_orthogonalize(const ar_comm* comm, int nmatrices, size_t rows, size_t cols, double eps, int steps,
+                                const double* given, std::vector<double>* coefficients)
+{
+    if (!comm) return fail(AR_ERR_INVALID_ARGUMENT, "comm is NULL");
+    if (!orthogonalize_fits(nmatrices, rows, cols))
+        return fail(AR_ERR_INVALID_ARGUMENT,
+                    "nmatrices %d, rows %zu, cols %zu: at most %d matrices of sides below 2^20, one of up to 2^16, and 2^34 "
+                    "elements",
+                    nmatrices, rows, cols, AR_MAX_TENSORS);
+    if (!(eps >= kLeastEps) || std::isinf(eps))
+        return fail(AR_ERR_INVALID_ARGUMENT, "eps %g is not a finite number of at least %g", eps, kLeastEps);
+    return step_coefficients(steps, given, coefficients);
+}
+
+// Matrix t of a list: pushes what it spans.
+ar_result_t check_listed(const char* what, int t, const void* p, size_t rows, size_t cols, size_t* ld, size_t elem,
+                         std::vector<Interval>* iv)
+{
+    const ar_result_t rc = check_matrix(what, p, rows, cols, ld, elem, iv);
+    if (rc == AR_SUCCESS) iv->back().rank = t;
+    return rc;
+}
+
+// No interval of a list with what is written may overlap another; what is only
+// read may.
+ar_result_t check_written(const std::vector<Interval>& reads, std::vector<Interval> writes)
+{
+    size_t a, b;
+    if (find_overlap(writes, &a, &b))
+        return fail(AR_ERR_INVALID_ARGUMENT, "%s %d overlaps %s %d", writes[a].what, writes[a].rank, writes[b].what,
+                    writes[b].rank);
+    // the writes are disjoint and sorted: a read overlaps one if it overlaps the
+    // last that starts before its end
+    for (const Interval& r : reads) {
+        auto it = std::lower_bound(writes.begin(), writes.end(), r.hi,
+                                   [](const Interval& w, uintptr_t hi) { return w.lo < hi; });
+        if (it == writes.begin()) continue;
+        --it;
+        if (it->hi > r.lo)
+            return fail(AR_ERR_INVALID_ARGUMENT, "%s %d overlaps %s %d", it->what, it->rank, r.what, r.rank);
+    }
+    return AR_SUCCESS;
+}
+
+}  // namespace
+
+AR_EXPORT size_t ar_orthogonalize_workspace_bytes(int nmatrices, size_t rows, size_t cols)
+{
+    if (!orthogonalize_fits(nmatrices, rows, cols)) return static_cast<size_t>(-1);
+    return ar::lm::orthogonalize_bytes(nmatrices, rows, cols);
+}
+
+AR_EXPORT ar_result_t ar_orthogonalize(ar_comm_t comm, int nmatrices, const void* const in[], void* const out[],
+                                       size_t rows, size_t cols, size_t ld_in, size_t ld_out, int steps,
+                                       const double coefficients[], double eps, ar_dtype_t dtype, hipStream_t stream)
+{
+    return guarded([&] {
+        std::vector<double> co;
+        ar_result_t rc = check_orthogonalize(comm, nmatrices, rows, cols, eps, steps, coefficients, &co);
+        if (rc == AR_SUCCESS) rc = check_float(dtype);
+        if (rc != AR_SUCCESS) return rc;
+        if (nmatrices > 0 && (!in || !out)) return fail(AR_ERR_INVALID_ARGUMENT, "NULL array of matrices");
+        if (nmatrices == 0 || rows == 0 || cols == 0) return AR_SUCCESS;
+        const size_t e = elem_size(dtype);
+        std::vector<Interval> reads, writes;
+        for (int t = 0; t < nmatrices; ++t) {
+            rc = check_listed("out", t, out[t], rows, cols, &ld_out, e, &writes);
+            // in place: the matrix is read before it is written
+            if (rc == AR_SUCCESS) rc = check_listed("in", t, in[t], rows, cols, &ld_in, e, &reads);
+            if (rc != AR_SUCCESS) return rc;
+            if (in[t] == out[t] && ld_in == ld_out) reads.pop_back();
+        }
+        const size_t need = ar::lm::orthogonalize_bytes(nmatrices, rows, cols);
+        if ((rc = check_workspace(comm, need)) != AR_SUCCESS) return rc;
+        const uintptr_t w = reinterpret_cast<uintptr_t>(comm->ws);
+        writes.push_back({w, w + need, "workspace", 0});
+        if ((rc = check_written(reads, std::move(writes))) != AR_SUCCESS) return rc;
+        DeviceGuard g(comm->device);
+        if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");
+        ar::lm::OrthogonalizeArgs a{};
+        a.count = nmatrices;
+        a.rows = rows;
+        a.cols = cols;
+        a.in = in;
+        a.out = out;
+        a.ld_in = ld_in;
+        a.ld_out = ld_out;
+        a.dtype = a.out_dtype = dtype;
+        a.steps = steps;
+        a.coefficients = co.data();
+        a.eps = eps;
+        a.nranks = 1;
+        const hipError_t err = ar::lm::launch_orthogonalize(a, static_cast<char*>(comm->ws), stream);
+        return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
+    });
+}
+
+AR_EXPORT ar_result_t ar_muon_update(ar_comm_t comm, int nmatrices, const void* const grads[],
+                                     const float* const momentum_in[], float* const momentum_out[],
+                                     const void* const weights_in[], void* const weights_out[], size_t rows, size_t cols,
+                                     size_t ld_grads, size_t ld_momentum, size_t ld_weights, double decay, int nesterov,
+                                     double lr, double weight_decay, double update_scale, int steps,
+                                     const double coefficients[], double eps, ar_dtype_t dtype, ar_dtype_t weight_dtype,
+                                     hipStream_t stream)
+{
+    return guarded([&] {
+        std::vector<double> co;
+        ar_result_t rc = check_orthogonalize(comm, nmatrices, rows, cols, eps, steps, coefficients, &co);
+        if (rc == AR_SUCCESS) rc = check_float(dtype);
+        if (rc == AR_SUCCESS) rc = check_float(weight_dtype);
+        if (rc != AR_SUCCESS) return rc;
+        if (weight_dtype != dtype && weight_dtype != AR_FLOAT32)
+            return fail(AR_ERR_UNSUPPORTED, "weight_dtype is dtype or fp32");
+        if (!(decay >= 0.0 && decay < 1.0)) return fail(AR_ERR_INVALID_ARGUMENT, "decay %g is outside 0..1", decay);
+        if (!std::isfinite(lr) || !std::isfinite(weight_decay) || !std::isfinite(update_scale))
+            return fail(AR_ERR_INVALID_ARGUMENT, "lr, weight_decay and update_scale are finite numbers");
+        if (nmatrices > 0 && (!grads || !momentum_in || !momentum_out || !weights_in || !weights_out))
+            return fail(AR_ERR_INVALID_ARGUMENT, "NULL array of matrices");
+        if (nmatrices == 0 || rows == 0 || cols == 0) return AR_SUCCESS;
+        const int n = comm->nranks;
+        const size_t e = elem_size(dtype), we = elem_size(weight_dtype);
+        std::vector<Interval> reads, writes;
+        for (int t = 0; t < nmatrices; ++t) {
+            rc = check_listed("grads", t, grads[t], rows, cols, &ld_grads, e, &reads);
+            if (rc == AR_SUCCESS) rc = check_listed("momentum_out", t, momentum_out[t], rows, cols, &ld_momentum, 4, &writes);
+            if (rc == AR_SUCCESS) rc = check_listed("momentum_in", t, momentum_in[t], rows, cols, &ld_momentum, 4, &reads);
+            if (rc != AR_SUCCESS) return rc;
+            if (momentum_in[t] == momentum_out[t]) reads.pop_back();  // element by element, in place
+            rc = check_listed("weights_in", t, weights_in[t], rows, cols, &ld_weights, we, &reads);
+            if (rc != AR_SUCCESS) return rc;
+            bool in_place = false;
+            for (int r = 0; r < n; ++r) {
+                void* out = weights_out[static_cast<size_t>(t) * n + r];
+                in_place = in_place || out == weights_in[t];
+                if ((rc = check_listed("weights_out", t, out, rows, cols, &ld_weights, we, &writes)) != AR_SUCCESS) return rc;
+            }
+            if (in_place) reads.pop_back();
+        }
+        const size_t need = ar::lm::orthogonalize_bytes(nmatrices, rows, cols);
+        if ((rc = check_workspace(comm, need)) != AR_SUCCESS) return rc;
+        const uintptr_t w = reinterpret_cast<uintptr_t>(comm->ws);
+        writes.push_back({w, w + need, "workspace", 0});
+        if ((rc = check_written(reads, std::move(writes))) != AR_SUCCESS) return rc;
+        DeviceGuard g(comm->device);
+        if (g.err != hipSuccess) return hip_fail(g.err, "hipSetDevice");
+        ar::lm::OrthogonalizeArgs a{};
+        a.count = nmatrices;
+        a.rows = rows;
+        a.cols = cols;
+        a.in = grads;
+        a.out = weights_out;
+        a.ld_in = ld_grads;
+        a.ld_out = ld_weights;
+        a.dtype = dtype;
+        a.out_dtype = weight_dtype;
+        a.steps = steps;
+        a.coefficients = co.data();
+        a.eps = eps;
+        a.momentum_in = momentum_in;
+        a.momentum_out = momentum_out;
+        a.weights_in = weights_in;
+        a.ld_momentum = ld_momentum;
+        a.nranks = n;
+        a.decay = decay;
+        a.lr = lr;
+        a.weight_decay = weight_decay;
+        a.update_scale = update_scale;
+        a.nesterov = nesterov ? 1 : 0;
+        const hipError_t err = ar::lm::launch_orthogonalize(a, static_cast<char*>(comm->ws), stream);
+        return err == hipSuccess ? AR_SUCCESS : hip_fail(err, "kernel launch");
+    });
+}

@@ -174,5 +174,30 @@ hipError_t launch_cross_entropy(const CrossEntropyArgs& a, const CrossEntropyPla
 hipError_t launch_cross_entropy_backward(const CrossEntropyArgs& a, const CrossEntropyPlan& p, ar_dtype_t dtype,
                                          char* ws, hipStream_t stream);
 
+// ---- orthogonalised updates -------------------------------------------------------
+// Matrices and pointers of one launch: what fits kernel arguments.
+constexpr int kMostGroup = 32, kMostGroupOut = 384;
+
+struct OrthogonalizeArgs {
+    uint64_t count, rows, cols;
+    const void* const* in;  // matrices, or gradients
+    void* const* out;       // matrices, or the weights of every rank: [matrix][rank]
+    uint64_t ld_in, ld_out;
+    ar_dtype_t dtype, out_dtype;
+    int steps;
+    const double* coefficients;  // three for each step
+    double eps;
+    // the update of weights; momentum_in and weights_in null: none
+    const float* const* momentum_in;
+    float* const* momentum_out;
+    const void* const* weights_in;
+    uint64_t ld_momentum;
+    int nranks;
+    double decay, lr, weight_decay, update_scale;
+    int nesterov;
+};
+uint64_t orthogonalize_bytes(uint64_t count, uint64_t rows, uint64_t cols);
+hipError_t launch_orthogonalize(const OrthogonalizeArgs& a, char* ws, hipStream_t stream);
+
 }  // namespace lm
 }  // namespace ar
