@@ -45,6 +45,10 @@ struct HalvesArgs {
     uint32_t tiles_m, tiles_n;
     uint32_t per_matrix;        // tiles; of a symmetric product those with tm >= tn
     int symmetric;
+    // the first `whole` tiles of all matrices are one workgroup's each, the others'
+    // sums are split along the depth and joined by a launch of its own
+    uint32_t whole, splits;
+    float* partial;  // [tile - whole][split][16-byte vector of a thread][thread]
 };
 
 template <int B>
@@ -142,12 +146,22 @@ private:
     }
 };
 
-// The tile of a workgroup: XCD after XCD a contiguous part of the order, as
-// tile_of_workgroup.
-__device__ __forceinline__ void halves_tile(const HalvesArgs& g, uint32_t* matrix, uint32_t* tm, uint32_t* tn)
+// The tile of a workgroup. Whole ones: XCD after XCD a contiguous part of the
+// order, as tile_of_workgroup; then the parts of split ones.
+__device__ __forceinline__ uint32_t halves_tile_id(const HalvesArgs& g, uint32_t* split)
 {
-    const uint32_t total = gridDim.x, xcd = blockIdx.x & 7, part = total >> 3, rest = total & 7;
-    uint32_t id = xcd * part + min(xcd, rest) + (blockIdx.x >> 3);
+    *split = 0;
+    if (blockIdx.x >= g.whole) {
+        const uint32_t id = blockIdx.x - g.whole;
+        *split = id % g.splits;
+        return g.whole + id / g.splits;
+    }
+    const uint32_t xcd = blockIdx.x & 7, part = g.whole >> 3, rest = g.whole & 7;
+    return xcd * part + min(xcd, rest) + (blockIdx.x >> 3);
+}
+__device__ __forceinline__ void halves_place(const HalvesArgs& g, uint32_t id, uint32_t* matrix, uint32_t* tm,
+                                             uint32_t* tn)
+{
     *matrix = id / g.per_matrix;
     id -= *matrix * g.per_matrix;
     if (g.symmetric) {
@@ -167,86 +181,111 @@ __device__ __forceinline__ void halves_tile(const HalvesArgs& g, uint32_t* matri
 }
 
 // B x B tiles, four waves of B/2 x B/2, two workgroups a CU: one waits or stores
-// while the other multiplies.
-template <int B, class Epilogue>
+// while the other multiplies. JOIN: the split tiles' sums.
+template <int B, bool JOIN, class Epilogue>
 __global__ __launch_bounds__(256, 2) void gemm_halves(const HalvesArgs g, const Epilogue epi)
 {
     using S = HalvesShape<B>;
     using T = MmaF16;
     constexpr int N = S::kTiles;
     __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStage];
-    uint32_t matrix, tm, tn;
-    halves_tile(g, &matrix, &tm, &tn);
+    uint32_t matrix, tm, tn, split = 0;
+    const uint32_t id = JOIN ? g.whole + blockIdx.x : halves_tile_id(g, &split);
+    halves_place(g, id, &matrix, &tm, &tn);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t wm = (wave >> 1) * S::kWave, wn = (wave & 1) * S::kWave;
     const uint32_t m_base = tm * B, n_base = tn * B;
 
-    auto rows_of = [&](const char* p, uint64_t batch, uint32_t ld, uint32_t r0, uint32_t rows) {
-        const uint32_t left = rows > r0 ? min(rows - r0, static_cast<uint32_t>(B)) : 0;
-        return __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(p + matrix * batch + static_cast<uint64_t>(r0) * ld), 0, static_cast<int>(left * ld), 0x00020000);
-    };
-    const __amdgpu_buffer_rsrc_t ra = rows_of(g.a, g.batch_a, g.lda, m_base, g.m);
-    const __amdgpu_buffer_rsrc_t rb = rows_of(g.b, g.batch_b, g.ldb, n_base, g.n);
-    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 16;
-    uint32_t off_a[S::kLoads], off_b[S::kLoads];
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-        off_a[i] = (i * 32 + (tid >> 3)) * g.lda + col;
-        off_b[i] = (i * 32 + (tid >> 3)) * g.ldb + col;
-    }
-    auto fetch = [&](uint32_t to, uint32_t step) {
-        const uint32_t at = step * 128;
-        const bool in = step < g.steps;
-        char* p = lds + to + wave * 1024;
-#pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) load_to_lds(ra, p + i * 4096, in ? off_a[i] : kPastEnd, at);
-#pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) load_to_lds(rb, p + S::kB + i * 4096, in ? off_b[i] : kPastEnd, at);
-    };
-
+    f32x4* partial = nullptr;
+    if (JOIN || id >= g.whole)
+        partial = reinterpret_cast<f32x4*>(g.partial) + (static_cast<uint64_t>(id - g.whole) * g.splits + split) * (N * N * 256) + tid;
     Tile<N, N> acc;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-    const int frow = lane & 15, fcol = lane >> 4;
-    const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
-    const uint32_t pa = base + (wm + frow) * 128 + swizzled, pb = base + S::kB + (wn + frow) * 128 + swizzled;
-    constexpr int kAhead = S::kStages - 1;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i * S::kStage, i);
-    uint32_t stage = 0, ahead = kAhead * S::kStage;
-    i32x4 fa[N][2], fb[N][2];
-    for (uint32_t k = 0; k < g.steps; ++k) {
-        // this stage has arrived in every wave, and nobody reads the one before any more
-        arrive<(kAhead - 1) * 2 * S::kLoads>();
-        fetch(ahead, k + kAhead);
-        const uint32_t xa = pa + stage, xb = pb + stage;
-        if constexpr (B == 128) {
-            read_fragments<0, 0>(fa, fb[0], fb[1], xa, xa ^ 64, xb, xb ^ 64);
-            read_fragments4(fb[2], fb[3], (xb ^ 0) + 4096, (xb ^ 64) + 4096);
-        } else {
-            read_few<2, 2>(fa, fb, xa, xa ^ 64, xb, xb ^ 64);
-        }
-        constexpr int kOfA[3] = {0, 1, 0}, kOfB[3] = {1, 0, 0};  // the smaller products first
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
+    if constexpr (JOIN) {
+        for (uint32_t k = 0; k < g.splits; ++k, partial += N * N * 256)
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    acc.v[i][j] = T::mma(__builtin_bit_cast(T::Frag, fa[i][kOfA[p]]),
-                                         __builtin_bit_cast(T::Frag, fb[j][kOfB[p]]), acc.v[i][j]);
-        ahead = stage;
-        stage = stage == kAhead * S::kStage ? 0 : stage + S::kStage;
+                for (int j = 0; j < N; ++j) acc.v[i][j] += partial[(i * N + j) * 256];
+    } else {
+        uint32_t from = 0, to = g.steps;
+        if (partial) {
+            const uint32_t part = (g.steps + g.splits - 1) / g.splits;
+            from = min(split * part, g.steps);
+            to = min(from + part, g.steps);
+        }
+        auto rows_of = [&](const char* p, uint64_t batch, uint32_t ld, uint32_t r0, uint32_t rows) {
+            const uint32_t left = rows > r0 ? min(rows - r0, static_cast<uint32_t>(B)) : 0;
+            return __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<char*>(p + matrix * batch + static_cast<uint64_t>(r0) * ld), 0, static_cast<int>(left * ld), 0x00020000);
+        };
+        const __amdgpu_buffer_rsrc_t ra = rows_of(g.a, g.batch_a, g.lda, m_base, g.m);
+        const __amdgpu_buffer_rsrc_t rb = rows_of(g.b, g.batch_b, g.ldb, n_base, g.n);
+        const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 16;
+        uint32_t off_a[S::kLoads], off_b[S::kLoads];
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) {
+            off_a[i] = (i * 32 + (tid >> 3)) * g.lda + col;
+            off_b[i] = (i * 32 + (tid >> 3)) * g.ldb + col;
+        }
+        auto fetch = [&](uint32_t where, uint32_t step) {
+            const uint32_t at = step * 128;
+            const bool in = step < to;
+            char* p = lds + where + wave * 1024;
+#pragma unroll
+            for (int i = 0; i < S::kLoads; ++i) load_to_lds(ra, p + i * 4096, in ? off_a[i] : kPastEnd, at);
+#pragma unroll
+            for (int i = 0; i < S::kLoads; ++i) load_to_lds(rb, p + S::kB + i * 4096, in ? off_b[i] : kPastEnd, at);
+        };
+
+        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+        const int frow = lane & 15, fcol = lane >> 4;
+        const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
+        const uint32_t pa = base + (wm + frow) * 128 + swizzled, pb = base + S::kB + (wn + frow) * 128 + swizzled;
+        constexpr int kAhead = S::kStages - 1;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i * S::kStage, from + i);
+        uint32_t stage = 0, ahead = kAhead * S::kStage;
+        i32x4 fa[N][2], fb[N][2];
+        for (uint32_t k = from; k < to; ++k) {
+            // this stage has arrived in every wave, and nobody reads the one before any more
+            arrive<(kAhead - 1) * 2 * S::kLoads>();
+            fetch(ahead, k + kAhead);
+            const uint32_t xa = pa + stage, xb = pb + stage;
+            if constexpr (B == 128) {
+                read_fragments<0, 0>(fa, fb[0], fb[1], xa, xa ^ 64, xb, xb ^ 64);
+                read_fragments4(fb[2], fb[3], (xb ^ 0) + 4096, (xb ^ 64) + 4096);
+            } else {
+                read_few<2, 2>(fa, fb, xa, xa ^ 64, xb, xb ^ 64);
+            }
+            constexpr int kOfA[3] = {0, 1, 0}, kOfB[3] = {1, 0, 0};  // the smaller products first
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        acc.v[i][j] = T::mma(__builtin_bit_cast(T::Frag, fa[i][kOfA[p]]),
+                                             __builtin_bit_cast(T::Frag, fb[j][kOfB[p]]), acc.v[i][j]);
+            ahead = stage;
+            stage = stage == kAhead * S::kStage ? 0 : stage + S::kStage;
+        }
+        // the loads past the end have arrived too: LDS is the epilogue's
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (partial) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int j = 0; j < N; ++j) partial[(i * N + j) * 256] = acc.v[i][j];
+            return;
+        }
     }
-    // the loads past the end have arrived too: LDS is the epilogue's
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     epi(acc, m_base + wm, n_base + wn, g, matrix, HalvesStaging<B>{lds, wm, wn, m_base, n_base}, tm, tn);
 }
 

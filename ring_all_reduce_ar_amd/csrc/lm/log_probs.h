@@ -114,10 +114,9 @@ private:
 
 __device__ __forceinline__ LogParts join_parts(LogParts a, LogParts b)
 {
-    const float m = fmaxf(a.top, b.top);
-    if (m == -INFINITY) return LogParts{m, a.sum + b.sum, 0.0f};
     // (the part of nothing has the top -infinity and sums of 0)
-    const float da = fmaxf(a.top - m, -1e4f), db = fmaxf(b.top - m, -1e4f);
+    const float m = fmaxf(a.top, b.top), base = m == -INFINITY ? 0.0f : m;
+    const float da = fmaxf(a.top - base, -1e4f), db = fmaxf(b.top - base, -1e4f);
     const float fa = __builtin_amdgcn_exp2f(da * kLog2e), fb = __builtin_amdgcn_exp2f(db * kLog2e);
     return LogParts{m, a.sum * fa + b.sum * fb, (a.dot + da * a.sum) * fa + (b.dot + db * b.sum) * fb};
 }
@@ -196,14 +195,32 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x)
     return __builtin_amdgcn_readlane(x, 63);
 }
 
+// The number of a wave's lanes whose key is above this lane's.
+__device__ __forceinline__ uint32_t rank_of(uint64_t key)
+{
+    uint32_t rank = 0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) {
+        const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(key >> 32, i))) << 32 |
+                               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(key), i));
+        rank += other > key ? 1 : 0;
+    }
+    return rank;
+}
+
 // A wave's list of the `top` (at most 64) largest keys that it has met, lane l
 // holding the l-th.
 constexpr int kTopBatch = 8;
 struct TopList {
     uint64_t mine = 0;   // this lane's place
     uint64_t last = 0;   // the list's last key: what is not above it has no place
-    // Keys of one batch (0: none), each met once.
-    __device__ __forceinline__ void add(uint64_t (&key)[kTopBatch], int top)
+
+    // Keys of one batch (0: none), each met once. `room`: 64 keys in LDS of the
+    // wave's own. No key below the top-th largest of the lanes' largest ones has a
+    // place. Mostly the others are at most 64, one for each lane: they find their
+    // places by counting the larger ones. If not, places are filled one by one;
+    // 20 of 640 keys took 8 us so, the counting takes 1.5.
+    __device__ __forceinline__ void add(uint64_t (&key)[kTopBatch], int top, uint64_t* room)
     {
         const uint32_t lane = threadIdx.x & 63;
         uint64_t best = 0;
@@ -211,21 +228,49 @@ struct TopList {
         for (int i = 0; i < kTopBatch; ++i) best = key[i] > best ? key[i] : best;
         if (!__any(best > last)) return;
         best = mine > best ? mine : best;
-        uint64_t held = mine, list = 0;
-        for (int k = 0; k < top; ++k) {
-            const uint32_t high = wave_max(static_cast<uint32_t>(best >> 32));
-            if (high == 0) break;  // no more keys
-            const bool first = static_cast<uint32_t>(best >> 32) == high;
-            const uint32_t low = wave_max(first ? static_cast<uint32_t>(best) : 0u);
-            const uint64_t won = static_cast<uint64_t>(high) << 32 | low;
-            if (lane == static_cast<uint32_t>(k)) list = won;
-            if (best == won) {  // one lane: it goes on with its next one
-                held = held == won ? 0 : held;
-                best = held;
+        const uint64_t at_place = __ballot(best != 0 && rank_of(best) == static_cast<uint32_t>(top - 1));
+        const uint64_t least = at_place ? __shfl(best, __builtin_ctzll(at_place), 64) : 1;
+        uint32_t count = 0;
+        auto give = [&](uint64_t k) {
+            const uint64_t in = __ballot(k >= least);
+            const uint32_t to = count + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(in >> 32),
+                                                                  __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(in), 0));
+            if (k >= least && to < 64) room[to] = k;
+            count += static_cast<uint32_t>(__builtin_popcountll(in));
+        };
+        give(mine);
 #pragma unroll
-                for (int i = 0; i < kTopBatch; ++i) {
-                    key[i] = key[i] == won ? 0 : key[i];
-                    best = key[i] > best ? key[i] : best;
+        for (int i = 0; i < kTopBatch; ++i) give(key[i]);
+        uint64_t list = 0;
+        if (count <= 64) {
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const uint64_t one = lane < count ? room[lane] : 0;
+            const uint32_t place = rank_of(one);
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (lane < count && place < static_cast<uint32_t>(top)) room[place] = one;
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            list = lane < min(count, static_cast<uint32_t>(top)) ? room[lane] : 0;
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            uint64_t held = mine;
+            for (int k = 0; k < top; ++k) {
+                const uint32_t high = wave_max(static_cast<uint32_t>(best >> 32));
+                if (high == 0) break;  // no more keys
+                const bool first = static_cast<uint32_t>(best >> 32) == high;
+                const uint32_t low = wave_max(first ? static_cast<uint32_t>(best) : 0u);
+                const uint64_t won = static_cast<uint64_t>(high) << 32 | low;
+                if (lane == static_cast<uint32_t>(k)) list = won;
+                if (best == won) {  // one lane: it goes on with its next one
+                    held = held == won ? 0 : held;
+                    best = held;
+#pragma unroll
+                    for (int i = 0; i < kTopBatch; ++i) {
+                        key[i] = key[i] == won ? 0 : key[i];
+                        best = key[i] > best ? key[i] : best;
+                    }
                 }
             }
         }
@@ -244,8 +289,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
                                                                     int32_t* top_ids)
 {
     constexpr int TOKENS = W == 1 ? 4 : 1;
-    __shared__ uint64_t lists[TOKENS][W][64];
-    __shared__ LogParts sums[TOKENS][W];
+    __shared__ uint64_t lists[W == 1 ? 1 : W][64], rooms[TOKENS * W][64];
+    __shared__ LogParts sums[W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int slot = W == 1 ? wave : 0, w = W == 1 ? 0 : wave;
     const uint64_t t = static_cast<uint64_t>(blockIdx.x) * TOKENS + slot, n = out.ntokens;
@@ -255,14 +300,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
     auto join_lists = [&](TopList& list) {
         if constexpr (W > 1) {
             __syncthreads();
-            lists[slot][w][lane] = list.mine;
+            lists[w][lane] = list.mine;
             __syncthreads();
             list = TopList{};
             uint64_t key[kTopBatch] = {};
             static_assert(W <= kTopBatch, "one batch takes all lists");
 #pragma unroll
-            for (int i = 0; i < W; ++i) key[i] = lists[slot][i][lane];
-            list.add(key, top);
+            for (int i = 0; i < W; ++i) key[i] = lists[i][lane];
+            list.add(key, top, rooms[wave]);
         }
     };
 
@@ -270,18 +315,19 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
     LogParts s{-INFINITY, 0.0f, 0.0f};
     if (on) {
         for (uint64_t g0 = static_cast<uint64_t>(w) * 64 * kTopBatch; g0 < groups; g0 += W * 64 * kTopBatch) {
+            // all loads first: within a branch each would be waited for by itself
+            LogParts p[kTopBatch];
             uint64_t key[kTopBatch];
+#pragma unroll
+            for (int i = 0; i < kTopBatch; ++i) p[i] = parts[min(g0 + i * 64 + lane, groups - 1) * n + t];
 #pragma unroll
             for (int i = 0; i < kTopBatch; ++i) {
                 const uint64_t g = g0 + i * 64 + lane;
-                key[i] = 0;
-                if (g < groups) {
-                    const LogParts p = parts[g * n + t];
-                    key[i] = order_key(p.top, static_cast<uint32_t>(g));
-                    s = join_parts(s, p);
-                }
+                const bool in = g < groups;
+                key[i] = in ? order_key(p[i].top, static_cast<uint32_t>(g)) : 0;
+                s = join_parts(s, in ? p[i] : LogParts{-INFINITY, 0.0f, 0.0f});
             }
-            best.add(key, top);
+            best.add(key, top, rooms[wave]);
         }
 #pragma unroll
         for (int m = 1; m <= 32; m *= 2)
@@ -289,11 +335,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
     }
     join_lists(best);
     if constexpr (W > 1) {
-        if (lane == 0) sums[slot][w] = s;
+        if (lane == 0) sums[w] = s;
         __syncthreads();
-        s = sums[slot][0];
+        s = sums[0];
 #pragma unroll
-        for (int i = 1; i < W; ++i) s = join_parts(s, sums[slot][i]);
+        for (int i = 1; i < W; ++i) s = join_parts(s, sums[i]);
     }
 
     TopList found;
@@ -302,19 +348,19 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
         const uint32_t per_batch = 64 * kTopBatch / group_rows;  // groups
         for (uint32_t k0 = w * per_batch; k0 < static_cast<uint32_t>(top); k0 += W * per_batch) {
             uint64_t key[kTopBatch];
+            float z[kTopBatch];
+            uint32_t ids[kTopBatch];
 #pragma unroll
             for (int i = 0; i < kTopBatch; ++i) {
                 const uint32_t e = i * 64 + lane, k = k0 + e / group_rows, row = e % group_rows;
                 const uint64_t group = __shfl(best.mine, k & 63, 64);
-                key[i] = 0;
-                if (k < static_cast<uint32_t>(top) && group != 0) {
-                    const uint64_t id = static_cast<uint64_t>(key_id(group)) * group_rows + row;
-                    if (id < out.vocab)
-                        key[i] = order_key(logits[logit_at(key_id(group), blocks, t, group_rows / 16, row)],
-                                           static_cast<uint32_t>(id));
-                }
+                const bool in = k < static_cast<uint32_t>(top) && group != 0;
+                ids[i] = in ? key_id(group) * group_rows + row : UINT32_MAX;
+                z[i] = logits[in ? logit_at(key_id(group), blocks, t, group_rows / 16, row) : 0];
             }
-            found.add(key, top);
+#pragma unroll
+            for (int i = 0; i < kTopBatch; ++i) key[i] = ids[i] < out.vocab ? order_key(z[i], ids[i]) : 0;
+            found.add(key, top, rooms[wave]);
         }
     }
     join_lists(found);

@@ -4,9 +4,18 @@
 //   X = U / max(|U|, eps),  then `steps` times  X <- (a I + b A + c A A) X,  A = X X^T
 //
 // on the smaller side (m rows of n, m <= n), which leaves each singular value s
-// as p(p(..p(s))), p(s) = a s + b s^3 + c s^5. The bracket is built without a sum
+// as p(p(..p(s))), p(s) = a s + b s^3 + c s^5. The bracket Q is built without a sum
 // of matrices: with D = A + (b / 2c) I it is c D D + (a - b^2 / 4c) I, so both
 // products change a diagonal only.
+//
+// Where the matrix is clearly wider than high, X is left alone for up to three
+// steps: the next A is Q A Q, since all of these are polynomials of A, and the
+// steps' brackets are multiplied into P, by which X is multiplied at the end.
+// These products are of the smaller side alone and symmetric: a segment of k
+// steps costs m^2 (n + (4k - 3) m + 2n) products (of half of a symmetric result)
+// where steps by themselves take k m^2 (3n + m). Errors of A for small singular
+// values grow with a^2 a step there, in X with a: five steps on end lose a digit
+// against fp32, segments of three and two are as exact as steps by themselves.
 //
 // Small singular values grow by a factor of a in each step (485 in five of them),
 // and what a rounding adds to X grows alike: in bf16, results are off by 4-30%, in
@@ -19,6 +28,7 @@
 // side's products are symmetric: their tiles below the diagonal are written
 // twice.
 #include <algorithm>
+#include <cmath>
 
 #include "gemm_halves.h"
 #include "rows.h"
@@ -194,12 +204,12 @@ __global__ __launch_bounds__(kBlock) void lay_out_matrices(const GroupIn p, cons
 // ---------------------------------------------------------------------------
 // epilogues
 // ---------------------------------------------------------------------------
-// out = factor C + shift I for the symmetric product C.
+// factor C + shift I of the symmetric product C, up to two of them.
 struct SymmetricEpilogue {
-    char* out;
+    char* out[2];  // the first may be null
     uint64_t batch;
     uint32_t ld, pad;  // bytes, elements
-    float factor, shift;
+    float factor[2], shift[2];
 
     template <int N, class S>
     __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
@@ -207,17 +217,22 @@ struct SymmetricEpilogue {
     {
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int k = 0; k < 2; ++k) {
+            if (!out[k]) continue;
+            Tile<N, N> x;
 #pragma unroll
-            for (int j = 0; j < N; ++j)
+            for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t row = m0 + i * 16 + quad * 4 + r, col = n0 + j * 16 + (lane & 15);
-                    acc.v[i][j][r] = factor * acc.v[i][j][r] + (row == col && row < g.m ? shift : 0.0f);
-                }
-        char* to = out + matrix * batch;
-        stage.store_by_column(acc, to, ld, g.n, pad);
-        if (tm != tn) stage.store_by_row(acc, to, ld, g.m, pad);
+                for (int j = 0; j < N; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t row = m0 + i * 16 + quad * 4 + r, col = n0 + j * 16 + (lane & 15);
+                        x.v[i][j][r] = factor[k] * acc.v[i][j][r] + (row == col && row < g.m ? shift[k] : 0.0f);
+                    }
+            char* to = out[k] + matrix * batch;
+            stage.store_by_column(x, to, ld, g.n, pad);
+            if (tm != tn) stage.store_by_row(x, to, ld, g.m, pad);
+        }
     }
 };
 
@@ -227,6 +242,7 @@ struct NextEpilogue {
     char* columns;  // [n][m]
     uint64_t batch_r, batch_c;
     uint32_t pad_n, pad_m;
+    float factor;
 
     template <int N, class S>
     __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t, uint32_t, const HalvesArgs& g, uint32_t matrix,
@@ -235,7 +251,7 @@ struct NextEpilogue {
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc.v[i][j] *= 1.0f / kHalvesScale;
+            for (int j = 0; j < N; ++j) acc.v[i][j] *= factor;
         stage.store_by_column(acc, columns + matrix * batch_c, halves_bytes(pad_m), g.n, pad_m);
         stage.store_by_row(acc, rows + matrix * batch_r, halves_bytes(pad_n), g.m, pad_n);
     }
@@ -247,12 +263,13 @@ struct ResultEpilogue {
     void* out[kMostGroup];
     uint64_t ld;
     int vec;
+    float unit;
 
     template <int N, class S>
     __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
                                                uint32_t matrix, const S&, uint32_t, uint32_t) const
     {
-        each_four(acc, m0, n0, g, [&](uint32_t row, uint32_t col, float (&x)[4], uint32_t left) {
+        each_four(acc, m0, n0, g, unit, [&](uint32_t row, uint32_t col, float (&x)[4], uint32_t left) {
             put(out[matrix], row * ld + col, x, left, vec);
         });
     }
@@ -260,7 +277,7 @@ struct ResultEpilogue {
     // fn(row, column, four results, how many of them there are)
     template <int N, class Fn>
     static __device__ __forceinline__ void each_four(const Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
-                                                     Fn fn)
+                                                     float unit, Fn fn)
     {
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
 #pragma unroll
@@ -273,7 +290,7 @@ struct ResultEpilogue {
                 if (col >= g.m) continue;
                 float x[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = acc.v[i][j][r] * kHalvesUnit;
+                for (int r = 0; r < 4; ++r) x[r] = acc.v[i][j][r] * unit;
                 fn(row, col, x, g.m - col);
             }
         }
@@ -298,7 +315,7 @@ struct UpdateEpilogue {
     void* out[kMostGroupOut];  // [matrix][rank]
     uint64_t ld;
     int nranks, vec;
-    float keep, gain;
+    float keep, gain, unit;
 
     template <int N, class S>
     __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
@@ -307,7 +324,7 @@ struct UpdateEpilogue {
         using R = ResultEpilogue<F>;
         using Raw = RawOf<F>;
         const void* from = in[matrix];
-        R::each_four(acc, m0, n0, g, [&](uint32_t row, uint32_t col, float (&x)[4], uint32_t left) {
+        R::each_four(acc, m0, n0, g, unit, [&](uint32_t row, uint32_t col, float (&x)[4], uint32_t left) {
             const uint64_t at = row * ld + col;
             Raw w[4] = {};
             if (vec && left >= 4) {
@@ -332,13 +349,38 @@ struct UpdateEpilogue {
 // one call
 // ---------------------------------------------------------------------------
 constexpr uint64_t kCUs = 256;
+constexpr int kSegment = 3;  // steps
+
+// Workgroups that run at a time, and what the parts of split tiles take.
+constexpr uint32_t kSlots = 2 * kCUs;
+constexpr uint32_t kLeastPart = 8;  // steps
+constexpr uint64_t kPartialBytes = uint64_t(kSlots) * 128 * 128 * 4;
+
+// The parts of each tile behind the last full round of `tiles`, whose number goes
+// to *whole; 1: none is split.
+uint32_t splits_of(uint32_t tiles, uint32_t steps, int tile, uint32_t* whole)
+{
+    *whole = tiles;
+    const uint32_t rest = tiles % kSlots;
+    if (rest == 0) return 1;
+    const uint32_t splits = std::min({kSlots / rest, steps / kLeastPart, 16u});
+    if (splits < 2) return 1;
+    *whole = tiles - rest;
+    return splits;
+}
 
 struct Layout {
     uint64_t m, n, pad_m, pad_n;
     uint64_t rows, columns, square;  // bytes of X by rows, by columns, of D
     int parts;                       // of a matrix's sum of squares
+    int squares;                     // matrices of the smaller side
     uint64_t per_matrix;             // bytes of all
 };
+
+// Whether steps go in segments: nine products of 9 (n - m) m^2 less in five steps,
+// and three launches more.
+bool in_segments(uint64_t m, uint64_t n) { return 4 * n >= 5 * m; }
+
 Layout layout_of(uint64_t rows, uint64_t cols)
 {
     Layout l;
@@ -350,9 +392,13 @@ Layout layout_of(uint64_t rows, uint64_t cols)
     l.columns = round_up(l.n * halves_bytes(l.pad_m), 256);
     l.square = round_up(l.m * halves_bytes(l.pad_m), 256);
     l.parts = static_cast<int>(std::min<uint64_t>((rows * cols + kBlock * 32 - 1) / (kBlock * 32), 256));
-    l.per_matrix = l.rows + 2 * l.columns + 2 * l.square + round_up(l.parts * sizeof(double), 256);
+    l.squares = in_segments(l.m, l.n) ? 7 : 2;
+    l.per_matrix = l.rows + 2 * l.columns + l.squares * l.square + round_up(l.parts * sizeof(double), 256);
     return l;
 }
+
+// Whether a product is ever deep enough for parts.
+bool may_split(const Layout& l) { return l.pad_n >= 2 * kLeastPart * kHalvesDepth; }
 
 // Matrices of a group: as many as their pointers fit kernel arguments, and about
 // kGroupBytes of workspace; a matrix beyond that fills the chip alone.
@@ -363,17 +409,27 @@ uint64_t group_of(uint64_t count, const Layout& l, int nranks)
     return std::max<uint64_t>(1, std::min({count, most, kGroupBytes / l.per_matrix}));
 }
 
+template <int B, class Epilogue>
+hipError_t launch_tiles(HalvesArgs g, uint64_t matrices, float* partial, const Epilogue& epi, hipStream_t s)
+{
+    const uint32_t tiles = static_cast<uint32_t>(g.per_matrix * matrices);
+    g.splits = splits_of(tiles, g.steps, B, &g.whole);
+    g.partial = partial;
+    hipLaunchKernelGGL((gemm_halves<B, false, Epilogue>), dim3(g.whole + (tiles - g.whole) * g.splits), dim3(256), 0, s, g, epi);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || g.whole == tiles) return e;
+    hipLaunchKernelGGL((gemm_halves<B, true, Epilogue>), dim3(tiles - g.whole), dim3(256), 0, s, g, epi);
+    return hipGetLastError();
+}
+
 template <class Epilogue>
-hipError_t launch_halves(HalvesArgs g, uint64_t matrices, int tile, const Epilogue& epi, hipStream_t s)
+hipError_t launch_halves(HalvesArgs g, uint64_t matrices, int tile, float* partial, const Epilogue& epi, hipStream_t s)
 {
     const uint32_t b = static_cast<uint32_t>(tile);
     g.tiles_m = (g.m + b - 1) / b;
     g.tiles_n = (g.n + b - 1) / b;
     g.per_matrix = g.symmetric ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
-    const dim3 grid(static_cast<uint32_t>(g.per_matrix * matrices));
-    if (tile == 128) hipLaunchKernelGGL((gemm_halves<128, Epilogue>), grid, dim3(256), 0, s, g, epi);
-    else hipLaunchKernelGGL((gemm_halves<64, Epilogue>), grid, dim3(256), 0, s, g, epi);
-    return hipGetLastError();
+    return tile == 128 ? launch_tiles<128>(g, matrices, partial, epi, s) : launch_tiles<64>(g, matrices, partial, epi, s);
 }
 
 // Tiles of 64 where those of 128 leave CUs idle.
@@ -447,7 +503,7 @@ struct Group {
     }
 
     template <class F>
-    hipError_t finish(const HalvesArgs& g, int tile) const
+    hipError_t finish(const HalvesArgs& g, int tile, float unit) const
     {
         constexpr uint64_t e = sizeof(RawOf<F>);
         uintptr_t mis = a.ld_out * e;
@@ -458,8 +514,9 @@ struct Group {
                 mis |= reinterpret_cast<uintptr_t>(epi.out[i]);
             }
             epi.ld = a.ld_out;
+            epi.unit = unit;
             epi.vec = mis % (4 * e) == 0;
-            return launch_halves(g, count, tile, epi, s);
+            return launch_halves(g, count, tile, sums(), epi, s);
         }
         UpdateEpilogue<F> epi{};
         for (uint64_t i = 0; i < count; ++i) {
@@ -476,7 +533,8 @@ struct Group {
         epi.vec = mis % (4 * e) == 0;
         epi.keep = static_cast<float>(1.0 - a.lr * a.weight_decay);
         epi.gain = static_cast<float>(a.lr * a.update_scale);
-        return launch_halves(g, count, tile, epi, s);
+        epi.unit = unit;
+        return launch_halves(g, count, tile, sums(), epi, s);
     }
 
     hipError_t run() const
@@ -489,9 +547,11 @@ struct Group {
         };
         char* x = take(l.rows);
         char* xt[2] = {take(l.columns), take(l.columns)};
-        char *d = take(l.square), *q = take(l.square);
+        char* square[7] = {};
+        for (int i = 0; i < l.squares; ++i) square[i] = take(l.square);
         double* partial = reinterpret_cast<double*>(take(round_up(l.parts * sizeof(double), 256)));
         const bool tall = a.rows > a.cols;
+        const int wide_tile = tile_of(l.m, l.n, count, false);
         char *straight = tall ? xt[0] : x, *turned = tall ? x : xt[0];
         const uint64_t batch_s = tall ? l.columns : l.rows, batch_t = tall ? l.rows : l.columns;
         hipError_t e;
@@ -502,41 +562,112 @@ struct Group {
         default: return hipErrorInvalidValue;
         }
         if (e != hipSuccess) return e;
-        const int square_tile = tile_of(l.m, l.m, count, true), wide_tile = tile_of(l.m, l.n, count, false);
-        const uint32_t ld_square = static_cast<uint32_t>(halves_bytes(l.pad_m)), pad_m = static_cast<uint32_t>(l.pad_m);
-        for (int step = 0; step < a.steps; ++step) {
-            const double ca = a.coefficients[3 * step], cb = a.coefficients[3 * step + 1], cc = a.coefficients[3 * step + 2];
-            // operands are held times 2^11, products times 2^22
-            auto symmetric = [&](char* out, double factor, double shift) {
-                return SymmetricEpilogue{out, l.square, ld_square, pad_m, static_cast<float>(factor / kHalvesScale),
-                                         static_cast<float>(shift * kHalvesScale)};
-            };
-            const HalvesArgs xx = product(x, l.rows, l.m, x, l.rows, l.m, l.pad_n, true);
-            if (cc != 0.0) {
-                if ((e = launch_halves(xx, count, square_tile, symmetric(d, 1.0, cb / (2.0 * cc)), s)) != hipSuccess) return e;
-                e = launch_halves(product(d, l.square, l.m, d, l.square, l.m, l.pad_m, true), count, square_tile,
-                                  symmetric(q, cc, ca - cb * cb / (4.0 * cc)), s);
-            } else {
-                e = launch_halves(xx, count, square_tile, symmetric(q, cb, ca), s);
+        const bool segments = in_segments(l.m, l.n);
+        double top = 1.0;  // of the singular values
+        int turn = 0;      // which of xt holds X
+        for (int k = 0; k < a.steps;) {
+            // segments of up to three steps, the longer ones first
+            const int left = a.steps - k, count_left = (left + kSegment - 1) / kSegment;
+            const int size = segments ? (left + count_left - 1) / count_left : 1;
+            const char* p;
+            double p_scale;
+            if ((e = segment(x, square, k, size, &top, &p, &p_scale)) != hipSuccess) return e;
+            k += size;
+            const float unit = static_cast<float>(1.0 / p_scale);  // X keeps its 2^11
+            if (k == a.steps) {
+                // four neighbours of a row of the result lie in a lane
+                const HalvesArgs g = tall ? product(p, l.square, l.m, xt[turn], l.columns, l.n, l.pad_m, false)
+                                          : product(xt[turn], l.columns, l.n, p, l.square, l.m, l.pad_m, false);
+                const float out_unit = unit / kHalvesScale;
+                switch (a.out_dtype) {
+                case AR_FLOAT32: return finish<F32>(g, wide_tile, out_unit);
+                case AR_FLOAT16: return finish<F16>(g, wide_tile, out_unit);
+                case AR_BFLOAT16: return finish<BF16>(g, wide_tile, out_unit);
+                default: return hipErrorInvalidValue;
+                }
             }
+            const NextEpilogue next{x, xt[turn ^ 1], l.rows, l.columns, static_cast<uint32_t>(l.pad_n),
+                                    static_cast<uint32_t>(l.pad_m), unit};
+            e = launch_halves(product(p, l.square, l.m, xt[turn], l.columns, l.n, l.pad_m, false), count, wide_tile, sums(), next, s);
             if (e != hipSuccess) return e;
-            if (step + 1 < a.steps) {
-                const NextEpilogue next{x, xt[(step + 1) & 1], l.rows, l.columns, static_cast<uint32_t>(l.pad_n), pad_m};
-                e = launch_halves(product(q, l.square, l.m, xt[step & 1], l.columns, l.n, l.pad_m, false), count, wide_tile,
-                                  next, s);
+            turn ^= 1;
+        }
+        return hipSuccess;  // not reached: there is at least one step
+    }
+
+    // Steps k .. k + size - 1 of X's rows `x`: *p is the product of their brackets,
+    // held times *p_scale. *top bounds the singular values before and after.
+    hipError_t segment(const char* x, char* const square[7], int k, int size, double* top, const char** p,
+                       double* p_scale) const
+    {
+        char *d = square[0], *q[2] = {square[1], square[4]}, *gram = square[2], *t = square[3], *prod[2] = {square[5], square[6]};
+        const int tile = tile_of(l.m, l.m, count, true);
+        hipError_t e;
+        double largest = 1.0;  // of P's eigenvalues
+        for (int i = 0; i < size; ++i) {
+            const double ca = a.coefficients[3 * (k + i)], cb = a.coefficients[3 * (k + i) + 1],
+                         cc = a.coefficients[3 * (k + i) + 2];
+            char* bracket = q[i & 1];
+            // A, if a later step needs it, and D (or the bracket itself of a cubic)
+            SymmetricEpilogue epi = symmetric(cc != 0.0 ? d : bracket, cc != 0.0 ? 1.0 : cb, cc != 0.0 ? cb / (2.0 * cc) : ca);
+            if (i + 1 < size) {
+                epi.out[0] = gram;
+                epi.factor[0] = 1.0f / kHalvesScale;
+            }
+            const HalvesArgs g = i == 0 ? product(x, l.rows, l.m, x, l.rows, l.m, l.pad_n, true)
+                                        : square_product(t, q[(i - 1) & 1]);
+            if ((e = launch_halves(g, count, tile, sums(), epi, s)) != hipSuccess) return e;
+            if (cc != 0.0) {
+                e = launch_halves(square_product(d, d), count, tile, sums(), symmetric(bracket, cc, ca - cb * cb / (4.0 * cc)), s);
                 if (e != hipSuccess) return e;
             }
+            double most = 0.0, next = 0.0;
+            for (int j = 0; j <= 1000; ++j) {
+                const double v = *top * j / 1000.0, u = std::fabs(ca + cb * v * v + cc * v * v * v * v);
+                most = std::max(most, u);
+                next = std::max(next, u * v);
+            }
+            *top = next * 1.001;
+            largest *= std::max(most * 1.001, 1e-3);
+            auto scale_of = [](double bound) { return kHalvesScale * std::exp2(-std::max(0.0, std::ceil(std::log2(bound / 8.0)))); };
+            if (i == 0) {
+                *p = bracket;
+                *p_scale = kHalvesScale;
+            } else {
+                const double scale = scale_of(largest);
+                char* to = prod[i & 1];
+                SymmetricEpilogue join = symmetric(to, 1.0, 0.0);
+                join.factor[1] = static_cast<float>(scale / (kHalvesScale * *p_scale));
+                if ((e = launch_halves(square_product(bracket, *p), count, tile, sums(), join, s)) != hipSuccess) return e;
+                *p = to;
+                *p_scale = scale;
+            }
+            if (i + 1 < size) {  // A Q, then (A Q) Q at the head of the loop
+                if ((e = launch_halves(square_product(gram, bracket), count, tile, sums(), symmetric(t, 1.0, 0.0), s)) != hipSuccess)
+                    return e;
+            }
         }
-        // four neighbours of a row of the result lie in a lane
-        char* last = xt[(a.steps - 1) & 1];
-        const HalvesArgs g = tall ? product(q, l.square, l.m, last, l.columns, l.n, l.pad_m, false)
-                                  : product(last, l.columns, l.n, q, l.square, l.m, l.pad_m, false);
-        switch (a.out_dtype) {
-        case AR_FLOAT32: return finish<F32>(g, wide_tile);
-        case AR_FLOAT16: return finish<F16>(g, wide_tile);
-        case AR_BFLOAT16: return finish<BF16>(g, wide_tile);
-        default: return hipErrorInvalidValue;
-        }
+        return hipSuccess;
+    }
+
+    // (behind the group's matrices)
+    float* sums() const { return reinterpret_cast<float*>(ws + count * l.per_matrix); }
+
+    HalvesArgs square_product(const char* u, const char* v) const
+    {
+        return product(u, l.square, l.m, v, l.square, l.m, l.pad_m, true);
+    }
+    // Operands are held times 2^11, products times 2^22.
+    SymmetricEpilogue symmetric(char* out, double factor, double shift) const
+    {
+        SymmetricEpilogue epi{};
+        epi.out[1] = out;
+        epi.batch = l.square;
+        epi.ld = static_cast<uint32_t>(halves_bytes(l.pad_m));
+        epi.pad = static_cast<uint32_t>(l.pad_m);
+        epi.factor[1] = static_cast<float>(factor / kHalvesScale);
+        epi.shift[1] = static_cast<float>(shift * kHalvesScale);
+        return epi;
     }
 };
 
@@ -546,7 +677,7 @@ uint64_t orthogonalize_bytes(uint64_t count, uint64_t rows, uint64_t cols)
 {
     if (count == 0 || rows == 0 || cols == 0) return 0;
     const Layout l = layout_of(rows, cols);
-    return group_of(count, l, 1) * l.per_matrix;
+    return group_of(count, l, 1) * l.per_matrix + (may_split(l) ? kPartialBytes : 0);
 }
 
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a, char* ws, hipStream_t stream)

@@ -12,10 +12,10 @@ SIZE = ar.ar_orthogonalize_workspace_bytes
 def test_workspace_sizes():
     assert SIZE(0, 10, 10) == 0 and SIZE(3, 0, 10) == 0
     one, four, many = SIZE(1, 300, 500), SIZE(4, 300, 500), SIZE(1000, 300, 500)
-    assert 300 * 500 * 12 < one < 300 * 500 * 24 and four == 4 * one and many <= 32 * one
+    assert 300 * 500 * 12 < one and one < four <= 4 * one < many <= 32 * one
     assert SIZE(1, 300, 500) == SIZE(1, 500, 300)
     # a list of large matrices goes through the workspace in groups
-    assert SIZE(32, 4096, 8192) <= max(4 << 30, SIZE(1, 4096, 8192))
+    assert SIZE(32, 4096, 8192) <= (4 << 30) + SIZE(1, 4096, 8192)
     for bad in ((-1, 4, 4), (1, 1 << 20, 4), (1, 4, 1 << 20), (1, 1 << 17, 1 << 17), (1, 1 << 16, 1 << 19),
                 (ar.MAX_TENSORS + 1, 4, 4)):
         with pytest.raises(ValueError):
