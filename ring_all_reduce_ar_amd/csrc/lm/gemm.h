@@ -313,6 +313,13 @@ __device__ __forceinline__ void meet()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// One operand's part: rows row0 .. of `rows`, from depth 0 on.
+struct LargeOperand {
+    const char* p;
+    uint64_t ld;  // bytes
+    uint32_t row0, rows;
+};
+
 // 256 x 256 x 64 tiles, 8 waves of 128 x 64. The two waves of a SIMD (w and
 // w + 4) take turns: while one issues a half step's 32 matrix instructions,
 // the other reads its fragments for the next half step and issues direct
@@ -322,30 +329,25 @@ __device__ __forceinline__ void meet()
 // passed, and only the oldest loads are waited for. 8192 x 4096 x 13312 bf16 in
 // 600 us, 1.49 PFLOP/s, as much as a large library product reaches (1.3-1.48);
 // with one barrier a step and all loads waited for it took 929.
-template <class T, class Epilogue>
-__global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epilogue epi)
+//
+// HALVES: the 64 of a step are 32 hi and 32 lo of pairs (gemm_halves.h), of whose
+// products lo lo is left out and the smaller ones come first.
+template <class T, bool HALVES>
+__device__ __forceinline__ void multiply_large(char* lds, const LargeOperand& oa, const LargeOperand& ob, uint32_t depth,
+                                               Tile<8, 4>& acc)
 {
     constexpr uint32_t kStage = 65536, kA1 = 16384, kB = 32768, kB1 = 49152;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
-    uint32_t tm, tn, split;
-    tile_of_workgroup(g, &tm, &tn, &split);
-
+    const uint32_t steps = (depth + kTileK - 1) / kTileK;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const uint32_t m_base = tm * 256, n_base = tn * 256;
-    const uint32_t k0 = split * g.k;
-    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
-    const uint32_t steps = (depth + kTileK - 1) / kTileK;
 
     const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 8;
-    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(g.lda) + col * 2;
-    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(g.ldb) + col * 2;
-    const char *a = g.a + static_cast<uint64_t>(k0) * 2, *b = g.b + static_cast<uint64_t>(k0) * 2;
-    const __amdgpu_buffer_rsrc_t ra0 = row_buffer(a, g.lda, m_base, g.m), ra1 = row_buffer(a, g.lda, m_base + 64, g.m);
-    const __amdgpu_buffer_rsrc_t ra2 = row_buffer(a, g.lda, m_base + 128, g.m), ra3 = row_buffer(a, g.lda, m_base + 192, g.m);
-    const __amdgpu_buffer_rsrc_t rb0 = row_buffer(b, g.ldb, n_base, g.n), rb1 = row_buffer(b, g.ldb, n_base + 64, g.n);
-    const __amdgpu_buffer_rsrc_t rb2 = row_buffer(b, g.ldb, n_base + 128, g.n), rb3 = row_buffer(b, g.ldb, n_base + 192, g.n);
+    const uint32_t off_a = (tid >> 3) * static_cast<uint32_t>(oa.ld) + col * 2;
+    const uint32_t off_b = (tid >> 3) * static_cast<uint32_t>(ob.ld) + col * 2;
+    auto part = [](const LargeOperand& o, uint32_t at) { return row_buffer(o.p, o.ld, o.row0 + at, o.rows); };
+    const __amdgpu_buffer_rsrc_t ra0 = part(oa, 0), ra1 = part(oa, 64), ra2 = part(oa, 128), ra3 = part(oa, 192);
+    const __amdgpu_buffer_rsrc_t rb0 = part(ob, 0), rb1 = part(ob, 64), rb2 = part(ob, 128), rb3 = part(ob, 192);
     auto fetch = [&](__amdgpu_buffer_rsrc_t x, __amdgpu_buffer_rsrc_t y, uint32_t to, uint32_t off, uint32_t step) {
         const uint32_t at = step * kTileK;
         const uint32_t v = at + col < depth ? off : kPastEnd;
@@ -354,7 +356,6 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
         load_to_lds(y, p + 8192, v, at * 2);
     };
 
-    Tile<8, 4> acc;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -362,14 +363,15 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
     i32x4 fa0[4][2], fa1[4][2], fb[4][2];
     auto multiply = [&](i32x4 (&f)[4][2], int i0) {
         __builtin_amdgcn_s_setprio(1);
+        constexpr int kOfA[3] = {0, 1, 0}, kOfB[3] = {HALVES ? 1 : 0, HALVES ? 0 : 1, 0};
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int p = 0; p < (HALVES ? 3 : 2); ++p)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    acc.v[i0 + i][j] = T::mma(__builtin_bit_cast(typename T::Frag, f[i][kk]),
-                                              __builtin_bit_cast(typename T::Frag, fb[j][kk]), acc.v[i0 + i][j]);
+                    acc.v[i0 + i][j] = T::mma(__builtin_bit_cast(typename T::Frag, f[i][kOfA[p]]),
+                                              __builtin_bit_cast(typename T::Frag, fb[j][kOfB[p]]), acc.v[i0 + i][j]);
         __builtin_amdgcn_s_setprio(0);
     };
 
@@ -411,6 +413,22 @@ __global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epi
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
     }
+}
+
+template <class T, class Epilogue>
+__global__ __launch_bounds__(512, 2) void gemm_large(const GemmArgs g, const Epilogue epi)
+{
+    __shared__ __attribute__((aligned(1024))) char lds[2 * 65536];
+    uint32_t tm, tn, split;
+    tile_of_workgroup(g, &tm, &tn, &split);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const uint32_t m_base = tm * 256, n_base = tn * 256;
+    const uint32_t k0 = split * g.k;
+    const uint32_t depth = k0 < g.k_all ? min(g.k, g.k_all - k0) : 0;
+    Tile<8, 4> acc;
+    multiply_large<T, false>(lds, LargeOperand{g.a + static_cast<uint64_t>(k0) * 2, g.lda, m_base, g.m},
+                             LargeOperand{g.b + static_cast<uint64_t>(k0) * 2, g.ldb, n_base, g.n}, depth, acc);
     epi(acc, m_base + wm * 128, n_base + wn * 64, g, tm * 2 + wm, split, Staging{lds, wm * 128u, wn * 64u, m_base, n_base});
 }
 

@@ -51,21 +51,29 @@ struct HalvesArgs {
     float* partial;  // [tile - whole][split][16-byte vector of a thread][thread]
 };
 
+// B x B tiles. 256: multiply_large's, one workgroup of eight waves of 128 x 64 a
+// CU. 128, 64: four waves of B/2 x B/2, two workgroups a CU: one waits or stores
+// while the other multiplies.
 template <int B>
 struct HalvesShape {
-    static_assert(B == 128 || B == 64, "tiles");
-    static constexpr int kStages = B == 128 ? 2 : 4;
+    static_assert(B == 256 || B == 128 || B == 64, "tiles");
+    static constexpr int kThreads = B == 256 ? 512 : 256;
+    static constexpr int kStages = B == 64 ? 4 : 2;
     static constexpr uint32_t kB = B * 128, kStage = 2 * kB;
     static constexpr int kLoads = B / 32;  // of one operand, a stage and a thread
-    static constexpr int kWave = B / 2, kTiles = kWave / 16;
+    static constexpr uint32_t kWaveM = B / 2, kWaveN = B == 256 ? 64 : B / 2;
+    static constexpr int MT = kWaveM / 16, NT = kWaveN / 16;
+    static constexpr uint32_t kWavesN = B / kWaveN;
 };
 
-// A tile leaves through LDS in rows of pieces.
+// A tile leaves through LDS in rows of pieces: at once, or, of 256, a half of
+// each wave's columns (or rows) after the other.
 template <int B>
 struct HalvesStaging {
-    static constexpr int N = HalvesShape<B>::kTiles;
+    using S = HalvesShape<B>;
+    static constexpr int MT = S::MT, NT = S::NT, kParts = B == 256 ? 2 : 1;
     char* lds;
-    uint32_t wm, wn;          // the wave's first row and column within the tile
+    uint32_t wm, wn;          // the wave's row and column among the waves
     uint32_t m_base, n_base;  // the tile's
 
     // Rows of B * 4 bytes, the 16-byte columns permuted within groups of eight.
@@ -75,62 +83,74 @@ struct HalvesStaging {
     }
 
     // out[n][m], rows `ld` bytes apart, for the first `rows` n and `depth` m (a multiple of 32).
-    __device__ __forceinline__ void store_by_column(const Tile<N, N>& x, char* out, uint64_t ld, uint32_t rows,
+    __device__ __forceinline__ void store_by_column(const Tile<MT, NT>& x, char* out, uint64_t ld, uint32_t rows,
                                                     uint32_t depth) const
     {
+        constexpr int J = NT / kParts;
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
-        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int part = 0; part < kParts; ++part) {
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t row = wn + j * 16 + (lane & 15), k = wm + i * 16 + quad * 4;
-                const f32x4 v = x.v[i][j];
-                u32x2 hi, lo;
-                uint32_t h0, h1, l0, l1;
-                split_halves(v[0], v[1], &h0, &l0);
-                split_halves(v[2], v[3], &h1, &l1);
-                hi = u32x2{h0, h1};
-                lo = u32x2{l0, l1};
-                *reinterpret_cast<u32x2*>(lds + at(row, halves_at(k, 0), row)) = hi;
-                *reinterpret_cast<u32x2*>(lds + at(row, halves_at(k, 1), row)) = lo;
+            for (int j = 0; j < J; ++j) {
+                if constexpr (B == 256) __builtin_amdgcn_sched_barrier(0);  // bounds the registers in use
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const uint32_t row = (wn * J + j) * 16 + (lane & 15), k = wm * S::kWaveM + i * 16 + quad * 4;
+                    const f32x4 v = x.v[i][part * J + j];
+                    uint32_t h0, h1, l0, l1;
+                    split_halves(v[0], v[1], &h0, &l0);
+                    split_halves(v[2], v[3], &h1, &l1);
+                    *reinterpret_cast<u32x2*>(lds + at(row, halves_at(k, 0), row)) = u32x2{h0, h1};
+                    *reinterpret_cast<u32x2*>(lds + at(row, halves_at(k, 1), row)) = u32x2{l0, l1};
+                }
             }
-        __syncthreads();
-        copy_rows(out, ld, n_base, rows, m_base, depth, 0);
+            __syncthreads();
+            copy_rows<J * 16, S::kWaveN>(out, ld, n_base + part * J * 16, rows, m_base, depth, 0);
+        }
     }
 
     // out[m][n]: neighbouring columns lie in neighbouring lanes, which exchange
     // halves, so that each has two columns of two rows.
-    __device__ __forceinline__ void store_by_row(const Tile<N, N>& x, char* out, uint64_t ld, uint32_t rows,
+    __device__ __forceinline__ void store_by_row(const Tile<MT, NT>& x, char* out, uint64_t ld, uint32_t rows,
                                                  uint32_t depth) const
     {
+        constexpr int I = MT / kParts;
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4, odd = lane & 1;
-        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int part = 0; part < kParts; ++part) {
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const f32x4 v = x.v[i][j];
-                uint32_t p01[2], p23[2];
-                split_halves(v[0], v[1], &p01[0], &p01[1]);
-                split_halves(v[2], v[3], &p23[0], &p23[1]);
-                const uint32_t row = wm + i * 16 + quad * 4 + odd * 2, k = wn + j * 16 + (lane & 14);
+            for (int j = 0; j < NT; ++j) {
+                if constexpr (B == 256) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t give = odd ? p01[q] : p23[q], keep = odd ? p23[q] : p01[q];
-                    const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);  // lane ^ 1
-                    const uint32_t lo = odd ? got : keep, hi = odd ? keep : got;
-                    const uint32_t byte = halves_at(k, q);
-                    *reinterpret_cast<uint32_t*>(lds + at(row, byte, row >> 1)) = __builtin_amdgcn_perm(hi, lo, 0x05040100);
-                    *reinterpret_cast<uint32_t*>(lds + at(row + 1, byte, row >> 1)) =
-                        __builtin_amdgcn_perm(hi, lo, 0x07060302);
+                for (int i = 0; i < I; ++i) {
+                    const f32x4 v = x.v[part * I + i][j];
+                    uint32_t p01[2], p23[2];
+                    split_halves(v[0], v[1], &p01[0], &p01[1]);
+                    split_halves(v[2], v[3], &p23[0], &p23[1]);
+                    const uint32_t row = (wm * I + i) * 16 + quad * 4 + odd * 2, k = wn * S::kWaveN + j * 16 + (lane & 14);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t give = odd ? p01[q] : p23[q], keep = odd ? p23[q] : p01[q];
+                        const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+                        const uint32_t lo = odd ? got : keep, hi = odd ? keep : got;
+                        const uint32_t byte = halves_at(k, q);
+                        *reinterpret_cast<uint32_t*>(lds + at(row, byte, row >> 1)) =
+                            __builtin_amdgcn_perm(hi, lo, 0x05040100);
+                        *reinterpret_cast<uint32_t*>(lds + at(row + 1, byte, row >> 1)) =
+                            __builtin_amdgcn_perm(hi, lo, 0x07060302);
+                    }
                 }
             }
-        __syncthreads();
-        copy_rows(out, ld, m_base, rows, n_base, depth, 1);
+            __syncthreads();
+            copy_rows<I * 16, S::kWaveM>(out, ld, m_base + part * I * 16, rows, n_base, depth, 1);
+        }
     }
 
 private:
+    // Row r of LDS is row r % PART of the part of wave r / PART, of WAVE rows each.
+    template <uint32_t PART, uint32_t WAVE>
     __device__ __forceinline__ void copy_rows(char* out, uint64_t ld, uint32_t row0, uint32_t rows, uint32_t k0,
                                               uint32_t depth, int key_shift) const
     {
@@ -138,9 +158,10 @@ private:
         const uint32_t c = threadIdx.x % kChunks;
         if (k0 + c / 8 * 32 >= depth) return;
 #pragma unroll 4
-        for (uint32_t r = threadIdx.x / kChunks; r < B; r += 256 / kChunks) {
-            if (row0 + r >= rows) break;
-            *reinterpret_cast<u32x4*>(out + static_cast<uint64_t>(row0 + r) * ld + halves_bytes(k0) + c * 16) =
+        for (uint32_t r = threadIdx.x / kChunks; r < B / kParts; r += S::kThreads / kChunks) {
+            const uint32_t to = row0 + r / PART * WAVE + r % PART;
+            if (to >= rows) continue;
+            *reinterpret_cast<u32x4*>(out + to * ld + halves_bytes(k0) + c * 16) =
                 *reinterpret_cast<const u32x4*>(lds + at(r, c * 16, r >> key_shift));
         }
     }
@@ -180,113 +201,148 @@ __device__ __forceinline__ void halves_place(const HalvesArgs& g, uint32_t id, u
     *tn = in / high;
 }
 
-// B x B tiles, four waves of B/2 x B/2, two workgroups a CU: one waits or stores
-// while the other multiplies. JOIN: the split tiles' sums.
-template <int B, bool JOIN, class Epilogue>
-__global__ __launch_bounds__(256, 2) void gemm_halves(const HalvesArgs g, const Epilogue epi)
+// The product of one tile, into `acc`.
+template <int B>
+__device__ __forceinline__ void multiply_halves(char* lds, const char* a, const char* b, const HalvesArgs& g,
+                                                uint32_t m_base, uint32_t n_base, uint32_t steps,
+                                                Tile<HalvesShape<B>::MT, HalvesShape<B>::NT>& acc)
 {
     using S = HalvesShape<B>;
     using T = MmaF16;
-    constexpr int N = S::kTiles;
-    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStage];
-    uint32_t matrix, tm, tn, split = 0;
-    const uint32_t id = JOIN ? g.whole + blockIdx.x : halves_tile_id(g, &split);
-    halves_place(g, id, &matrix, &tm, &tn);
-
+    constexpr int N = S::NT;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t wm = (wave >> 1) * S::kWave, wn = (wave & 1) * S::kWave;
-    const uint32_t m_base = tm * B, n_base = tn * B;
+    const uint32_t wm = (wave >> 1) * S::kWaveM, wn = (wave & 1) * S::kWaveN;
+    auto rows_of = [&](const char* p, uint32_t ld, uint32_t r0, uint32_t rows) {
+        const uint32_t left = rows > r0 ? min(rows - r0, static_cast<uint32_t>(B)) : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p + static_cast<uint64_t>(r0) * ld), 0,
+                                                 static_cast<int>(left * ld), 0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t ra = rows_of(a, g.lda, m_base, g.m);
+    const __amdgpu_buffer_rsrc_t rb = rows_of(b, g.ldb, n_base, g.n);
+    const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 16;
+    uint32_t off_a[S::kLoads], off_b[S::kLoads];
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) {
+        off_a[i] = (i * 32 + (tid >> 3)) * g.lda + col;
+        off_b[i] = (i * 32 + (tid >> 3)) * g.ldb + col;
+    }
+    auto fetch = [&](uint32_t where, uint32_t step) {
+        const uint32_t at = step * 128;
+        const bool in = step < steps;
+        char* p = lds + where + wave * 1024;
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) load_to_lds(ra, p + i * 4096, in ? off_a[i] : kPastEnd, at);
+#pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) load_to_lds(rb, p + S::kB + i * 4096, in ? off_b[i] : kPastEnd, at);
+    };
 
-    f32x4* partial = nullptr;
-    if (JOIN || id >= g.whole)
-        partial = reinterpret_cast<f32x4*>(g.partial) + (static_cast<uint64_t>(id - g.whole) * g.splits + split) * (N * N * 256) + tid;
-    Tile<N, N> acc;
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+    const int frow = lane & 15, fcol = lane >> 4;
+    const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
+    const uint32_t pa = base + (wm + frow) * 128 + swizzled, pb = base + S::kB + (wn + frow) * 128 + swizzled;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    if constexpr (JOIN) {
-        for (uint32_t k = 0; k < g.splits; ++k, partial += N * N * 256)
+    constexpr int kAhead = S::kStages - 1;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i * S::kStage, i);
+    uint32_t stage = 0, ahead = kAhead * S::kStage;
+    i32x4 fa[N][2], fb[N][2];
+    for (uint32_t k = 0; k < steps; ++k) {
+        // this stage has arrived in every wave, and nobody reads the one before any more
+        arrive<(kAhead - 1) * 2 * S::kLoads>();
+        fetch(ahead, k + kAhead);
+        const uint32_t xa = pa + stage, xb = pb + stage;
+        if constexpr (B == 128) {
+            read_fragments<0, 0>(fa, fb[0], fb[1], xa, xa ^ 64, xb, xb ^ 64);
+            read_fragments4(fb[2], fb[3], xb + 4096, (xb ^ 64) + 4096);
+        } else {
+            read_few<2, 2>(fa, fb, xa, xa ^ 64, xb, xb ^ 64);
+        }
+        constexpr int kOfA[3] = {0, 1, 0}, kOfB[3] = {1, 0, 0};  // the smaller products first
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc.v[i][j] += partial[(i * N + j) * 256];
+                for (int j = 0; j < N; ++j)
+                    acc.v[i][j] = T::mma(__builtin_bit_cast(T::Frag, fa[i][kOfA[p]]),
+                                         __builtin_bit_cast(T::Frag, fb[j][kOfB[p]]), acc.v[i][j]);
+        ahead = stage;
+        stage = stage == kAhead * S::kStage ? 0 : stage + S::kStage;
+    }
+    // the loads past the end have arrived too: LDS is the epilogue's
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// JOIN: the split tiles' sums.
+template <int B, bool JOIN, class Epilogue>
+__global__ __launch_bounds__(HalvesShape<B>::kThreads, 2) void gemm_halves(const HalvesArgs g, const Epilogue epi)
+{
+    using S = HalvesShape<B>;
+    constexpr int MT = S::MT, NT = S::NT;
+    __shared__ __attribute__((aligned(1024))) char lds[S::kStages * S::kStage];
+    uint32_t matrix, tm, tn, split = 0;
+    const uint32_t id = JOIN ? g.whole + blockIdx.x : halves_tile_id(g, &split);
+    halves_place(g, id, &matrix, &tm, &tn);
+    const int tid = threadIdx.x;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t wm = wave / S::kWavesN, wn = wave % S::kWavesN;
+    const uint32_t m_base = tm * B, n_base = tn * B;
+
+    // (decided by `id`, the same in all lanes, and not by the pointer: descriptors
+    // that may differ from lane to lane are loaded through in loops)
+    const bool cut = JOIN || id >= g.whole;
+    f32x4* partial = reinterpret_cast<f32x4*>(g.partial) + tid;
+    if (cut) partial += (static_cast<uint64_t>(id - g.whole) * g.splits + split) * (MT * NT * S::kThreads);
+    Tile<MT, NT> acc;
+    if constexpr (JOIN) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc.v[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // two parts' loads at a time: sixteen of 16 tiles of 128 in 15 us rather than 29
+        constexpr uint32_t kPart = MT * NT * S::kThreads;
+        uint32_t k = 0;
+        for (; k + 2 <= g.splits; k += 2, partial += 2 * kPart) {
+            f32x4 x[MT * NT], y[MT * NT];
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) x[i] = partial[i * S::kThreads];
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) y[i] = partial[i * S::kThreads + kPart];
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) acc.v[i / NT][i % NT] += x[i];
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) acc.v[i / NT][i % NT] += y[i];
+        }
+        for (; k < g.splits; ++k, partial += kPart)
+#pragma unroll
+            for (int i = 0; i < MT * NT; ++i) acc.v[i / NT][i % NT] += partial[i * S::kThreads];
     } else {
         uint32_t from = 0, to = g.steps;
-        if (partial) {
+        if (cut) {
             const uint32_t part = (g.steps + g.splits - 1) / g.splits;
             from = min(split * part, g.steps);
             to = min(from + part, g.steps);
         }
-        auto rows_of = [&](const char* p, uint64_t batch, uint32_t ld, uint32_t r0, uint32_t rows) {
-            const uint32_t left = rows > r0 ? min(rows - r0, static_cast<uint32_t>(B)) : 0;
-            return __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<char*>(p + matrix * batch + static_cast<uint64_t>(r0) * ld), 0, static_cast<int>(left * ld), 0x00020000);
-        };
-        const __amdgpu_buffer_rsrc_t ra = rows_of(g.a, g.batch_a, g.lda, m_base, g.m);
-        const __amdgpu_buffer_rsrc_t rb = rows_of(g.b, g.batch_b, g.ldb, n_base, g.n);
-        const uint32_t col = static_cast<uint32_t>((tid & 7) ^ ((tid >> 3) & 7)) * 16;
-        uint32_t off_a[S::kLoads], off_b[S::kLoads];
+        const char *a = g.a + matrix * g.batch_a + from * 128ull, *b = g.b + matrix * g.batch_b + from * 128ull;
+        if constexpr (B == 256)
+            multiply_large<MmaF16, true>(lds, LargeOperand{a, g.lda, m_base, g.m}, LargeOperand{b, g.ldb, n_base, g.n},
+                                         (to - from) * kTileK, acc);
+        else
+            multiply_halves<B>(lds, a, b, g, m_base, n_base, to - from, acc);
+        if (cut) {
 #pragma unroll
-        for (int i = 0; i < S::kLoads; ++i) {
-            off_a[i] = (i * 32 + (tid >> 3)) * g.lda + col;
-            off_b[i] = (i * 32 + (tid >> 3)) * g.ldb + col;
-        }
-        auto fetch = [&](uint32_t where, uint32_t step) {
-            const uint32_t at = step * 128;
-            const bool in = step < to;
-            char* p = lds + where + wave * 1024;
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int i = 0; i < S::kLoads; ++i) load_to_lds(ra, p + i * 4096, in ? off_a[i] : kPastEnd, at);
-#pragma unroll
-            for (int i = 0; i < S::kLoads; ++i) load_to_lds(rb, p + S::kB + i * 4096, in ? off_b[i] : kPastEnd, at);
-        };
-
-        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-        const int frow = lane & 15, fcol = lane >> 4;
-        const uint32_t swizzled = static_cast<uint32_t>((fcol ^ (frow & 7)) * 16);
-        const uint32_t pa = base + (wm + frow) * 128 + swizzled, pb = base + S::kB + (wn + frow) * 128 + swizzled;
-        constexpr int kAhead = S::kStages - 1;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) fetch(i * S::kStage, from + i);
-        uint32_t stage = 0, ahead = kAhead * S::kStage;
-        i32x4 fa[N][2], fb[N][2];
-        for (uint32_t k = from; k < to; ++k) {
-            // this stage has arrived in every wave, and nobody reads the one before any more
-            arrive<(kAhead - 1) * 2 * S::kLoads>();
-            fetch(ahead, k + kAhead);
-            const uint32_t xa = pa + stage, xb = pb + stage;
-            if constexpr (B == 128) {
-                read_fragments<0, 0>(fa, fb[0], fb[1], xa, xa ^ 64, xb, xb ^ 64);
-                read_fragments4(fb[2], fb[3], (xb ^ 0) + 4096, (xb ^ 64) + 4096);
-            } else {
-                read_few<2, 2>(fa, fb, xa, xa ^ 64, xb, xb ^ 64);
-            }
-            constexpr int kOfA[3] = {0, 1, 0}, kOfB[3] = {1, 0, 0};  // the smaller products first
-#pragma unroll
-            for (int p = 0; p < 3; ++p)
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        acc.v[i][j] = T::mma(__builtin_bit_cast(T::Frag, fa[i][kOfA[p]]),
-                                             __builtin_bit_cast(T::Frag, fb[j][kOfB[p]]), acc.v[i][j]);
-            ahead = stage;
-            stage = stage == kAhead * S::kStage ? 0 : stage + S::kStage;
-        }
-        // the loads past the end have arrived too: LDS is the epilogue's
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (partial) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < N; ++j) partial[(i * N + j) * 256] = acc.v[i][j];
+                for (int j = 0; j < NT; ++j) partial[(i * NT + j) * S::kThreads] = acc.v[i][j];
             return;
         }
     }
-    epi(acc, m_base + wm, n_base + wn, g, matrix, HalvesStaging<B>{lds, wm, wn, m_base, n_base}, tm, tn);
+    epi(acc, m_base + wm * S::kWaveM, n_base + wn * S::kWaveN, g, matrix, HalvesStaging<B>{lds, wm, wn, m_base, n_base}, tm,
+        tn);
 }
 
 }  // namespace

@@ -204,34 +204,42 @@ __global__ __launch_bounds__(kBlock) void lay_out_matrices(const GroupIn p, cons
 // ---------------------------------------------------------------------------
 // epilogues
 // ---------------------------------------------------------------------------
-// factor C + shift I of the symmetric product C, up to two of them.
+// factor C + shift I of the symmetric product C, and of that again, if there
+// are two to be written.
 struct SymmetricEpilogue {
     char* out[2];  // the first may be null
     uint64_t batch;
     uint32_t ld, pad;  // bytes, elements
     float factor[2], shift[2];
 
-    template <int N, class S>
-    __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
+    template <int MT, int NT, class S>
+    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
                                                uint32_t matrix, const S& stage, uint32_t tm, uint32_t tn) const
     {
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (!out[k]) continue;
-            Tile<N, N> x;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint32_t row = m0 + i * 16 + quad * 4 + r, col = n0 + j * 16 + (lane & 15);
-                        x.v[i][j][r] = factor[k] * acc.v[i][j][r] + (row == col && row < g.m ? shift[k] : 0.0f);
-                    }
+                    for (int r = 0; r < 4; ++r) acc.v[i][j][r] *= factor[k];
+            if (tm == tn && shift[k] != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t row = m0 + i * 16 + quad * 4 + r, col = n0 + j * 16 + (lane & 15);
+                            acc.v[i][j][r] += row == col && row < g.m ? shift[k] : 0.0f;
+                        }
+            }
             char* to = out[k] + matrix * batch;
-            stage.store_by_column(x, to, ld, g.n, pad);
-            if (tm != tn) stage.store_by_row(x, to, ld, g.m, pad);
+            stage.store_by_column(acc, to, ld, g.n, pad);
+            if (tm != tn) stage.store_by_row(acc, to, ld, g.m, pad);
         }
     }
 };
@@ -244,14 +252,14 @@ struct NextEpilogue {
     uint32_t pad_n, pad_m;
     float factor;
 
-    template <int N, class S>
-    __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t, uint32_t, const HalvesArgs& g, uint32_t matrix,
+    template <int MT, int NT, class S>
+    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t, uint32_t, const HalvesArgs& g, uint32_t matrix,
                                                const S& stage, uint32_t, uint32_t) const
     {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc.v[i][j] *= factor;
+            for (int j = 0; j < NT; ++j) acc.v[i][j] *= factor;
         stage.store_by_column(acc, columns + matrix * batch_c, halves_bytes(pad_m), g.n, pad_m);
         stage.store_by_row(acc, rows + matrix * batch_r, halves_bytes(pad_n), g.m, pad_n);
     }
@@ -265,8 +273,8 @@ struct ResultEpilogue {
     int vec;
     float unit;
 
-    template <int N, class S>
-    __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
+    template <int MT, int NT, class S>
+    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
                                                uint32_t matrix, const S&, uint32_t, uint32_t) const
     {
         each_four(acc, m0, n0, g, unit, [&](uint32_t row, uint32_t col, float (&x)[4], uint32_t left) {
@@ -275,17 +283,17 @@ struct ResultEpilogue {
     }
 
     // fn(row, column, four results, how many of them there are)
-    template <int N, class Fn>
-    static __device__ __forceinline__ void each_four(const Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
+    template <int MT, int NT, class Fn>
+    static __device__ __forceinline__ void each_four(const Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
                                                      float unit, Fn fn)
     {
         const uint32_t lane = threadIdx.x & 63, quad = lane >> 4;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
+        for (int j = 0; j < NT; ++j) {
             const uint32_t row = n0 + j * 16 + (lane & 15);
             if (row >= g.n) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < MT; ++i) {
                 const uint32_t col = m0 + i * 16 + quad * 4;
                 if (col >= g.m) continue;
                 float x[4];
@@ -317,8 +325,8 @@ struct UpdateEpilogue {
     int nranks, vec;
     float keep, gain, unit;
 
-    template <int N, class S>
-    __device__ __forceinline__ void operator()(Tile<N, N>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
+    template <int MT, int NT, class S>
+    __device__ __forceinline__ void operator()(Tile<MT, NT>& acc, uint32_t m0, uint32_t n0, const HalvesArgs& g,
                                                uint32_t matrix, const S&, uint32_t, uint32_t) const
     {
         using R = ResultEpilogue<F>;
@@ -348,40 +356,84 @@ struct UpdateEpilogue {
 // ---------------------------------------------------------------------------
 // one call
 // ---------------------------------------------------------------------------
-constexpr uint64_t kCUs = 256;
+constexpr uint32_t kCUs = 256;
 constexpr int kSegment = 3;  // steps
 
-// Workgroups that run at a time, and what the parts of split tiles take.
-constexpr uint32_t kSlots = 2 * kCUs;
-constexpr uint32_t kLeastPart = 8;  // steps
-constexpr uint64_t kPartialBytes = uint64_t(kSlots) * 128 * 128 * 4;
+// How a product goes through its tiles: of which size, and in how many parts
+// those behind the last full round of workgroups are split.
+struct Tiling {
+    int tile;
+    uint32_t splits;  // 1: none
+    double cost;      // microseconds
+};
+constexpr uint32_t kLeastSteps = 16;  // of a split sum
+constexpr uint64_t kPartialBytes = uint64_t(2 * kCUs) * 128 * 128 * 4;
 
-// The parts of each tile behind the last full round of `tiles`, whose number goes
-// to *whole; 1: none is split.
-uint32_t splits_of(uint32_t tiles, uint32_t steps, int tile, uint32_t* whole)
+// Microseconds that fit the products measured, to within a fifth: a step of 32 with
+// all slots taken (two workgroups a CU; one of 256), with half of them, and what a
+// full round and a last one cost beside their steps. 4096 x 8192 x 4096: 481 us in
+// tiles of 256, 596 of 128, 873 of 64; 8 symmetric 1024 x 1024 x 1024: 58, 43 and 38.
+// The parts of split tiles are joined by a launch of its own: symmetric 4096 x 4096 x
+// 4096, 16 tiles of 128 behind a round of 512, 217 us whole, 169 in four parts, 192 in 32.
+struct TileCost {
+    int tile;
+    uint32_t slots;
+    double full, half, round, last, join;
+};
+constexpr TileCost kTileCosts[] = {{64, 2 * kCUs, 0.45, 0.27, 2.0, 3.0, 0.25},
+                                   {128, 2 * kCUs, 1.2, 0.75, 11.0, 4.5, 0.9},
+                                   {256, kCUs, 1.9, 1.55, 17.0, 7.0, 0.0}};
+
+uint64_t tiles_of(uint64_t m, uint64_t n, uint64_t matrices, bool symmetric, int tile)
 {
-    *whole = tiles;
-    const uint32_t rest = tiles % kSlots;
-    if (rest == 0) return 1;
-    const uint32_t splits = std::min({kSlots / rest, steps / kLeastPart, 16u});
-    if (splits < 2) return 1;
-    *whole = tiles - rest;
-    return splits;
+    const uint64_t tm = (m + tile - 1) / tile, tn = (n + tile - 1) / tile;
+    return matrices * (symmetric ? tm * (tm + 1) / 2 : tm * tn);
+}
+
+Tiling tiling_of(uint64_t m, uint64_t n, uint64_t depth, uint64_t matrices, bool symmetric)
+{
+    Tiling best{64, 1, 0.0};
+    const double steps = static_cast<double>(depth / kHalvesDepth);
+    for (const TileCost& c : kTileCosts) {
+        if (symmetric && c.tile == 256) continue;
+        const uint64_t tiles = tiles_of(m, n, matrices, symmetric, c.tile), rounds = tiles / c.slots, rest = tiles % c.slots;
+        for (uint32_t splits : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u}) {
+            if (splits > 1 && (rest == 0 || rest * splits > c.slots || depth < kLeastSteps * kHalvesDepth || c.tile == 256))
+                break;
+            double t = rounds * (steps * c.full + c.round);
+            if (rest) {
+                // workgroups end one by one: the last ones start early
+                const double each = std::ceil(steps / splits) * (2 * rest * splits > c.slots ? c.full : c.half);
+                t += c.last + each * (rounds ? 0.65 : 1.0) + (splits > 1 ? 5.0 + splits * c.join : 0.0);
+            }
+            if (best.cost == 0.0 || t < best.cost) best = Tiling{c.tile, splits, t};
+        }
+    }
+    return best;
 }
 
 struct Layout {
     uint64_t m, n, pad_m, pad_n;
     uint64_t rows, columns, square;  // bytes of X by rows, by columns, of D
     int parts;                       // of a matrix's sum of squares
+    bool segments;                   // the way the steps go
     int squares;                     // matrices of the smaller side
     uint64_t per_matrix;             // bytes of all
 };
 
-// Whether steps go in segments: nine products of 9 (n - m) m^2 less in five steps,
-// and three launches more.
-bool in_segments(uint64_t m, uint64_t n) { return 4 * n >= 5 * m; }
-
-Layout layout_of(uint64_t rows, uint64_t cols)
+// Whether steps go in segments: products of the smaller side alone, 14 in five
+// steps beside two of each with the larger one, or five of each kind; what a
+// launch costs beside its product decides for small ones. 3 x 1027 x 770 XXX us by
+// steps, XXX in segments, 4 x 64 x 192 67 and 82, 8 x 2048 x 4096 XXX and XXX.
+bool in_segments(uint64_t m, uint64_t n, uint64_t count)
+{
+    constexpr double kLaunch = 2.0;
+    const double gram = tiling_of(m, m, round_up(n, kHalvesDepth), count, true).cost + kLaunch,
+                 square = tiling_of(m, m, round_up(m, kHalvesDepth), count, true).cost + kLaunch,
+                 wide = tiling_of(m, n, round_up(m, kHalvesDepth), count, false).cost + kLaunch;
+    return 2 * gram + 14 * square + 2 * wide < 5 * (gram + square + wide);
+}
+Layout layout_of(uint64_t rows, uint64_t cols, uint64_t count)
 {
     Layout l;
     l.m = std::min(rows, cols);
@@ -392,13 +444,14 @@ Layout layout_of(uint64_t rows, uint64_t cols)
     l.columns = round_up(l.n * halves_bytes(l.pad_m), 256);
     l.square = round_up(l.m * halves_bytes(l.pad_m), 256);
     l.parts = static_cast<int>(std::min<uint64_t>((rows * cols + kBlock * 32 - 1) / (kBlock * 32), 256));
-    l.squares = in_segments(l.m, l.n) ? 7 : 2;
+    l.segments = in_segments(l.m, l.n, std::min<uint64_t>(count, kMostGroup));
+    l.squares = l.segments ? 7 : 2;
     l.per_matrix = l.rows + 2 * l.columns + l.squares * l.square + round_up(l.parts * sizeof(double), 256);
     return l;
 }
 
-// Whether a product is ever deep enough for parts.
-bool may_split(const Layout& l) { return l.pad_n >= 2 * kLeastPart * kHalvesDepth; }
+// Whether a product may be deep enough for parts.
+bool may_split(const Layout& l) { return l.pad_n >= kLeastSteps * kHalvesDepth; }
 
 // Matrices of a group: as many as their pointers fit kernel arguments, and about
 // kGroupBytes of workspace; a matrix beyond that fills the chip alone.
@@ -410,33 +463,36 @@ uint64_t group_of(uint64_t count, const Layout& l, int nranks)
 }
 
 template <int B, class Epilogue>
-hipError_t launch_tiles(HalvesArgs g, uint64_t matrices, float* partial, const Epilogue& epi, hipStream_t s)
+hipError_t launch_tiles(HalvesArgs g, uint64_t matrices, uint32_t splits, const Epilogue& epi, hipStream_t s)
 {
+    g.tiles_m = (g.m + B - 1) / B;
+    g.tiles_n = (g.n + B - 1) / B;
+    g.per_matrix = g.symmetric ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
     const uint32_t tiles = static_cast<uint32_t>(g.per_matrix * matrices);
-    g.splits = splits_of(tiles, g.steps, B, &g.whole);
-    g.partial = partial;
-    hipLaunchKernelGGL((gemm_halves<B, false, Epilogue>), dim3(g.whole + (tiles - g.whole) * g.splits), dim3(256), 0, s, g, epi);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || g.whole == tiles) return e;
-    hipLaunchKernelGGL((gemm_halves<B, true, Epilogue>), dim3(tiles - g.whole), dim3(256), 0, s, g, epi);
-    return hipGetLastError();
+    g.splits = splits;
+    g.whole = splits > 1 ? tiles - tiles % (2 * kCUs) : tiles;
+    hipLaunchKernelGGL((gemm_halves<B, false, Epilogue>), dim3(g.whole + (tiles - g.whole) * splits),
+                       dim3(HalvesShape<B>::kThreads), 0, s, g, epi);
+    hipError_t e = hipGetLastError();
+    if constexpr (B < 256) {
+        if (e == hipSuccess && g.whole < tiles) {
+            hipLaunchKernelGGL((gemm_halves<B, true, Epilogue>), dim3(tiles - g.whole), dim3(HalvesShape<B>::kThreads), 0, s,
+                               g, epi);
+            e = hipGetLastError();
+        }
+    }
+    return e;
 }
 
 template <class Epilogue>
-hipError_t launch_halves(HalvesArgs g, uint64_t matrices, int tile, float* partial, const Epilogue& epi, hipStream_t s)
+hipError_t launch_halves(const HalvesArgs& g, uint64_t matrices, const Epilogue& epi, hipStream_t s)
 {
-    const uint32_t b = static_cast<uint32_t>(tile);
-    g.tiles_m = (g.m + b - 1) / b;
-    g.tiles_n = (g.n + b - 1) / b;
-    g.per_matrix = g.symmetric ? g.tiles_m * (g.tiles_m + 1) / 2 : g.tiles_m * g.tiles_n;
-    return tile == 128 ? launch_tiles<128>(g, matrices, partial, epi, s) : launch_tiles<64>(g, matrices, partial, epi, s);
-}
-
-// Tiles of 64 where those of 128 leave CUs idle.
-int tile_of(uint64_t m, uint64_t n, uint64_t matrices, bool symmetric)
-{
-    const uint64_t tm = (m + 127) / 128, tn = (n + 127) / 128;
-    return matrices * (symmetric ? tm * (tm + 1) / 2 : tm * tn) >= kCUs ? 128 : 64;
+    const Tiling t = tiling_of(g.m, g.n, static_cast<uint64_t>(g.steps) * kHalvesDepth, matrices, g.symmetric);
+    if constexpr (!std::is_same<Epilogue, SymmetricEpilogue>::value) {
+        if (t.tile == 256) return launch_tiles<256>(g, matrices, 1, epi, s);
+    }
+    return t.tile == 128 ? launch_tiles<128>(g, matrices, t.splits, epi, s)
+                         : launch_tiles<64>(g, matrices, t.splits, epi, s);
 }
 
 struct Group {
@@ -459,6 +515,7 @@ struct Group {
         g.n = static_cast<uint32_t>(rows_y);
         g.steps = static_cast<uint32_t>(depth / kHalvesDepth);
         g.symmetric = symmetric;
+        g.partial = sums();
         return g;
     }
 
@@ -503,7 +560,7 @@ struct Group {
     }
 
     template <class F>
-    hipError_t finish(const HalvesArgs& g, int tile, float unit) const
+    hipError_t finish(const HalvesArgs& g, float unit) const
     {
         constexpr uint64_t e = sizeof(RawOf<F>);
         uintptr_t mis = a.ld_out * e;
@@ -516,7 +573,7 @@ struct Group {
             epi.ld = a.ld_out;
             epi.unit = unit;
             epi.vec = mis % (4 * e) == 0;
-            return launch_halves(g, count, tile, sums(), epi, s);
+            return launch_halves(g, count, epi, s);
         }
         UpdateEpilogue<F> epi{};
         for (uint64_t i = 0; i < count; ++i) {
@@ -534,7 +591,7 @@ struct Group {
         epi.keep = static_cast<float>(1.0 - a.lr * a.weight_decay);
         epi.gain = static_cast<float>(a.lr * a.update_scale);
         epi.unit = unit;
-        return launch_halves(g, count, tile, sums(), epi, s);
+        return launch_halves(g, count, epi, s);
     }
 
     hipError_t run() const
@@ -551,7 +608,6 @@ struct Group {
         for (int i = 0; i < l.squares; ++i) square[i] = take(l.square);
         double* partial = reinterpret_cast<double*>(take(round_up(l.parts * sizeof(double), 256)));
         const bool tall = a.rows > a.cols;
-        const int wide_tile = tile_of(l.m, l.n, count, false);
         char *straight = tall ? xt[0] : x, *turned = tall ? x : xt[0];
         const uint64_t batch_s = tall ? l.columns : l.rows, batch_t = tall ? l.rows : l.columns;
         hipError_t e;
@@ -562,13 +618,12 @@ struct Group {
         default: return hipErrorInvalidValue;
         }
         if (e != hipSuccess) return e;
-        const bool segments = in_segments(l.m, l.n);
         double top = 1.0;  // of the singular values
         int turn = 0;      // which of xt holds X
         for (int k = 0; k < a.steps;) {
             // segments of up to three steps, the longer ones first
             const int left = a.steps - k, count_left = (left + kSegment - 1) / kSegment;
-            const int size = segments ? (left + count_left - 1) / count_left : 1;
+            const int size = l.segments ? (left + count_left - 1) / count_left : 1;
             const char* p;
             double p_scale;
             if ((e = segment(x, square, k, size, &top, &p, &p_scale)) != hipSuccess) return e;
@@ -580,15 +635,15 @@ struct Group {
                                           : product(xt[turn], l.columns, l.n, p, l.square, l.m, l.pad_m, false);
                 const float out_unit = unit / kHalvesScale;
                 switch (a.out_dtype) {
-                case AR_FLOAT32: return finish<F32>(g, wide_tile, out_unit);
-                case AR_FLOAT16: return finish<F16>(g, wide_tile, out_unit);
-                case AR_BFLOAT16: return finish<BF16>(g, wide_tile, out_unit);
+                case AR_FLOAT32: return finish<F32>(g, out_unit);
+                case AR_FLOAT16: return finish<F16>(g, out_unit);
+                case AR_BFLOAT16: return finish<BF16>(g, out_unit);
                 default: return hipErrorInvalidValue;
                 }
             }
             const NextEpilogue next{x, xt[turn ^ 1], l.rows, l.columns, static_cast<uint32_t>(l.pad_n),
                                     static_cast<uint32_t>(l.pad_m), unit};
-            e = launch_halves(product(p, l.square, l.m, xt[turn], l.columns, l.n, l.pad_m, false), count, wide_tile, sums(), next, s);
+            e = launch_halves(product(p, l.square, l.m, xt[turn], l.columns, l.n, l.pad_m, false), count, next, s);
             if (e != hipSuccess) return e;
             turn ^= 1;
         }
@@ -601,7 +656,6 @@ struct Group {
                        double* p_scale) const
     {
         char *d = square[0], *q[2] = {square[1], square[4]}, *gram = square[2], *t = square[3], *prod[2] = {square[5], square[6]};
-        const int tile = tile_of(l.m, l.m, count, true);
         hipError_t e;
         double largest = 1.0;  // of P's eigenvalues
         for (int i = 0; i < size; ++i) {
@@ -613,12 +667,13 @@ struct Group {
             if (i + 1 < size) {
                 epi.out[0] = gram;
                 epi.factor[0] = 1.0f / kHalvesScale;
+                epi.factor[1] *= kHalvesScale;
             }
             const HalvesArgs g = i == 0 ? product(x, l.rows, l.m, x, l.rows, l.m, l.pad_n, true)
                                         : square_product(t, q[(i - 1) & 1]);
-            if ((e = launch_halves(g, count, tile, sums(), epi, s)) != hipSuccess) return e;
+            if ((e = launch_halves(g, count, epi, s)) != hipSuccess) return e;
             if (cc != 0.0) {
-                e = launch_halves(square_product(d, d), count, tile, sums(), symmetric(bracket, cc, ca - cb * cb / (4.0 * cc)), s);
+                e = launch_halves(square_product(d, d), count, symmetric(bracket, cc, ca - cb * cb / (4.0 * cc)), s);
                 if (e != hipSuccess) return e;
             }
             double most = 0.0, next = 0.0;
@@ -638,12 +693,12 @@ struct Group {
                 char* to = prod[i & 1];
                 SymmetricEpilogue join = symmetric(to, 1.0, 0.0);
                 join.factor[1] = static_cast<float>(scale / (kHalvesScale * *p_scale));
-                if ((e = launch_halves(square_product(bracket, *p), count, tile, sums(), join, s)) != hipSuccess) return e;
+                if ((e = launch_halves(square_product(bracket, *p), count, join, s)) != hipSuccess) return e;
                 *p = to;
                 *p_scale = scale;
             }
             if (i + 1 < size) {  // A Q, then (A Q) Q at the head of the loop
-                if ((e = launch_halves(square_product(gram, bracket), count, tile, sums(), symmetric(t, 1.0, 0.0), s)) != hipSuccess)
+                if ((e = launch_halves(square_product(gram, bracket), count, symmetric(t, 1.0, 0.0), s)) != hipSuccess)
                     return e;
             }
         }
@@ -676,13 +731,13 @@ struct Group {
 uint64_t orthogonalize_bytes(uint64_t count, uint64_t rows, uint64_t cols)
 {
     if (count == 0 || rows == 0 || cols == 0) return 0;
-    const Layout l = layout_of(rows, cols);
+    const Layout l = layout_of(rows, cols, count);
     return group_of(count, l, 1) * l.per_matrix + (may_split(l) ? kPartialBytes : 0);
 }
 
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a, char* ws, hipStream_t stream)
 {
-    const Layout l = layout_of(a.rows, a.cols);
+    const Layout l = layout_of(a.rows, a.cols, a.count);
     const uint64_t most = group_of(a.count, l, a.nranks);
     for (uint64_t first = 0; first < a.count; first += most) {
         const hipError_t e = Group{a, l, first, std::min(most, a.count - first), ws, stream}.run();
