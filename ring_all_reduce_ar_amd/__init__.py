@@ -561,9 +561,15 @@ def _matrices(bufs, ld: int):
     """(addresses, row pitch) of a list of matrices of one size: the tensors' own
     pitch, the same for all, where none is given."""
     bufs = _flat(bufs)
-    if ld or not len(bufs) or isinstance(bufs[0], int):
-        return _ptrs([b if isinstance(b, int) else _rows(b, ld or 1)[0] for b in bufs] if ld else bufs), ld
-    rows = [_rows(b, 0) for b in bufs]
+    if not len(bufs) or isinstance(bufs[0], int):
+        return _ptrs(bufs), ld
+    # rows alike, as in most lists: one look serves for all (a pitch below the width is refused with the call)
+    if not ld:
+        strides = {b.stride() for b in bufs}
+        first = bufs[0].stride()
+        if len(strides) == 1 and len(first) == 2 and first[1] == 1 and bufs[0].shape[0] > 1:
+            return _ptrs([b.data_ptr() for b in bufs]), first[0]
+    rows = [_rows(b, ld) for b in bufs]
     if any(pitch != rows[0][1] for _, pitch in rows):
         raise ValueError("the matrices of a list have one row pitch")
     return _ptrs([p for p, _ in rows]), rows[0][1]

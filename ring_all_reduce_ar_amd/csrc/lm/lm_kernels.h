@@ -1,6 +1,6 @@
 // lm_kernels.h -- internal interface between lm_api.cpp and the kernels of the
 // language-model operators (clip.hip, embedding.hip, cross_entropy.hip with
-// log_probs.h, orthogonalize.hip).
+// log_probs.h, orthogonalize.hip, orthogonalize_small.hip).
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -198,6 +198,9 @@ struct OrthogonalizeArgs {
 };
 uint64_t orthogonalize_bytes(uint64_t count, uint64_t rows, uint64_t cols);
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a, char* ws, hipStream_t stream);
+// Matrices of one workgroup each (orthogonalize_small.hip), without a workspace.
+bool is_small(uint64_t rows, uint64_t cols, int steps);
+hipError_t launch_orthogonalize_small(const OrthogonalizeArgs& a, hipStream_t stream);
 
 }  // namespace lm
 }  // namespace ar

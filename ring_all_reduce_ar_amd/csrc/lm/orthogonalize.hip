@@ -30,97 +30,25 @@
 #include <algorithm>
 #include <cmath>
 
-#include "gemm_halves.h"
-#include "rows.h"
+#include "orthogonalize.h"
 
 namespace ar {
 namespace lm {
 
 namespace {
 
-template <class F>
-using RawOf = typename std::conditional<F::kEpv == 8, uint16_t, float>::type;
-
-// Four elements as floats.
-template <class F>
-__device__ __forceinline__ void widen4(const RawOf<F>* raw, float* x)
-{
-    if constexpr (F::kEpv == 8) {
-        u32x2 v;
-        __builtin_memcpy(&v, raw, 8);
-        F::unpack4(v, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = raw[i];
-    }
-}
-
-// ---------------------------------------------------------------------------
-// the matrix that is orthogonalised
-// ---------------------------------------------------------------------------
 // Pointers of a group of matrices.
 struct GroupIn {
     const void* in[kMostGroup];             // or gradients
     const float* momentum_in[kMostGroup];
     float* momentum_out[kMostGroup];
-    uint64_t rows, cols, ld_in, ld_momentum;
-    float decay, rest;  // rest = 1 - decay
-    int nesterov;
-};
+    SourceShape shape;
 
-// Eight elements of a row of U, from column c on: the matrix itself, or the
-// momentum's update, FIRST: which is also stored.
-template <class F, bool MUON, bool VEC>
-struct Source {
-    using Raw = RawOf<F>;
-    static constexpr int A = VEC ? 16 : sizeof(Raw), AM = VEC ? 16 : 4;
-
-    template <bool FIRST>
-    static __device__ __forceinline__ void get(const GroupIn& p, uint32_t matrix, uint64_t row, uint64_t c, float (&u)[8])
+    __device__ __forceinline__ SourcePointers of(uint32_t matrix) const
     {
-        const uint64_t left = p.cols - c;
-        Raw raw[8];
-        get8<Raw, A>(p.in[matrix], row * p.ld_in + c, left, raw);
-        widen4<F>(raw, u);
-        widen4<F>(raw + 4, u + 4);
-        if constexpr (MUON) {
-            float m[8];
-            const uint64_t at = row * p.ld_momentum + c;
-            get8<float, AM>(FIRST ? p.momentum_in[matrix] : p.momentum_out[matrix], at, left, m);
-            if constexpr (FIRST) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m[i] = p.decay * m[i] + p.rest * u[i];
-                float* to = p.momentum_out[matrix] + at;
-                if (VEC && left >= 8) {
-                    f32x4 v[2];
-                    __builtin_memcpy(v, m, sizeof(m));
-                    reinterpret_cast<f32x4*>(to)[0] = v[0];
-                    reinterpret_cast<f32x4*>(to)[1] = v[1];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (static_cast<uint64_t>(i) < left) to[i] = m[i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = p.nesterov ? p.decay * m[i] + p.rest * u[i] : m[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = static_cast<uint64_t>(i) < left ? u[i] : 0.0f;
+        return SourcePointers{in[matrix], momentum_in[matrix], momentum_out[matrix]};
     }
 };
-
-template <int THREADS>
-__device__ __forceinline__ double block_sum(double x, double* waves)
-{
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
-    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = 0.0;
-    for (int w = 0; w < THREADS / 64; ++w) x += waves[w];
-    return x;
-}
 
 // partial[matrix][block] = its part of the sum of squares, in fp64: neither
 // squares beyond fp32's range nor small elements are lost.
@@ -130,30 +58,16 @@ __global__ __launch_bounds__(kBlock) void measure_matrices(const GroupIn p, int 
     __shared__ double waves[kBlock / 64];
     const uint32_t per = kBlock / lanes;
     double sum = 0.0;
-    for (uint64_t r = static_cast<uint64_t>(blockIdx.x) * per + threadIdx.x / lanes; r < p.rows;
+    for (uint64_t r = static_cast<uint64_t>(blockIdx.x) * per + threadIdx.x / lanes; r < p.shape.rows;
          r += static_cast<uint64_t>(gridDim.x) * per)
-        for (uint64_t c = (threadIdx.x & (lanes - 1)) * 8ull; c < p.cols; c += lanes * 8ull) {
+        for (uint64_t c = (threadIdx.x & (lanes - 1)) * 8ull; c < p.shape.cols; c += lanes * 8ull) {
             float u[8];
-            Source<F, MUON, VEC>::template get<true>(p, blockIdx.y, r, c, u);
+            Source<F, MUON, VEC>::template get<true>(p.shape, p.of(blockIdx.y), r, c, u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += static_cast<double>(u[i]) * u[i];
         }
     sum = block_sum<kBlock>(sum, waves);
     if (threadIdx.x == 0) partial[static_cast<uint64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = sum;
-}
-
-__device__ __forceinline__ void put_halves(char* row, uint32_t k, const float (&x)[8])
-{
-    u32x4 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h, l;
-        split_halves(x[2 * i], x[2 * i + 1], &h, &l);
-        hi[i] = h;
-        lo[i] = l;
-    }
-    *reinterpret_cast<u32x4*>(row + halves_at(k, 0)) = hi;
-    *reinterpret_cast<u32x4*>(row + halves_at(k, 1)) = lo;
 }
 
 // X in pieces, in the given order and transposed, zeros up to whole steps of
@@ -171,8 +85,8 @@ __global__ __launch_bounds__(kBlock) void lay_out_matrices(const GroupIn p, cons
     const float factor = static_cast<float>(kHalvesScale / (norm < eps ? eps : norm));
     straight += blockIdx.y * batch_s;
     turned += blockIdx.y * batch_t;
-    const uint64_t pad_r = (p.rows + 31) / 32 * 32, pad_c = (p.cols + 31) / 32 * 32;
-    const uint32_t high = static_cast<uint32_t>((p.rows + 63) / 64);
+    const uint64_t pad_r = (p.shape.rows + 31) / 32 * 32, pad_c = (p.shape.cols + 31) / 32 * 32;
+    const uint32_t high = static_cast<uint32_t>((p.shape.rows + 63) / 64);
     const uint64_t r0 = static_cast<uint64_t>(blockIdx.x % high) * 64, c0 = static_cast<uint64_t>(blockIdx.x / high) * 64;
     const int slot = threadIdx.x & 7;
 #pragma unroll
@@ -180,20 +94,20 @@ __global__ __launch_bounds__(kBlock) void lay_out_matrices(const GroupIn p, cons
         const int row = i * 32 + (threadIdx.x >> 3);
         const uint64_t r = r0 + row, c = c0 + slot * 8;
         float x[8] = {};
-        if (r < p.rows && c < p.cols) Source<F, MUON, VEC>::template get<false>(p, blockIdx.y, r, c, x);
+        if (r < p.shape.rows && c < p.shape.cols) Source<F, MUON, VEC>::template get<false>(p.shape, p.of(blockIdx.y), r, c, x);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             x[k] *= factor;
             tile[row][slot * 8 + k] = x[k];
         }
-        if (r < p.rows && c < pad_c) put_halves(straight + r * halves_bytes(pad_c), static_cast<uint32_t>(c), x);
+        if (r < p.shape.rows && c < pad_c) put_halves(straight + r * halves_bytes(pad_c), static_cast<uint32_t>(c), x);
     }
     __syncthreads();
     if (r0 + slot * 8 >= pad_r) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int c = i * 32 + (threadIdx.x >> 3);
-        if (c0 + c >= p.cols) continue;
+        if (c0 + c >= p.shape.cols) continue;
         float x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = tile[slot * 8 + k][c];
@@ -533,13 +447,7 @@ struct Group {
             p.momentum_out[i] = a.momentum_out[first + i];
             mis |= reinterpret_cast<uintptr_t>(p.momentum_in[i]) | reinterpret_cast<uintptr_t>(p.momentum_out[i]);
         }
-        p.rows = a.rows;
-        p.cols = a.cols;
-        p.ld_in = a.ld_in;
-        p.ld_momentum = a.ld_momentum;
-        p.decay = static_cast<float>(a.decay);
-        p.rest = static_cast<float>(1.0 - a.decay);
-        p.nesterov = a.nesterov;
+        p.shape = source_shape(a);
         const int lanes = lanes_for((a.cols + 7) / 8);
         const uint64_t tiles = ((a.rows + 63) / 64) * ((a.cols + 63) / 64);
         auto launch = [&](auto measure, auto lay_out) {
@@ -737,6 +645,7 @@ uint64_t orthogonalize_bytes(uint64_t count, uint64_t rows, uint64_t cols)
 
 hipError_t launch_orthogonalize(const OrthogonalizeArgs& a, char* ws, hipStream_t stream)
 {
+    if (is_small(a.rows, a.cols, a.steps)) return launch_orthogonalize_small(a, stream);
     const Layout l = layout_of(a.rows, a.cols, a.count);
     const uint64_t most = group_of(a.count, l, a.nranks);
     for (uint64_t first = 0; first < a.count; first += most) {

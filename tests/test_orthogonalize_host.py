@@ -115,6 +115,7 @@ def test_lists_of_matrices():
     assert list(p) == [x.data_ptr(), x.data_ptr() + 20] and ld == 10
     assert list(ar._matrices([64, 128], 12)[0]) == [64, 128] and ar._matrices([64], 12)[1] == 12
     assert ar._matrices([x[:, :4]], 12)[1] == 12 and ar._matrices([], 0)[1] == 0
+    assert list(ar._matrices([x, x[:, :4]], 12)[0]) == [x.data_ptr()] * 2
     with pytest.raises(ValueError):
         ar._matrices([x[:, :4], torch.zeros(6, 4)], 0)
     with pytest.raises(ValueError):
