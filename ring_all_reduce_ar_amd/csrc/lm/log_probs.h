@@ -128,14 +128,24 @@ struct LogProbOut {
     const float* target_logit;             // of the chunk
     float *log_probs, *entropy, *lse;      // of the call; entropy may be null
 
-    __device__ __forceinline__ float put(uint64_t t, const LogParts& s) const
+    // The target's logit, if it is not ignored: a kernel asks for it before
+    // the rest of its work, whose loads then hide these two.
+    struct Aim {
+        bool on;
+        float logit;
+    };
+    __device__ __forceinline__ Aim aim(uint64_t t) const
+    {
+        const bool on = load_target(targets, first_token + t, ignore, vocab) >= 0;
+        return Aim{on, on ? target_logit[t] : 0.0f};
+    }
+    __device__ __forceinline__ void put(uint64_t t, const LogParts& s, const Aim& aim) const
     {
         const uint64_t at = first_token + t;
         const float log_sum = logf(s.sum), l = s.top + log_sum;
         lse[at] = l;
-        log_probs[at] = load_target(targets, at, ignore, vocab) >= 0 ? target_logit[t] - l : 0.0f;
+        log_probs[at] = aim.on ? aim.logit - l : 0.0f;
         if (entropy) entropy[at] = log_sum - s.dot / s.sum;
-        return l;
     }
 };
 
@@ -148,7 +158,9 @@ __global__ __launch_bounds__(kJoinBlock) void join_log_probs(const LogParts* par
     const int x = threadIdx.x % X, y = threadIdx.x / X;
     const uint64_t t = static_cast<uint64_t>(blockIdx.x) * X + x;
     LogParts s{-INFINITY, 0.0f, 0.0f};
+    LogProbOut::Aim aim{};
     if (t < out.ntokens) {
+        if (y == 0) aim = out.aim(t);
 #pragma unroll 4
         for (uint64_t r = y; r < groups; r += Y) s = join_parts(s, parts[r * out.ntokens + t]);
     }
@@ -158,7 +170,7 @@ __global__ __launch_bounds__(kJoinBlock) void join_log_probs(const LogParts* par
         __syncthreads();
         if (y < h) part[y][x] = join_parts(part[y][x], part[y + h][x]);
     }
-    if (y == 0 && t < out.ntokens) out.put(t, part[0][x]);
+    if (y == 0 && t < out.ntokens) out.put(t, part[0][x], aim);
 }
 
 // ---------------------------------------------------------------------------
@@ -195,17 +207,38 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x)
     return __builtin_amdgcn_readlane(x, 63);
 }
 
-// The number of a wave's lanes whose key is above this lane's.
-__device__ __forceinline__ uint32_t rank_of(uint64_t key)
+// How many of the first `count` lanes' keys are above this lane's.
+__device__ __forceinline__ uint32_t rank_of(uint64_t key, uint32_t count)
 {
     uint32_t rank = 0;
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
+#pragma unroll 4
+    for (uint32_t i = 0; i < count; ++i) {
         const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(key >> 32, i))) << 32 |
                                static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(key), i));
         rank += other > key ? 1 : 0;
     }
     return rank;
+}
+
+// A value that at least `top` keys reach, from each lane's largest. Up to 8: the
+// least of the maxima of eight sets of lanes (of their upper halves), which about
+// 22 of 512 keys reach; more: the top-th largest.
+__device__ __forceinline__ uint64_t bound_of(uint64_t best, int top)
+{
+    if (top <= 8) {
+        uint32_t x = static_cast<uint32_t>(best >> 32);
+        auto step = [&](auto dpp) {
+            const uint32_t y = __builtin_amdgcn_mov_dpp(x, decltype(dpp)::value, 0xF, 0xF, true);
+            x = x > y ? x : y;
+        };
+        step(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+        step(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+        step(std::integral_constant<int, 0x141>{});  // the other four of eight
+        const uint32_t least = ~wave_max(~x);
+        return least ? static_cast<uint64_t>(least) << 32 : 1;
+    }
+    const uint64_t at_place = __ballot(best != 0 && rank_of(best, 64) == static_cast<uint32_t>(top - 1));
+    return at_place ? __shfl(best, __builtin_ctzll(at_place), 64) : 1;
 }
 
 // A wave's list of the `top` (at most 64) largest keys that it has met, lane l
@@ -216,10 +249,9 @@ struct TopList {
     uint64_t last = 0;   // the list's last key: what is not above it has no place
 
     // Keys of one batch (0: none), each met once. `room`: 64 keys in LDS of the
-    // wave's own. No key below the top-th largest of the lanes' largest ones has a
-    // place. Mostly the others are at most 64, one for each lane: they find their
-    // places by counting the larger ones. If not, places are filled one by one;
-    // 20 of 640 keys took 8 us so, the counting takes 1.5.
+    // wave's own. A bound from the lanes' largest keys mostly leaves at most 64, one
+    // for each lane, which find their places by counting the larger ones. If not,
+    // places are filled one by one; 20 of 640 keys took 8 us so.
     __device__ __forceinline__ void add(uint64_t (&key)[kTopBatch], int top, uint64_t* room)
     {
         const uint32_t lane = threadIdx.x & 63;
@@ -228,8 +260,11 @@ struct TopList {
         for (int i = 0; i < kTopBatch; ++i) best = key[i] > best ? key[i] : best;
         if (!__any(best > last)) return;
         best = mine > best ? mine : best;
-        const uint64_t at_place = __ballot(best != 0 && rank_of(best) == static_cast<uint32_t>(top - 1));
-        const uint64_t least = at_place ? __shfl(best, __builtin_ctzll(at_place), 64) : 1;
+        uint32_t all = static_cast<uint32_t>(__builtin_popcountll(__ballot(mine != 0)));
+#pragma unroll
+        for (int i = 0; i < kTopBatch; ++i) all += static_cast<uint32_t>(__builtin_popcountll(__ballot(key[i] != 0)));
+        uint64_t least = 1;
+        if (all > 64) least = bound_of(best, top);
         uint32_t count = 0;
         auto give = [&](uint64_t k) {
             const uint64_t in = __ballot(k >= least);
@@ -246,7 +281,7 @@ struct TopList {
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             const uint64_t one = lane < count ? room[lane] : 0;
-            const uint32_t place = rank_of(one);
+            const uint32_t place = rank_of(one, count);
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             if (lane < count && place < static_cast<uint32_t>(top)) room[place] = one;
@@ -305,15 +340,21 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
             list = TopList{};
             uint64_t key[kTopBatch] = {};
             static_assert(W <= kTopBatch, "one batch takes all lists");
+            // (the keys of a list in neighbouring lanes, so that every lane has large ones)
 #pragma unroll
-            for (int i = 0; i < W; ++i) key[i] = lists[i][lane];
+            for (int i = 0; i < W; ++i) {
+                const int e = i * 64 + lane;
+                if (e < W * top) key[i] = lists[e / top][e % top];
+            }
             list.add(key, top, rooms[wave]);
         }
     };
 
     TopList best;
     LogParts s{-INFINITY, 0.0f, 0.0f};
+    LogProbOut::Aim aim{};
     if (on) {
+        if (w == 0) aim = out.aim(t);
         for (uint64_t g0 = static_cast<uint64_t>(w) * 64 * kTopBatch; g0 < groups; g0 += W * 64 * kTopBatch) {
             // all loads first: within a branch each would be waited for by itself
             LogParts p[kTopBatch];
@@ -343,10 +384,12 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
     }
 
     TopList found;
-    if (on) {
+    // up to two batches take one wave no longer than a join of several waves' lists
+    const uint32_t per_batch = 64 * kTopBatch / group_rows;  // groups
+    const bool alone = W == 1 || static_cast<uint32_t>(top) <= 2 * per_batch;
+    if (on && (w == 0 || !alone)) {
         const uint64_t blocks = (n + 15) / 16;
-        const uint32_t per_batch = 64 * kTopBatch / group_rows;  // groups
-        for (uint32_t k0 = w * per_batch; k0 < static_cast<uint32_t>(top); k0 += W * per_batch) {
+        for (uint32_t k0 = w * per_batch; k0 < static_cast<uint32_t>(top); k0 += (alone ? 1 : W) * per_batch) {
             uint64_t key[kTopBatch];
             float z[kTopBatch];
             uint32_t ids[kTopBatch];
@@ -363,10 +406,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
             found.add(key, top, rooms[wave]);
         }
     }
-    join_lists(found);
+    if (!alone) join_lists(found);
     if (!on || w != 0) return;
     const float l = s.top + logf(s.sum);
-    if (lane == 0) out.put(t, s);
+    if (lane == 0) out.put(t, s, aim);
     if (lane < top) {
         const uint64_t at = (out.first_token + t) * top + lane;
         top_log_probs[at] = key_value(found.mine) - l;
