@@ -20,8 +20,7 @@
 #include <type_traits>
 #include <utility>
 
-#include "log_probs.h"
-#include "rows.h"
+#include "few_gradients.h"
 
 namespace ar {
 namespace lm {
@@ -741,13 +740,47 @@ struct Call {
                                a.ignore_index, a.vocab, a.ntokens, r, scale);
             const hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            return backward_by(LogProbD{a.lse, a.grad_entropy ? a.entropy : nullptr, r, a.scale}, 1.0f / kLogProbScale, r.g);
+            const LogProbD rule{a.lse, a.grad_entropy ? a.entropy : nullptr, r, a.scale};
+            return p.few ? backward_few(rule) : backward_by(rule, 1.0f / kLogProbScale, r.g);
         }
         hipLaunchKernelGGL(row_scale, dim3(1), dim3(1024), 0, s, a.grad_losses, a.targets, a.ignore_index, a.vocab,
                            a.ntokens, scale);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         return backward_by(LossD{a.lse, a.grad_losses}, 1.0f / kDScale, a.grad_losses);
+    }
+
+    hipError_t backward_few(const LogProbD& rule) const
+    {
+        float* d = reinterpret_cast<float*>(ws + p.d);
+        const char *x, *w;
+        uint64_t ldx, ldw;
+        hipError_t e = hidden(&x, &ldx);
+        if (e != hipSuccess) return e;
+        const uint64_t piece = p.pack_weight ? p.piece : most_tiles(a.ntokens, p.tile_n) * kTileM;
+        for (uint64_t v0 = 0; v0 < a.vocab; v0 += piece) {
+            const uint64_t rows = std::min(a.vocab - v0, piece);
+            if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
+            const FewDEpilogue epi{d, rule, a.targets, a.ignore_index, a.vocab, v0};
+            if constexpr (PARTS == 1) e = launch_gemm_few<T, 16>(logits_args(w, ldw, x, ldx, rows, a.ntokens), epi, s);
+            else e = hipErrorInvalidValue;  // few tokens are never in pieces
+            if (e != hipSuccess) return e;
+        }
+        FewArgs f{};
+        f.weight = a.weight;
+        f.hidden = a.hidden;
+        f.grad_weight = a.grad_weight;
+        f.partial = a.grad_hidden ? reinterpret_cast<float*>(ws + p.grad_hidden_acc) : nullptr;
+        f.d = d;
+        f.targets = a.targets;
+        f.ignore = a.ignore_index;
+        f.vocab = a.vocab;
+        f.ntokens = a.ntokens;
+        f.width = a.width;
+        f.ld_weight = a.ld_weight;
+        f.ld_hidden = a.ld_hidden;
+        f.ld_grad_weight = a.ld_grad_weight;
+        return launch_few_gradients<F>(f, p.splits, a.grad_hidden, a.ld_grad_hidden, s);
     }
 
     template <class Rule>
@@ -924,7 +957,8 @@ uint64_t cross_entropy_bytes(uint64_t ntokens, uint64_t vocab, uint64_t width, a
     constexpr uint64_t kRounds = 2 * kCUs * kTileM * 256 * 4;
     const uint64_t hidden_sum = ntokens * width * 4, weight_sum = v_pad * width * 4;
     return bytes + width * t_pad * ob + std::max(hidden_sum, std::min(hidden_sum * kMostSplits, kRounds)) +
-           std::min(weight_sum * kMostSplits, kRounds) + sizeof(RowScale) + (kind.log_probs ? ntokens * 12 + 256 : 0);
+           std::min(weight_sum * kMostSplits, kRounds) + sizeof(RowScale) +
+           (kind.log_probs ? ntokens * 12 + 4 * 256 + v_pad * kFewTokens * 4 + few_partial_bytes(vocab, width) : 0);
 }
 
 CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t width, ar_dtype_t dtype, HeadKind kind)
@@ -948,7 +982,8 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     most = std::min(most, most_tiles(ntokens, p.tile_n));
     most = most < 1 ? 1 : most > whole ? whole : most;
     p.splits = p.weight_splits = 1;
-    if (!backward) {
+    p.few = backward && kind.log_probs && ntokens && ntokens <= kFewTokens && width >= kFewWidth;
+    if (!backward || p.few) {
         const uint64_t pieces = (whole + most - 1) / most;
         p.piece = (whole + pieces - 1) / pieces * kTileM;
     } else {
@@ -992,6 +1027,12 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         p.stats = take(p.stat_rows * p.chunk * stats_bytes(kind));
         p.target_logit = take(p.chunk * 4);
         if (kind.top) p.logits = take(logit_bytes(p.chunk, round_up(vocab, kTileM)));
+    } else if (p.few) {
+        p.splits = static_cast<int>(few_parts(ntokens, vocab, width, f32));
+        p.d = take(vocab * kFewTokens * 4);
+        p.grad_hidden_acc = take(static_cast<uint64_t>(p.splits) * ntokens * width * 4);
+        p.row_scale = take(sizeof(RowScale));
+        p.row_gradients = take(ntokens * 12);
     } else {
         p.d = take(ntokens * p.piece * ob);
         p.dt = take(p.piece * p.t_pad * ob);

@@ -134,6 +134,15 @@ def test_strided_rows(comms, dtype, pitch, offset):  # noqa: F811
     check(comms, 130, 700, 128, dtype, 52, pitch=pitch, offset=offset, index="i32", top=3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,vocab,width,pitch,offset", [(1, 5, 8, 0, 0), (1, 3000, 513, 0, 1), (2, 700, 9, 3, 0), (4, 40_000, 64, 0, 0),
+                                                        (5, 333, 1100, 0, 0), (8, 1999, 260, 5, 3), (9, 64, 2056, 0, 0),
+                                                        (16, 9001, 77, 1, 0), (12, 31, 8, 8, 8)])
+def test_few_tokens(comms, dtype, n, vocab, width, pitch, offset):  # noqa: F811
+    """Both gradients in one pass over the weight, rows at any address."""
+    check(comms, n, vocab, width, dtype, 55, pitch=pitch, offset=offset, ignored=0.3)
+
+
 @pytest.mark.parametrize("ignored", [0.0, 0.5, 1.0])
 def test_ignored_tokens(comms, ignored):  # noqa: F811
     check(comms, 70, 400, 64, "bf16", 53, ignored=ignored, top=2)
