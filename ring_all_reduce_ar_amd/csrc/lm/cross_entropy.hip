@@ -982,7 +982,8 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
     most = std::min(most, most_tiles(ntokens, p.tile_n));
     most = most < 1 ? 1 : most > whole ? whole : most;
     p.splits = p.weight_splits = 1;
-    p.few = backward && kind.log_probs && ntokens && ntokens <= kFewTokens && width >= kFewWidth;
+    p.few = backward && kind.log_probs && ntokens && ntokens <= kFewTokens && width >= kFewWidth &&
+            width < (1u << 20);  // (column chunks are counted in 16 bits)
     if (!backward || p.few) {
         const uint64_t pieces = (whole + most - 1) / most;
         p.piece = (whole + pieces - 1) / pieces * kTileM;
