@@ -588,10 +588,28 @@ struct Call {
     char* ws;
     hipStream_t s;
 
+    // Whether the logits are made from the weight's rows as they lie, though not on
+    // 16 bytes. (The cross entropy lays them out: its results are as they were.)
+    bool by_rows() const
+    {
+        return PARTS == 1 && a.log_probs && (a.losses || p.few) && p.tile_n == 16 && p.pack_weight &&
+               rows_fit(a.width * EB);
+    }
+    template <class Epilogue>
+    hipError_t few_logits(GemmArgs g, const Epilogue& epi) const
+    {
+        if constexpr (PARTS == 1) {
+            if (!by_rows()) return launch_gemm_few<T, 16>(g, epi, s);
+            g.k_all = static_cast<uint32_t>(a.width);
+            return launch_gemm_rows<T>(g, epi, s);
+        }
+        return hipErrorInvalidValue;  // few tokens are never in pieces
+    }
+
     // The logits' operands, packed where the plan says so, and their pitch in bytes.
     hipError_t hidden(const char** out, uint64_t* ld) const
     {
-        if (!p.pack_hidden) {
+        if (!p.pack_hidden && !by_rows()) {
             *out = static_cast<const char*>(a.hidden);
             *ld = a.ld_hidden * EB;
             return hipSuccess;
@@ -603,7 +621,7 @@ struct Call {
     hipError_t weight(uint64_t v0, uint64_t rows, const char** out, uint64_t* ld) const
     {
         const char* from = static_cast<const char*>(a.weight) + v0 * a.ld_weight * EB;
-        if (!p.pack_weight) {
+        if (!p.pack_weight || by_rows()) {
             *out = from;
             *ld = a.ld_weight * EB;
             return hipSuccess;
@@ -693,7 +711,7 @@ struct Call {
         LogParts* parts = reinterpret_cast<LogParts*>(ws + p.stats);
         float* target_logit = reinterpret_cast<float*>(ws + p.target_logit);
         float* logits = a.top ? reinterpret_cast<float*>(ws + p.logits) : nullptr;
-        const uint64_t piece = p.pack_weight ? p.piece : most_tiles(p.chunk, p.tile_n) * kTileM;
+        const uint64_t piece = p.pack_weight && !by_rows() ? p.piece : most_tiles(p.chunk, p.tile_n) * kTileM;
         for (uint64_t t0 = 0; t0 < a.ntokens; t0 += p.chunk) {
             const uint64_t tokens = std::min(a.ntokens - t0, p.chunk);
             uint64_t row0 = 0;
@@ -702,9 +720,9 @@ struct Call {
                 if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
                 const LogPartsEpilogue epi{parts, target_logit, logits, a.targets, a.ignore_index, a.vocab, v0, row0,
                                            t0, a.scale};
-                if ((e = product<T, PARTS>(logits_args(w, ldw, x + t0 * ldx, ldx, rows, tokens), p.tile_n, epi, s)) !=
-                    hipSuccess)
-                    return e;
+                const GemmArgs g = logits_args(w, ldw, x + t0 * ldx, ldx, rows, tokens);
+                e = p.tile_n == 16 ? few_logits(g, epi) : product<T, PARTS>(g, p.tile_n, epi, s);
+                if (e != hipSuccess) return e;
                 row0 += stat_rows_of(rows, p.tile_n);
             }
             const LogProbOut out{a.targets, a.ignore_index, a.vocab, t0, tokens, target_logit, a.losses, a.entropy, a.lse};
@@ -757,14 +775,12 @@ struct Call {
         uint64_t ldx, ldw;
         hipError_t e = hidden(&x, &ldx);
         if (e != hipSuccess) return e;
-        const uint64_t piece = p.pack_weight ? p.piece : most_tiles(a.ntokens, p.tile_n) * kTileM;
+        const uint64_t piece = p.pack_weight && !by_rows() ? p.piece : most_tiles(a.ntokens, p.tile_n) * kTileM;
         for (uint64_t v0 = 0; v0 < a.vocab; v0 += piece) {
             const uint64_t rows = std::min(a.vocab - v0, piece);
             if ((e = weight(v0, rows, &w, &ldw)) != hipSuccess) return e;
             const FewDEpilogue epi{d, rule, a.targets, a.ignore_index, a.vocab, v0};
-            if constexpr (PARTS == 1) e = launch_gemm_few<T, 16>(logits_args(w, ldw, x, ldx, rows, a.ntokens), epi, s);
-            else e = hipErrorInvalidValue;  // few tokens are never in pieces
-            if (e != hipSuccess) return e;
+            if ((e = few_logits(logits_args(w, ldw, x, ldx, rows, a.ntokens), epi)) != hipSuccess) return e;
         }
         FewArgs f{};
         f.weight = a.weight;

@@ -5,9 +5,11 @@
 // With so few tokens each element of W takes part in a few sums only: the time is
 // that of reading W and writing dW once, which one pass over the rows v does, with
 // the tokens' rows of X and of dX's sums in registers and d[.][v] in scalar ones.
-// The matrix cores would want W transposed (read, written and read again) and d in
-// 16 bits; here d is fp32. 3 tokens x 88513 x 1157 bf16, forward and gradients: XXX us
-// by the products, XXX so.
+// The matrix cores would want W transposed (read, written and read again) and d
+// in 16 bits; here d is fp32. Forward and gradients by the products and so, us: 1
+// token x 32000 x 4096 bf16 376 / 214, 8 of them 385 / 237, 16 383 / 312. From 8 tokens on
+// the pass is bound by its sums (16: 128 of them for 8 bytes of W), up to 4 by HBM,
+// 6.0 TB/s.
 #pragma once
 
 #include "log_probs.h"

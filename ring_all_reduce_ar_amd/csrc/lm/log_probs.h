@@ -21,6 +21,93 @@ namespace lm {
 namespace {
 
 // ---------------------------------------------------------------------------
+// logits of few tokens from rows at any address
+// ---------------------------------------------------------------------------
+// Direct loads to LDS want rows on 16 bytes. For up to 16 tokens a row of A is one
+// wave's alone and need not go through LDS: each lane loads its fragments, 16 bytes
+// at an element's alignment, kRowsAhead of them under way, and only the tokens'
+// rows, laid out as gemm_few has them, lie in LDS, all of their depth (which bounds
+// it). Laying the weight out first moves it three times: forward, us, by that and so,
+// 3 tokens x 88513 x 1157 bf16 149 / 75 (this kernel 66, 3.1 TB/s), 16 x 50000 x 3001
+// fp16 with 5 alternatives 239 / 152, 1 x 131072 x 999 fp32 437 / 102.
+constexpr int kRowsThreads = 512, kRowsAhead = 8;
+constexpr uint32_t kRowsLds = 144 * 1024;
+
+// The tokens' rows in LDS, 16 bytes apart from whole 128s.
+__host__ __device__ constexpr uint64_t rows_pitch(uint64_t depth_bytes) { return (depth_bytes + 127) / 128 * 128 + 16; }
+constexpr bool rows_fit(uint64_t depth_bytes) { return 16 * rows_pitch(depth_bytes) <= kRowsLds; }
+
+// g.k_all: the width; g.b: rows of whole 128-byte steps, zeros behind the width.
+template <class T, class Epilogue>
+__global__ __launch_bounds__(kRowsThreads) void gemm_rows(const GemmArgs g, const Epilogue epi)
+{
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr uint32_t EB = sizeof(typename T::Elem), kEach = 16 / EB;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t bytes = g.k_all * EB, steps = bytes / 64, pitch = static_cast<uint32_t>(rows_pitch(bytes));
+    const uint32_t chunks = (bytes + 127) / 128 * 8;
+    for (uint32_t i = threadIdx.x; i < 16 * chunks; i += kRowsThreads) {
+        const uint32_t row = i / chunks, at = i % chunks * 16;
+        const u32x4 none = {0, 0, 0, 0};
+        *reinterpret_cast<u32x4*>(lds + row * pitch + at) =
+            row < g.n ? *reinterpret_cast<const u32x4*>(g.b + row * g.ldb + at) : none;
+    }
+    __syncthreads();
+
+    // two tiles of 64 rows a workgroup, as gemm_few numbers them
+    const uint32_t tm = blockIdx.x * 2 + (wave >> 2), m0 = tm * kFewM + (wave & 3) * 16;
+    const uint32_t row = min(m0 + (lane & 15), g.m - 1), col = (lane >> 4) * 16;
+    const char *a = g.a + row * g.lda, *b = lds + (lane & 15) * pitch + col;
+    auto load = [&](uint32_t step) {
+        i32x4 v;
+        __builtin_memcpy(&v, a + min(step, steps - 1) * 64 + col, 16);
+        return v;
+    };
+    Tile<1, 1> acc;
+    acc.v[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](i32x4 x, uint32_t step) {
+        const i32x4 y = *reinterpret_cast<const i32x4*>(b + step * 64);
+        acc.v[0][0] = T::mma(__builtin_bit_cast(typename T::Frag, x), __builtin_bit_cast(typename T::Frag, y), acc.v[0][0]);
+    };
+    if (steps) {
+        i32x4 f[kRowsAhead];
+#pragma unroll
+        for (int i = 0; i < kRowsAhead; ++i) f[i] = load(i);
+        uint32_t k = 0;
+        for (; k + kRowsAhead <= steps; k += kRowsAhead)
+#pragma unroll
+            for (int i = 0; i < kRowsAhead; ++i) {
+                const i32x4 x = f[i];
+                f[i] = load(k + i + kRowsAhead);
+                multiply(x, k + i);
+            }
+#pragma unroll
+        for (int i = 0; i < kRowsAhead; ++i)
+            if (k + i < steps) multiply(f[i], k + i);
+    }
+    if (steps * 64 < bytes) {  // what is left of the rows
+        typename T::Elem x[kEach] = {};
+        const uint32_t at = steps * 64 + col;
+#pragma unroll
+        for (uint32_t e = 0; e < kEach; ++e)
+            if (at + e * EB < bytes) __builtin_memcpy(&x[e], a + at + e * EB, EB);
+        i32x4 v;
+        __builtin_memcpy(&v, x, 16);
+        multiply(v, steps);
+    }
+    if (tm < g.tiles_m) epi(acc, m0, 0, g, tm * 4 + (wave & 3), 0, NoStaging{});
+}
+
+template <class T, class Epilogue>
+hipError_t launch_gemm_rows(GemmArgs g, const Epilogue& epi, hipStream_t stream)
+{
+    g.tiles_m = (g.m + kFewM - 1) / kFewM;
+    const uint32_t lds = static_cast<uint32_t>(16 * rows_pitch(g.k_all * sizeof(typename T::Elem)));
+    hipLaunchKernelGGL((gemm_rows<T, Epilogue>), dim3((g.tiles_m + 1) / 2), dim3(kRowsThreads), lds, stream, g, epi);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 struct LogParts {

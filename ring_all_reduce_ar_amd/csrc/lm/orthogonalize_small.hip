@@ -3,7 +3,7 @@
 // A launch for each of the 15 products of five steps takes 4 us whatever its
 // size. Here a workgroup has a matrix for itself: X by rows and by columns, D and
 // the bracket lie in LDS as pairs of fp16 numbers, the sum of squares is its own,
-// and barriers part the products. 4 x 64 x 192 fp32 in XXX us rather than 72.
+// and barriers part the products. 4 x 64 x 192 fp32 in 38 us rather than 72.
 #include <cmath>
 
 #include "orthogonalize.h"

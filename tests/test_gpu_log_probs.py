@@ -143,6 +143,14 @@ def test_few_tokens(comms, dtype, n, vocab, width, pitch, offset):  # noqa: F811
     check(comms, n, vocab, width, dtype, 55, pitch=pitch, offset=offset, ignored=0.3)
 
 
+# widths whose tokens' rows just fit a workgroup's shared memory and do not, and no 16 bytes
+@pytest.mark.parametrize("n,vocab,width,dtype,pitch", [(16, 130, 4543, "bf16", 0), (15, 67, 4609, "f16", 0),
+                                                       (3, 64, 2271, "f32", 2), (2, 65, 2305, "f32", 0), (7, 200, 37, "f32", 1),
+                                                       (1, 193, 31, "f16", 0), (13, 1, 517, "bf16", 0)])
+def test_few_tokens_odd_rows(comms, n, vocab, width, dtype, pitch):  # noqa: F811
+    check(comms, n, vocab, width, dtype, 56, pitch=pitch, top=min(vocab, 4), ignored=0.2)
+
+
 @pytest.mark.parametrize("ignored", [0.0, 0.5, 1.0])
 def test_ignored_tokens(comms, ignored):  # noqa: F811
     check(comms, 70, 400, 64, "bf16", 53, ignored=ignored, top=2)
