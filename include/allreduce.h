@@ -503,7 +503,8 @@ ar_result_t ar_orthogonalize(ar_comm_t comm, int nmatrices, const void* const in
  * with X the orthogonalised U as above, in fp32. grads (dtype), momentum (fp32)
  * and weights_in are one buffer a matrix; weights_out[t*nranks + r] is rank r's
  * replica, all of which get the same. weights_in and weights_out are of
- * weight_dtype: dtype or fp32. decay: in [0, 1). In place is allowed for the
+ * weight_dtype: dtype or fp32. decay: in [0, 1); lr, weight_decay, update_scale
+ * and their products with lr are finite in fp32. In place is allowed for the
  * momentum (momentum_in[t] == momentum_out[t]) and for the weights (one of a
  * matrix's replicas == weights_in[t]). */
 ar_result_t ar_muon_update(ar_comm_t comm, int nmatrices, const void* const grads[], const float* const momentum_in[],

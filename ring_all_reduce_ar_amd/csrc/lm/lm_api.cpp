@@ -956,8 +956,11 @@ AR_EXPORT ar_result_t ar_muon_update(ar_comm_t comm, int nmatrices, const void* 
         if (weight_dtype != dtype && weight_dtype != AR_FLOAT32)
             return fail(AR_ERR_UNSUPPORTED, "weight_dtype is dtype or fp32");
         if (!(decay >= 0.0 && decay < 1.0)) return fail(AR_ERR_INVALID_ARGUMENT, "decay %g is outside 0..1", decay);
-        if (!std::isfinite(lr) || !std::isfinite(weight_decay) || !std::isfinite(update_scale))
-            return fail(AR_ERR_INVALID_ARGUMENT, "lr, weight_decay and update_scale are finite numbers");
+        // (as the kernels hold them: an infinite factor would make NaN of a zero)
+        for (const double x : {lr, weight_decay, update_scale, lr * update_scale, 1.0 - lr * weight_decay})
+            if (!std::isfinite(static_cast<float>(x)))
+                return fail(AR_ERR_INVALID_ARGUMENT,
+                            "lr, weight_decay, update_scale and their products are finite numbers of fp32");
         if (nmatrices > 0 && (!grads || !momentum_in || !momentum_out || !weights_in || !weights_out))
             return fail(AR_ERR_INVALID_ARGUMENT, "NULL array of matrices");
         if (nmatrices == 0 || rows == 0 || cols == 0) return AR_SUCCESS;

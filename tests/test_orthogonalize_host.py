@@ -77,6 +77,9 @@ def test_update_refusals():
     for k in ("lr", "weight_decay", "update_scale"):
         call(BAD, **{k: float("inf")})
         call(BAD, **{k: float("nan")})
+        call(BAD, **{k: 1e39})
+    call(BAD, lr=1e20, update_scale=1e20)
+    call(BAD, lr=-1e20, weight_decay=1e20)
     call(BAD, steps=0)
     call(BAD, eps=0.0)
     for k in ("g", "mi", "mo", "wi"):
