@@ -354,18 +354,63 @@ def test_gradients_of_nothing_and_almost_nothing(comms, tiny):  # noqa: F811
         assert (gx[::2] == 0).all() and (gx[1::2] != 0).any()
 
 
+@pytest.mark.parametrize("n", [6, 40])
+def test_gradients_of_ignored_tokens_may_be_anything(comms, n):  # noqa: F811
+    vocab, width = 300, 72
+    x, w, y, a = loss_inputs(n, vocab, width, "bf16", 69, ignored=0.5)
+    y[0] = 5
+    kept = (y != 5) & (y >= 0) & (y < vocab)
+    comm = comms(1, workspace(n, vocab, width, "bf16"))
+    got = forward(comm, x, w, y, n, vocab, width, "bf16")
+    b = 0.5 * a
+
+    def backward():
+        gx, gw = nan_like(n, width, dtype="bf16"), nan_like(vocab, width, dtype="bf16")
+        ar.ar_linear_log_probs_backward(comm, x, w, y, got["lse"], got["entropy"], a, b, gx, gw, n, vocab, width, "bf16",
+                                        ignore_index=5)
+        return gx, gw
+
+    want = backward()
+    assert (want[0][~kept] == 0).all() and torch.isfinite(want[1].float()).all()
+    a[~kept], b[~kept] = float("nan"), float("inf")
+    got["lse"][~kept], got["entropy"][~kept] = float("nan"), float("inf")
+    assert all(torch.equal(s, t) for s, t in zip(backward(), want))
+
+
+def test_rows_past_32_bits(comms):  # noqa: F811
+    """Rows of the weight and of its gradient whose offsets pass 2^32 bytes, on 16
+    bytes and not, of few tokens and of many."""
+    vocab, width, step = 2305, 40, 1 << 20
+    base, grad = (torch.empty(vocab * step, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for n, offset, pitch in ((3, 0, step), (2, 1, step - 1), (40, 0, step), (40, 1, step - 1)):
+        w = base.as_strided((vocab, width), (pitch, 1), offset)
+        gw = grad.as_strided((vocab, width), (pitch, 1), offset)
+        x, w0, y, a = loss_inputs(n, vocab, width, "bf16", 74, ignored=0.0)
+        w.copy_(w0)
+        comm = comms(1, workspace(n, vocab, width, "bf16", 4))
+        near, far = (forward(comm, x, m, y, n, vocab, width, "bf16", 4, ignore=-100) for m in (w0, w))
+        check_forward(far, head_ref(x, w0, y, -100, 1.0))
+        assert torch.equal(near["ids"], far["ids"])
+        gx, want = nan_like(n, width, dtype="bf16"), nan_like(vocab, width, dtype="bf16")
+        for m, out in ((w0, want), (w, gw)):
+            ar.ar_linear_log_probs_backward(comm, x, m, y, near["lse"], near["entropy"], a, a, gx, out, n, vocab, width, "bf16")
+        # sums of other orders: one rounding of the logits apart, twice
+        scale = want.double().abs().max()
+        assert float((gw.double() - want.double()).abs().max()) <= float(scale) * 2 * U["bf16"]
+
+
 # ---------------------------------------------------------------------------
 # streams and graphs
 # ---------------------------------------------------------------------------
-def test_on_another_stream_and_in_a_graph(comms):  # noqa: F811
+@pytest.mark.parametrize("n,vocab,width,top", [(600, 900, 64, 5), (4, 5000, 100, 20), (9, 700, 77, 0)])
+def test_on_another_stream_and_in_a_graph(comms, n, vocab, width, top):  # noqa: F811
     """A policy-gradient step captured and replayed between eager work, each
     replay against the eager result on the same inputs."""
-    n, vocab, width, top = 600, 900, 64, 5
     comm = comms(1, workspace(n, vocab, width, "bf16", top))
     x, w, y, a = loss_inputs(n, vocab, width, "bf16", 68)
     b = torch.full((n,), -0.01 / n, device="cuda")
     out = {k: nan_like(n, dtype="f32") for k in ("log_probs", "entropy", "lse")}
-    out |= {"top": nan_like(n, top, dtype="f32"), "ids": torch.zeros(n, top, dtype=torch.int32, device="cuda"),
+    out |= {"top": nan_like(n, max(top, 1), dtype="f32"), "ids": torch.zeros(n, max(top, 1), dtype=torch.int32, device="cuda"),
             "gx": torch.empty_like(x), "gw": torch.empty_like(w)}
 
     def step(stream):

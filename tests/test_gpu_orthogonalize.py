@@ -199,6 +199,20 @@ def test_in_place_and_nothing(comms):  # noqa: F811
     ar.ar_orthogonalize(comm, [0], [0], 0, 4, "f32")
 
 
+def test_rows_past_32_bits(comms):  # noqa: F811
+    """Rows whose offsets pass 2^32 bytes give what the same rows on end give."""
+    for rows, cols, pitch in ((70, 30, 1 << 24), (300, 130, 1 << 22)):
+        comm = workspace(comms, 1, rows, cols)
+        near = matrices(8, 1, rows, cols, "f32")[0]
+        big = torch.empty(2 * rows * pitch, device="cuda")
+        far, out = (big.as_strided((rows, cols), (pitch, 1), k * rows * pitch + 1) for k in range(2))
+        far.copy_(near)
+        want = torch.empty_like(near)
+        ar.ar_orthogonalize(comm, [near], [want], rows, cols, "f32")
+        ar.ar_orthogonalize(comm, [far], [out], rows, cols, "f32")
+        assert torch.equal(out, want)
+
+
 # ---------------------------------------------------------------------------
 # the update of weights
 # ---------------------------------------------------------------------------
@@ -274,10 +288,11 @@ def test_update_of_large_tiles(comms):  # noqa: F811
 # ---------------------------------------------------------------------------
 # streams and graphs
 # ---------------------------------------------------------------------------
-def test_on_another_stream_and_in_a_graph(comms):  # noqa: F811
+@pytest.mark.parametrize("rows,cols,count", [(96, 160, 3), (64, 100, 3), (600, 1100, 2)])
+def test_on_another_stream_and_in_a_graph(comms, rows, cols, count):  # noqa: F811
     """Averaged, clipped and applied in place: three steps of a captured graph
     between eager work, each against the eager steps."""
-    rows, cols, ranks, count = 96, 160, 2, 3
+    ranks = 2
     comm = comms(ranks, max(ar.ar_orthogonalize_workspace_bytes(count, rows, cols), ar.ar_clip_workspace_bytes()))
     grads = [matrices(20 + r, count, rows, cols, "bf16") for r in range(ranks)]
     grads = [[grads[r][t].contiguous() for r in range(ranks)] for t in range(count)]
