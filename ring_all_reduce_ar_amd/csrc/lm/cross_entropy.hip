@@ -881,6 +881,7 @@ struct Shape {
     uint64_t weight_m, weight_n;      // and of the weight gradient's
     uint64_t step;
     bool pieces;
+    bool log_probs;
 };
 
 uint64_t up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
@@ -918,9 +919,39 @@ double split_cost(uint64_t tiles, uint64_t depth, uint64_t step, double join, in
     return best;
 }
 
+// The same for the gradients of log probabilities, with any number of parts, and
+// parts that cost what their `bytes` take to be written and read (and a load's
+// latency, of which several are under way). Few tiles of few results take parts
+// that fill no round: forward and gradients, us, by split_cost / so, of 3971 tokens x
+// 1551 x 64 bf16, whose weight gradient has 7 tiles, 154 / 82, of 2877 x 624 x 326 129 / 95, of
+// 600 x 8000 x 256 202 / 91, of 1021 x 32000 x 1024 fp16 341 / 341.
+double parts_cost(uint64_t tiles, uint64_t depth, uint64_t step, double join, uint64_t bytes, int* splits)
+{
+    constexpr double kBytesAStep = 2.5e6;  // 0.85 us at 3 TB/s
+    double best = 0;
+    for (const uint64_t k : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+        if (k > 1 && (k > kMostSplits || tiles * k > 2 * kCUs || depth < k * 128)) break;
+        const double c = static_cast<double>(up(tiles * k, kCUs) * (up(up(depth, step), k) + 8)) +
+                         (k > 1 ? k * (0.25 + 2 * static_cast<double>(bytes) / kBytesAStep) + join : 0.0);
+        if (best == 0 || c < best) {
+            best = c;
+            *splits = static_cast<int>(k);
+        }
+    }
+    return best;
+}
+
 double piece_cost(const Shape& x, uint64_t rows, int* splits, int* weight_splits)
 {
-    return static_cast<double>(up(up(rows, x.tile_m) * up(x.ntokens, x.tile_n), kCUs) * (up(x.width, x.step) + 8)) +
+    const double logits =
+        static_cast<double>(up(up(rows, x.tile_m) * up(x.ntokens, x.tile_n), kCUs) * (up(x.width, x.step) + 8));
+    if (x.log_probs)
+        return logits +
+               parts_cost(gradient_tiles(x, x.ntokens, x.tile_m, x.tile_n), rows, x.step, 0, x.ntokens * x.width * 4, splits) +
+               parts_cost(gradient_tiles(x, rows, x.weight_m, x.weight_n), x.ntokens, x.step, 8, rows * x.width * 4,
+                          weight_splits) +
+               24;
+    return logits +
            split_cost(gradient_tiles(x, x.ntokens, x.tile_m, x.tile_n), rows, x.step, 0, splits) +
            split_cost(gradient_tiles(x, rows, x.weight_m, x.weight_n), x.ntokens, x.step, 8, weight_splits) +
            24;  // four launches
@@ -1009,8 +1040,8 @@ CrossEntropyPlan plan_cross_entropy(uint64_t ntokens, uint64_t vocab, uint64_t w
         // five rounds for 9.9, 2 and 4.9; of 13312 rows the weight gradient's 832
         // take four for 3.25.
         const uint64_t tile_m = small ? kFewM : kTileM, tile_n = static_cast<uint64_t>(p.tile_n);
-        const Shape shape = f32 ? Shape{ntokens, width, tile_m, tile_n, tile_m, small ? 64u : tile_n, step, p.pieces}
-                                : Shape{ntokens, width, tile_m, tile_n, kTileM, 256, step, false};
+        const Shape shape = f32 ? Shape{ntokens, width, tile_m, tile_n, tile_m, small ? 64u : tile_n, step, p.pieces, kind.log_probs}
+                                : Shape{ntokens, width, tile_m, tile_n, kTileM, 256, step, false, kind.log_probs};
         double best = 0;
         const uint64_t stride = most / 64 + 1;
         for (uint64_t m = most; m >= (most + 1) / 2 && m >= 1; m = m > stride ? m - stride : 0) {
