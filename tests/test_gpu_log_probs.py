@@ -225,6 +225,14 @@ def test_alternatives_of_many_groups(comms):  # noqa: F811
     check_top(comms, 520, 150_001, 16, "bf16", 20)
 
 
+def test_alternatives_of_the_largest_vocabulary(comms):  # noqa: F811
+    check_top(comms, 2, (1 << 24) - 1, 8, "bf16", 64)
+
+
+def test_many_tokens_of_a_small_vocabulary(comms):  # noqa: F811
+    check(comms, 70_001, 37, 16, "f16", 57, top=3)
+
+
 @pytest.mark.parametrize("dtype,n", [("f32", 3), ("f32", 300), ("bf16", 3), ("f16", 700)])
 def test_masked_rows(comms, dtype, n):  # noqa: F811
     """Rows of the vocabulary masked by -infinity: probability 0, no part in the

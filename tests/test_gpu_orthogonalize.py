@@ -109,6 +109,12 @@ def test_matrices(comms, dtype, rows, cols):  # noqa: F811
     check(comms, 3, rows, cols, dtype)
 
 
+@pytest.mark.parametrize("rows,cols,dtype", [(1, 1_000_003, "f32"), (3, 600_001, "bf16"), (700_001, 2, "f16"),
+                                             ((1 << 20) - 1, 1, "f32")])
+def test_long_and_thin(comms, rows, cols, dtype):  # noqa: F811
+    check(comms, 2, rows, cols, dtype, seed=3)
+
+
 @pytest.mark.parametrize("count,rows,cols,dtype", [(1, 1500, 1700, "f32"), (2, 2100, 1030, "bf16"), (20, 520, 640, "f32"),
                                                    (70, 130, 90, "bf16"), (40, 64, 64, "f16")])
 def test_large_tiles_and_groups(comms, count, rows, cols, dtype):  # noqa: F811
