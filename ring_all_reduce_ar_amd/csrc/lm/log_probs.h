@@ -294,15 +294,18 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x)
     return __builtin_amdgcn_readlane(x, 63);
 }
 
-// How many of the first `count` lanes' keys are above this lane's.
+// How many of the first `count` lanes' keys are above this lane's; the others' are 0.
 __device__ __forceinline__ uint32_t rank_of(uint64_t key, uint32_t count)
 {
     uint32_t rank = 0;
-#pragma unroll 4
-    for (uint32_t i = 0; i < count; ++i) {
+    auto above = [&](uint32_t i) {
         const uint64_t other = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(key >> 32, i))) << 32 |
                                static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<uint32_t>(key), i));
         rank += other > key ? 1 : 0;
+    };
+    for (uint32_t i = 0; i < count; i += 8) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) above(i + k);
     }
     return rank;
 }
