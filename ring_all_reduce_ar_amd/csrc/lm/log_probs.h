@@ -479,20 +479,28 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
     const bool alone = W == 1 || static_cast<uint32_t>(top) <= 2 * per_batch;
     if (on && (w == 0 || !alone)) {
         const uint64_t blocks = (n + 15) / 16;
-        for (uint32_t k0 = w * per_batch; k0 < static_cast<uint32_t>(top); k0 += (alone ? 1 : W) * per_batch) {
-            uint64_t key[kTopBatch];
+        struct Batch {
             float z[kTopBatch];
             uint32_t ids[kTopBatch];
+        };
+        auto load = [&](uint32_t k0, Batch& x) {
 #pragma unroll
             for (int i = 0; i < kTopBatch; ++i) {
                 const uint32_t e = i * 64 + lane, k = k0 + e / group_rows, row = e % group_rows;
                 const uint64_t group = __shfl(best.mine, k & 63, 64);
                 const bool in = k < static_cast<uint32_t>(top) && group != 0;
-                ids[i] = in ? key_id(group) * group_rows + row : UINT32_MAX;
-                z[i] = logits[in ? logit_at(key_id(group), blocks, t, group_rows / 16, row) : 0];
+                x.ids[i] = in ? key_id(group) * group_rows + row : UINT32_MAX;
+                x.z[i] = logits[in ? logit_at(key_id(group), blocks, t, group_rows / 16, row) : 0];
             }
+        };
+        const uint32_t stride = (alone ? 1 : W) * per_batch;
+        Batch x;
+        load(w * per_batch, x);
+        for (uint32_t k0 = w * per_batch; k0 < static_cast<uint32_t>(top); k0 += stride) {
+            uint64_t key[kTopBatch];
 #pragma unroll
-            for (int i = 0; i < kTopBatch; ++i) key[i] = ids[i] < out.vocab ? order_key(z[i], ids[i]) : 0;
+            for (int i = 0; i < kTopBatch; ++i) key[i] = x.ids[i] < out.vocab ? order_key(x.z[i], x.ids[i]) : 0;
+            if (k0 + stride < static_cast<uint32_t>(top)) load(k0 + stride, x);  // under way meanwhile
             found.add(key, top, rooms[wave]);
         }
     }
