@@ -174,14 +174,16 @@ __global__ __launch_bounds__(256) void few_gradients(const FewArgs p)
 }
 
 // grad_hidden from the parts: a workgroup has 64 columns of a token, its waves
-// every fourth part.
+// every fourth part. An ignored token's is 0, whatever its parts hold: its d is 0,
+// but 0 times an infinity or a NaN of the weight is NaN.
 template <class F>
-__global__ __launch_bounds__(256) void join_few(const float* partial, uint64_t parts, uint64_t ntokens, uint64_t width,
-                                                void* out, uint64_t ld)
+__global__ __launch_bounds__(256) void join_few(const float* partial, uint64_t parts, Indices targets, int64_t ignore,
+                                                uint64_t vocab, uint64_t ntokens, uint64_t width, void* out, uint64_t ld)
 {
     __shared__ float sums[4][64];
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t c = static_cast<uint64_t>(blockIdx.x) * 64 + lane, t = blockIdx.y;
+    const bool on = load_target(targets, t, ignore, vocab) >= 0;
     float s = 0.0f;
     if (c < width) {
 #pragma unroll 8
@@ -189,7 +191,8 @@ __global__ __launch_bounds__(256) void join_few(const float* partial, uint64_t p
     }
     sums[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && c < width) F::st(out, t * ld + c, (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]));
+    if (wave == 0 && c < width)
+        F::st(out, t * ld + c, on ? (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]) : 0.0f);
 }
 
 // Columns of a thread: as many as its registers take beside the tokens' rows, with
@@ -226,7 +229,8 @@ hipError_t launch_few_gradients(FewArgs p, uint64_t parts, void* grad_hidden, ui
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.partial) return e;
     hipLaunchKernelGGL((join_few<F>), dim3(static_cast<uint32_t>((p.width + 63) / 64), static_cast<uint32_t>(p.ntokens)),
-                       dim3(256), 0, s, p.partial, parts, p.ntokens, p.width, grad_hidden, ld_grad_hidden);
+                       dim3(256), 0, s, p.partial, parts, p.targets, p.ignore, p.vocab, p.ntokens, p.width, grad_hidden,
+                       ld_grad_hidden);
     return hipGetLastError();
 }
 
