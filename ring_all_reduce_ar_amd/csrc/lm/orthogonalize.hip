@@ -14,8 +14,8 @@
 // These products are of the smaller side alone and symmetric: a segment of k
 // steps costs m^2 (n + (4k - 3) m + 2n) products (of half of a symmetric result)
 // where steps by themselves take k m^2 (3n + m). Errors of A for small singular
-// values grow with a^2 a step there, in X with a: five steps on end lose a digit
-// against fp32, segments of three and two are as exact as steps by themselves.
+// values grow with a^2 a step there, in X with a, which bounds a segment's length
+// (segment_size): the default's five steps go as three and two.
 //
 // Small singular values grow by a factor of a in each step (485 in five of them),
 // and what a rounding adds to X grows alike: in bf16, results are off by 4-30%, in
@@ -272,6 +272,7 @@ struct UpdateEpilogue {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kCUs = 256;
 constexpr int kSegment = 3;  // steps
+constexpr double kMostGrowth = 144.0, kLateGrowth = 16.0;  // of errors of A in one
 
 // How a product goes through its tiles: of which size, and in how many parts
 // those behind the last full round of workgroups are split.
@@ -529,9 +530,7 @@ struct Group {
         double top = 1.0;  // of the singular values
         int turn = 0;      // which of xt holds X
         for (int k = 0; k < a.steps;) {
-            // segments of up to three steps, the longer ones first
-            const int left = a.steps - k, count_left = (left + kSegment - 1) / kSegment;
-            const int size = l.segments ? (left + count_left - 1) / count_left : 1;
+            const int size = l.segments ? segment_size(k) : 1;
             const char* p;
             double p_scale;
             if ((e = segment(x, square, k, size, &top, &p, &p_scale)) != hipSuccess) return e;
@@ -556,6 +555,31 @@ struct Group {
             turn ^= 1;
         }
         return hipSuccess;  // not reached: there is at least one step
+    }
+
+    // The steps of the segment that starts with step k, up to three. In a segment an
+    // error of A grows with a^2 a step but for the last, whose bracket takes it over.
+    // The rounding of X at the segment's start, which steps by themselves have too,
+    // grows with a in every step to come: the former may grow no more than that, nor
+    // by more than kMostGrowth, or kLateGrowth behind the first segment, where A has the
+    // size 1 whatever the matrix was and much of it has yet to grow. Largest errors of
+    // 30 kinds of singular values as multiples of those of fp32 products (where either
+    // is above 1e-6 of the result), 5 of 770 x 3000, in segments of three whatever the
+    // growth / so / by steps: 3 steps of the default 9.8 / 2.8 / 2.6, 4 steps 8.0 / 4.1 /
+    // 1.7, 5 steps 2.1 / 2.1 / 1.6, 8 steps 24 / 1.6 / 1.6, 5 steps of (8.3, -24, 17), (4.1,
+    // -2.9, 0.5) .. 17 / 2.4 / 1.6, the first 3 of them 53 / 4.0 / 2.7.
+    int segment_size(int k) const
+    {
+        auto growth = [&](int from, int to) {
+            double g = 1.0;
+            for (int i = from; i < to; ++i) g *= std::max(1.0, std::fabs(a.coefficients[3 * i]));
+            return g;
+        };
+        const double all = growth(k, a.steps) * 1.001;  // (equal products, in whatever order, are not more)
+        const double most = std::min(all, k ? kLateGrowth : kMostGrowth);
+        int size = std::min(a.steps - k, kSegment);
+        while (size > 1 && std::pow(growth(k, k + size - 1), 2) > most) --size;
+        return size;
     }
 
     // Steps k .. k + size - 1 of X's rows `x`: *p is the product of their brackets,
