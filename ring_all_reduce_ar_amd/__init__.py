@@ -508,6 +508,19 @@ def ar_linear_cross_entropy_backward(comm, hidden, weight, targets, lse, grad_lo
            "ar_linear_cross_entropy_backward")
 
 
+_TENSOR_TYPES = {AR_FLOAT32: torch.float32, AR_FLOAT16: torch.float16, AR_BFLOAT16: torch.bfloat16}
+
+
+def _typed(code: int, **bufs):
+    """Tensors (alone or in lists) hold what the call takes them for: memory of
+    another type would be read and written past its end."""
+    want = _TENSOR_TYPES.get(code)  # (a type that is none is refused with the call)
+    for what, some in bufs.items():
+        for b in some if isinstance(some, (list, tuple)) else (some,):
+            if want is not None and getattr(b, "dtype", want) != want:
+                raise TypeError(f"{what}: the call takes {want}, not {b.dtype}")
+
+
 def ar_linear_log_probs_workspace_bytes(ntokens: int, vocab: int, width: int, dtype, top: int = 0,
                                         backward: bool = False) -> int:
     return _check_size(_lib.ar_linear_log_probs_workspace_bytes(ntokens, vocab, width,
@@ -522,6 +535,9 @@ def ar_linear_log_probs(comm, hidden, weight, targets, log_probs, entropy, lse, 
     """log_probs[t] = z[t][targets[t]] - lse[t] with z = scale * hidden weight^T,
     its entropy (or None), and the ``top`` likeliest tokens' log probabilities
     and ids (int32)."""
+    d = _enum(dtype, DTYPE_NAMES, "dtype")
+    _typed(d, hidden=hidden, weight=weight)
+    _typed(AR_FLOAT32, log_probs=log_probs, entropy=entropy, lse=lse, top_log_probs=top_log_probs)
     x, ld_hidden = _rows(hidden, ld_hidden)
     w, ld_weight = _rows(weight, ld_weight)
     if not isinstance(top_ids, (int, type(None))) and top_ids.dtype != torch.int32:
@@ -530,8 +546,8 @@ def ar_linear_log_probs(comm, hidden, weight, targets, log_probs, entropy, lse, 
                                     None if entropy is None else _addr(entropy), _addr(lse), top,
                                     None if top_log_probs is None else _addr(top_log_probs),
                                     None if top_ids is None else _addr(top_ids), ntokens, vocab, width, ld_hidden,
-                                    ld_weight, scale, ignore_index, _enum(dtype, DTYPE_NAMES, "dtype"),
-                                    _stream(stream, _device(comm))), "ar_linear_log_probs")
+                                    ld_weight, scale, ignore_index, d, _stream(stream, _device(comm))),
+           "ar_linear_log_probs")
 
 
 def ar_linear_log_probs_backward(comm, hidden, weight, targets, lse, entropy, grad_log_probs, grad_entropy,
@@ -541,6 +557,9 @@ def ar_linear_log_probs_backward(comm, hidden, weight, targets, lse, entropy, gr
     """grad_hidden and grad_weight (either may be None) from lse, entropy and the
     gradients of each log probability and entropy (grad_entropy may be None, and
     entropy then too)."""
+    d = _enum(dtype, DTYPE_NAMES, "dtype")
+    _typed(d, hidden=hidden, weight=weight, grad_hidden=grad_hidden, grad_weight=grad_weight)
+    _typed(AR_FLOAT32, lse=lse, entropy=entropy, grad_log_probs=grad_log_probs, grad_entropy=grad_entropy)
     x, ld_hidden = _rows(hidden, ld_hidden)
     w, ld_weight = _rows(weight, ld_weight)
     gx, ld_grad_hidden = _rows(grad_hidden, ld_grad_hidden)
@@ -549,8 +568,8 @@ def ar_linear_log_probs_backward(comm, hidden, weight, targets, lse, entropy, gr
                                              None if entropy is None else _addr(entropy), _addr(grad_log_probs),
                                              None if grad_entropy is None else _addr(grad_entropy), gx, gw, ntokens,
                                              vocab, width, ld_hidden, ld_weight, ld_grad_hidden, ld_grad_weight, scale,
-                                             ignore_index, _enum(dtype, DTYPE_NAMES, "dtype"),
-                                             _stream(stream, _device(comm))), "ar_linear_log_probs_backward")
+                                             ignore_index, d, _stream(stream, _device(comm))),
+           "ar_linear_log_probs_backward")
 
 
 def ar_orthogonalize_workspace_bytes(nmatrices: int, rows: int, cols: int) -> int:
@@ -597,11 +616,13 @@ def ar_orthogonalize(comm, ins, outs, rows: int, cols: int, dtype, steps: int = 
     lists of matrices [rows][cols]. coefficients: (a, b, c), or three for each
     step."""
     _same_length("outs", len(outs), len(ins))
+    d = _enum(dtype, DTYPE_NAMES, "dtype")
+    _typed(d, ins=ins, outs=outs)
     p, ld_in = _matrices(ins, ld_in)
     q, ld_out = (p, ld_in) if outs is ins and not ld_out else _matrices(outs, ld_out)
     _check(_lib.ar_orthogonalize(_h(comm), len(ins), p, q, rows, cols, ld_in, ld_out, steps,
-                                 _coefficients(coefficients, steps), eps, _enum(dtype, DTYPE_NAMES, "dtype"),
-                                 _stream(stream, _device(comm))), "ar_orthogonalize")
+                                 _coefficients(coefficients, steps), eps, d, _stream(stream, _device(comm))),
+           "ar_orthogonalize")
 
 
 def ar_muon_update(comm, grads, momentum_in, momentum_out, weights_in, weights_out, rows: int, cols: int, dtype,
@@ -619,6 +640,10 @@ def ar_muon_update(comm, grads, momentum_in, momentum_out, weights_in, weights_o
                             ("weights_out", len(flat), n * nranks)):
         _same_length(what, got, want)
     d = _enum(dtype, DTYPE_NAMES, "dtype")
+    dw = d if weight_dtype is None else _enum(weight_dtype, DTYPE_NAMES, "weight_dtype")
+    _typed(d, grads=grads)
+    _typed(AR_FLOAT32, momentum_in=momentum_in, momentum_out=momentum_out)
+    _typed(dw, weights_in=weights_in, weights_out=flat)
     g, ld_grads = _matrices(grads, ld_grads)
     mi, ld_in = _matrices(momentum_in, ld_momentum)
     mo, ld_momentum = (mi, ld_in) if momentum_out is momentum_in else _matrices(momentum_out, ld_momentum)
@@ -628,6 +653,5 @@ def ar_muon_update(comm, grads, momentum_in, momentum_out, weights_in, weights_o
         raise ValueError("momentum_in and momentum_out, and weights_in and weights_out, have one row pitch each")
     _check(_lib.ar_muon_update(_h(comm), n, g, mi, mo, wi, wo, rows, cols, ld_grads, ld_momentum, ld_weights, decay,
                                1 if nesterov else 0, lr, weight_decay, update_scale, steps,
-                               _coefficients(coefficients, steps), eps, d,
-                               d if weight_dtype is None else _enum(weight_dtype, DTYPE_NAMES, "weight_dtype"),
-                               _stream(stream, _device(comm))), "ar_muon_update")
+                               _coefficients(coefficients, steps), eps, d, dw, _stream(stream, _device(comm))),
+           "ar_muon_update")
