@@ -582,11 +582,12 @@ def _matrices(bufs, ld: int):
     bufs = _flat(bufs)
     if not len(bufs) or isinstance(bufs[0], int):
         return _ptrs(bufs), ld
-    # rows alike, as in most lists: one look serves for all (a pitch below the width is refused with the call)
+    # rows alike, as in most lists: one look serves for all (a pitch below the width is refused with the
+    # call, but for an expanded tensor's 0, which would stand for dense rows there)
     if not ld:
         strides = {b.stride() for b in bufs}
         first = bufs[0].stride()
-        if len(strides) == 1 and len(first) == 2 and first[1] == 1 and bufs[0].shape[0] > 1:
+        if len(strides) == 1 and len(first) == 2 and first[0] and first[1] == 1 and bufs[0].shape[0] > 1:
             return _ptrs([b.data_ptr() for b in bufs]), first[0]
     rows = [_rows(b, ld) for b in bufs]
     if any(pitch != rows[0][1] for _, pitch in rows):
