@@ -694,6 +694,7 @@ ar_result_t check_log_probs(size_t vocab, float scale, int top)
 AR_EXPORT size_t ar_linear_log_probs_workspace_bytes(size_t ntokens, size_t vocab, size_t width, ar_dtype_t dtype,
                                                      int top, int backward)
 {
+    if (backward) top = 0;
     if (!valid_dtype(dtype) || dtype == AR_INT32 || width == 0 || !plan_fits(ntokens, vocab, width, dtype) || top < 0 ||
         top > ar::lm::kMostTop || (top && vocab >= kMostTopVocab))
         return static_cast<size_t>(-1);
