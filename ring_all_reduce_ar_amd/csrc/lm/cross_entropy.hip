@@ -569,9 +569,11 @@ uint64_t most_tiles(uint64_t ntokens, uint64_t tile_n)
     return (uint64_t(1) << 21) / (across ? across : 1);
 }
 
-// Up to so many tokens eight waves find the alternatives of one, since there
-// are CUs to spare.
-constexpr uint64_t kSelectFew = 512;
+// Up to so many tokens, one for each CU, eight waves find the alternatives of one.
+// Logits and alternatives by eight waves / by one, us, of 256 and of 384 tokens: 5 of
+// 32000 (x 64 bf16) 27 / 25 and 34 / 27, 20 of 65536 35 / 42 and 57 / 50, 50 of 131072
+// 122 / 178 and 218 / 197.
+constexpr uint64_t kSelectFew = 256;
 
 // What is larger than the last-level cache is stored around it: 8192 x 131072 x
 // 4096 bf16, loss and gradients, 25.3 -> 25.0 ms.

@@ -29,7 +29,8 @@ namespace {
 // rows, laid out as gemm_few has them, lie in LDS, all of their depth (which bounds
 // it). Laying the weight out first moves it three times: forward, us, by that and so,
 // 3 tokens x 88513 x 1157 bf16 149 / 75 (this kernel 66, 3.1 TB/s), 16 x 50000 x 3001
-// fp16 with 5 alternatives 239 / 152, 1 x 131072 x 999 fp32 437 / 102.
+// fp16 with 5 alternatives 239 / 152, 1 x 131072 x 999 fp32 437 / 102. With 4 / 8 / 16
+// loads under way the first takes 76 / 76 / 88 and the last 107 / 103 / 102.
 constexpr int kRowsThreads = 512, kRowsAhead = 8;
 constexpr uint32_t kRowsLds = 144 * 1024;
 
