@@ -514,10 +514,12 @@ _TENSOR_TYPES = {AR_FLOAT32: torch.float32, AR_FLOAT16: torch.float16, AR_BFLOAT
 def _typed(code: int, **bufs):
     """Tensors (alone or in lists) hold what the call takes them for: memory of
     another type would be read and written past its end."""
-    want = _TENSOR_TYPES.get(code)  # (a type that is none is refused with the call)
+    want = _TENSOR_TYPES.get(code)
+    if want is None:  # refused with the call
+        return
     for what, some in bufs.items():
         for b in some if isinstance(some, (list, tuple)) else (some,):
-            if want is not None and getattr(b, "dtype", want) != want:
+            if getattr(b, "dtype", want) is not want:
                 raise TypeError(f"{what}: the call takes {want}, not {b.dtype}")
 
 
@@ -618,7 +620,7 @@ def ar_orthogonalize(comm, ins, outs, rows: int, cols: int, dtype, steps: int = 
     step."""
     _same_length("outs", len(outs), len(ins))
     d = _enum(dtype, DTYPE_NAMES, "dtype")
-    _typed(d, ins=ins, outs=outs)
+    _typed(d, ins=ins, outs=() if outs is ins else outs)
     p, ld_in = _matrices(ins, ld_in)
     q, ld_out = (p, ld_in) if outs is ins and not ld_out else _matrices(outs, ld_out)
     _check(_lib.ar_orthogonalize(_h(comm), len(ins), p, q, rows, cols, ld_in, ld_out, steps,
@@ -643,7 +645,7 @@ def ar_muon_update(comm, grads, momentum_in, momentum_out, weights_in, weights_o
     d = _enum(dtype, DTYPE_NAMES, "dtype")
     dw = d if weight_dtype is None else _enum(weight_dtype, DTYPE_NAMES, "weight_dtype")
     _typed(d, grads=grads)
-    _typed(AR_FLOAT32, momentum_in=momentum_in, momentum_out=momentum_out)
+    _typed(AR_FLOAT32, momentum_in=momentum_in, momentum_out=() if momentum_out is momentum_in else momentum_out)
     _typed(dw, weights_in=weights_in, weights_out=flat)
     g, ld_grads = _matrices(grads, ld_grads)
     mi, ld_in = _matrices(momentum_in, ld_momentum)
