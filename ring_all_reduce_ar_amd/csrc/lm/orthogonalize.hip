@@ -29,6 +29,7 @@
 // twice.
 #include <algorithm>
 #include <cmath>
+#include <vector>
 
 #include "orthogonalize.h"
 
@@ -272,6 +273,7 @@ struct UpdateEpilogue {
 // ---------------------------------------------------------------------------
 constexpr uint32_t kCUs = 256;
 constexpr int kSegment = 3;  // steps
+constexpr double kMostTop = 4.0;
 constexpr double kMostGrowth = 144.0, kLateGrowth = 16.0;  // of errors of A in one
 
 // How a product goes through its tiles: of which size, and in how many parts
@@ -527,13 +529,13 @@ struct Group {
         default: return hipErrorInvalidValue;
         }
         if (e != hipSuccess) return e;
-        double top = 1.0;  // of the singular values
-        int turn = 0;      // which of xt holds X
+        const std::vector<StepBounds> bounds = l.segments ? bounds_of_steps() : std::vector<StepBounds>();
+        int turn = 0;  // which of xt holds X
         for (int k = 0; k < a.steps;) {
-            const int size = l.segments ? segment_size(k) : 1;
+            const int size = l.segments ? segment_size(k, bounds) : 1;
             const char* p;
             double p_scale;
-            if ((e = segment(x, square, k, size, &top, &p, &p_scale)) != hipSuccess) return e;
+            if ((e = segment(x, square, k, size, bounds, &p, &p_scale)) != hipSuccess) return e;
             k += size;
             const float unit = static_cast<float>(1.0 / p_scale);  // X keeps its 2^11
             if (k == a.steps) {
@@ -557,6 +559,29 @@ struct Group {
         return hipSuccess;  // not reached: there is at least one step
     }
 
+    // What a step makes of singular values of up to 1 before the first.
+    struct StepBounds {
+        double bracket;  // of the bracket's eigenvalues
+        double top;      // of the singular values after it; infinite from where they pass kMostTop
+    };
+    std::vector<StepBounds> bounds_of_steps() const
+    {
+        std::vector<StepBounds> all;
+        double top = 1.0;
+        for (int k = 0; k < a.steps; ++k) {
+            const double ca = a.coefficients[3 * k], cb = a.coefficients[3 * k + 1], cc = a.coefficients[3 * k + 2];
+            double bracket = 0.0, next = 0.0;
+            for (int j = 0; j <= 1000 && top <= kMostTop; ++j) {
+                const double v = top * j / 1000.0, u = std::fabs(ca + cb * v * v + cc * v * v * v * v);
+                bracket = std::max(bracket, u);
+                next = std::max(next, u * v);
+            }
+            top = top <= kMostTop && next * 1.001 <= kMostTop ? next * 1.001 : INFINITY;
+            all.push_back({std::max(bracket * 1.001, 1e-3), top});
+        }
+        return all;
+    }
+
     // The steps of the segment that starts with step k, up to three. In a segment an
     // error of A grows with a^2 a step but for the last, whose bracket takes it over.
     // The rounding of X at the segment's start, which steps by themselves have too,
@@ -568,7 +593,10 @@ struct Group {
     // growth / so / by steps: 3 steps of the default 9.8 / 2.8 / 2.6, 4 steps 8.0 / 4.1 /
     // 1.7, 5 steps 2.1 / 2.1 / 1.6, 8 steps 24 / 1.6 / 1.6, 5 steps of (8.3, -24, 17), (4.1,
     // -2.9, 0.5) .. 17 / 2.4 / 1.6, the first 3 of them 53 / 4.0 / 2.7.
-    int segment_size(int k) const
+    // The brackets' product is held at a scale for the largest singular values that
+    // there may be; where these would pass kMostTop, which those of the matrix need not,
+    // steps go by themselves.
+    int segment_size(int k, const std::vector<StepBounds>& bounds) const
     {
         auto growth = [&](int from, int to) {
             double g = 1.0;
@@ -578,14 +606,14 @@ struct Group {
         const double all = growth(k, a.steps) * 1.001;  // (equal products, in whatever order, are not more)
         const double most = std::min(all, k ? kLateGrowth : kMostGrowth);
         int size = std::min(a.steps - k, kSegment);
-        while (size > 1 && std::pow(growth(k, k + size - 1), 2) > most) --size;
+        while (size > 1 && (std::pow(growth(k, k + size - 1), 2) > most || bounds[k + size - 1].top > kMostTop)) --size;
         return size;
     }
 
     // Steps k .. k + size - 1 of X's rows `x`: *p is the product of their brackets,
-    // held times *p_scale. *top bounds the singular values before and after.
-    hipError_t segment(const char* x, char* const square[7], int k, int size, double* top, const char** p,
-                       double* p_scale) const
+    // held times *p_scale.
+    hipError_t segment(const char* x, char* const square[7], int k, int size, const std::vector<StepBounds>& bounds,
+                       const char** p, double* p_scale) const
     {
         char *d = square[0], *q[2] = {square[1], square[4]}, *gram = square[2], *t = square[3], *prod[2] = {square[5], square[6]};
         hipError_t e;
@@ -608,14 +636,7 @@ struct Group {
                 e = launch_halves(square_product(d, d), count, symmetric(bracket, cc, ca - cb * cb / (4.0 * cc)), s);
                 if (e != hipSuccess) return e;
             }
-            double most = 0.0, next = 0.0;
-            for (int j = 0; j <= 1000; ++j) {
-                const double v = *top * j / 1000.0, u = std::fabs(ca + cb * v * v + cc * v * v * v * v);
-                most = std::max(most, u);
-                next = std::max(next, u * v);
-            }
-            *top = next * 1.001;
-            largest *= std::max(most * 1.001, 1e-3);
+            if (size > 1) largest *= bounds[k + i].bracket;
             auto scale_of = [](double bound) { return kHalvesScale * std::exp2(-std::max(0.0, std::ceil(std::log2(bound / 8.0)))); };
             if (i == 0) {
                 *p = bracket;

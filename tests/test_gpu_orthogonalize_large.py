@@ -133,3 +133,23 @@ def test_update(comms, count, rows, cols, dtype, ranks):  # noqa: F811
         # (X's error times lr update_scale = 1, and the roundings of two products and their sum)
         assert off <= 8 * plain + 4 * U32 * (float(ref.norm()) + size), (off, plain, size)
         assert all(torch.equal(y, replicas[0]) for y in replicas)
+
+
+@pytest.mark.parametrize("rows,cols,count", [(770, 3000, 5), (3000, 770, 5), (520, 640, 2), (1100, 1300, 1)])
+def test_coefficients_that_singular_values_of_one_would_not_bear(comms, rows, cols, count):  # noqa: F811
+    """(0.5, 32, 32) takes small singular values to 0 and large ones beyond all bounds;
+    the matrices here have small ones. c D D of D = A + I / 2 is 16 times the bracket: each
+    step is off by up to 2^-17 of it, by the roundings of D and what a product leaves out."""
+    comm = workspace(comms, count, rows, cols)
+    g = gen(44)
+    ins = [normal(g, rows, cols) for _ in range(count)]
+    outs = [nan_like(rows, cols, dtype="f32") for _ in ins]
+    co, steps = (0.5, 32.0, 32.0), 5
+    ar.ar_orthogonalize(comm, ins, outs, rows, cols, "f32", steps=steps, coefficients=co)
+    for x, y in zip(ins, outs):
+        ref = iterate(x.double(), steps, co)
+        assert float((y.double() - ref).norm()) <= steps * 2.0 ** -17 * float(ref.norm())
+    for co in ((0.5, 32.0, 32.0), (4.0, 32.0, 32.0)):
+        zeros = [torch.zeros(rows, cols, device="cuda") for _ in range(count)]
+        ar.ar_orthogonalize(comm, zeros, outs, rows, cols, "f32", steps=32, coefficients=co)
+        assert all((y == 0).all() for y in outs)
