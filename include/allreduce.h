@@ -485,7 +485,8 @@ size_t ar_orthogonalize_workspace_bytes(int nmatrices, size_t rows, size_t cols)
  * same. coefficients (host): a, b and c of every step, or NULL for 3.4445,
  * -4.7750, 2.0315 in each; |a| is at most 16, |b| and |c| at most 32, and c is 0 or
  * so large that |b| <= 16 |c| and b^2 <= 64 |c|. Sums are fp32 or fp64; X and what
- * is made of it is held to 22 bits, within |x| < 32 (beyond, results are NaN).
+ * is made of it is held to 22 bits, below 2^-13 in steps of 2^-35, within |x| < 32
+ * (beyond, results are NaN).
  * A matrix that holds a NaN or an infinity, or whose iteration diverges, gives
  * NaN; one of zeros gives zeros. in and out are of dtype. In place (in[t] ==
  * out[t] of one pitch) is allowed; what a matrix spans with its pitch overlaps no

@@ -2,10 +2,13 @@
 //
 //   x 2^11 = hi + lo,  hi = fp16(x 2^11),  lo = fp16(x 2^11 - hi)
 //
-// hi + lo holds 22 bits of x (and all of a x below 2^-24 to steps of 2^-36);
-// of the four products of a pair, lo lo is left out, at 2^-22 of the whole, and
-// hi lo, lo hi and hi hi are summed in fp32: three matrix instructions where
-// one fp32 product of the library's takes as long as eight. |x| is below 32.
+// hi + lo holds 22 bits of x; below |x| = 2^-13, where lo is subnormal, it holds x in
+// steps of 2^-35. The elements of a matrix of norm 1 are about 1 / sqrt(rows cols),
+// 2^-12.5 of 4096 x 8192, 2^-17 of the largest taken: five steps on such, simulated,
+// are off by 1.2-1.5 times what 22 bits of every element would leave. Of the four products of a pair, lo lo is left out,
+// at 2^-22 of the whole, and hi lo, lo hi and hi hi are summed in fp32: three matrix
+// instructions where one fp32 product of the library's takes as long as eight. |x| is
+// below 32.
 //
 // A row holds, for each 32 of its depth, 32 hi and 32 lo: 128 bytes, the row of
 // a stage in LDS, its 16-byte columns permuted as gemm.h's.
@@ -262,7 +265,7 @@ __device__ __forceinline__ void multiply_halves(char* lds, const char* a, const 
             read_few<2, 2>(fa, fb, xa, xa ^ 64, xb, xb ^ 64);
         }
         constexpr int kOfA[3] = {0, 1, 0}, kOfB[3] = {1, 0, 0};  // the smaller products first
-        // (of 48 products, ahead of the other workgroup's reads: 4096 x 8192 4.63 -> 4.51 ms;
+        // (of 48 products, ahead of the other workgroup's reads: 4096 x 8192 4.64 -> 4.54 ms;
         // of 12 it costs: 3 x 1027 x 770 271 -> 274 us)
         if constexpr (B == 128) __builtin_amdgcn_s_setprio(1);
 #pragma unroll

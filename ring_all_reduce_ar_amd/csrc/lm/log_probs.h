@@ -521,7 +521,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void select_top(const LogPar
 // ---------------------------------------------------------------------------
 // d of a row is held over the row's larger gradient g = s max(|a|, |b|): |p
 // (log p + H)| is below 6 for a vocabulary of 2^28, so that 2^12 d stays within
-// fp16, where its steps are then 2^-36.
+// fp16, where its steps are then 2^-36. Rounding d to the operands' 16 bits, which the
+// matrix cores want, shows in bf16: gradients of 6000 x 131072 x 4096 are off by 0.0024
+// of their size, where a d of fp32 and one rounding at the end are off by 0.0017; in
+// fp16 (2048 x 32000 x 1024) by 0.00074 either way.
 constexpr float kLogProbBits = 12.0f, kLogProbScale = 4096.0f;
 
 struct RowGradients {

@@ -20,8 +20,8 @@
 // Small singular values grow by a factor of a in each step (485 in five of them),
 // and what a rounding adds to X grows alike: in bf16, results are off by 4-30%, in
 // fp16 by up to 6% of their norm's largest element. X, D and the bracket are held as two
-// fp16 numbers each (gemm_halves.h), 22 bits, whose results are those of fp32
-// products.
+// fp16 numbers each (gemm_halves.h), 22 bits, whose results are off by as much as those
+// of fp32 products, up to four times that, or by about 1e-6 of the result.
 //
 // Products want both operands contiguous along the sum: A = X X^T takes X by
 // rows, the last one X by columns, so X is written in both orders. The smaller
@@ -288,10 +288,14 @@ constexpr uint64_t kPartialBytes = uint64_t(2 * kCUs) * 128 * 128 * 4;
 
 // Microseconds that fit the products measured, to within a fifth: a step of 32 with
 // all slots taken (two workgroups a CU; one of 256), with half of them, and what a
-// full round and a last one cost beside their steps. 4096 x 8192 x 4096: 481 us in
-// tiles of 256, 596 of 128, 873 of 64; 8 symmetric 1024 x 1024 x 1024: 58, 43 and 38.
-// The parts of split tiles are joined by a launch of its own: symmetric 4096 x 4096 x
-// 4096, 16 tiles of 128 behind a round of 512, 217 us whole, 169 in four parts, 192 in 32.
+// full round and a last one cost beside their steps. The same product 400 times on
+// end, 4096 x 8192 x 4096: 530 us in tiles of 256, 615 of 128, 893 of 64; 8 symmetric
+// 1024 x 1024 x 1024: 58, 37 and 39. The parts of split tiles are joined by a launch of
+// its own: symmetric 4096 x 4096 x 4096, 16 tiles of 128 behind a round of 512, 230 us
+// whole, 177 in four parts, 175 in twelve, 193 in 32. Boxes differ by a tenth and more
+// (271, 204, 208 and 263 on another), and between a call's other products, at the
+// power limit, the first takes 635 and the last 192 + 16 for the join; the forms' order
+// is the same.
 struct TileCost {
     int tile;
     uint32_t slots;
@@ -341,7 +345,8 @@ struct Layout {
 // Whether steps go in segments: products of the smaller side alone, 14 in five
 // steps beside two of each with the larger one, or five of each kind; what a
 // launch costs beside its product decides for small ones. By steps / in segments,
-// us: 3 x 1027 x 770 281 / 291, 4 x 64 x 192 72 / 82, 8 x 2048 x 4096 7468 / 5386.
+// us: 3 x 1027 x 770 281 / 291, 4 x 64 x 192 72 / 82, 2 x 2100 x 1030 464 / 410, 5 x 770
+// x 3000 603 / 454, 4096 x 8192 5470 / 4490, 8 x 2048 x 4096 6060 / 5080.
 bool in_segments(uint64_t m, uint64_t n, uint64_t count)
 {
     constexpr double kLaunch = 2.0;

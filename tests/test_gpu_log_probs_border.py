@@ -9,6 +9,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("n", [255, 256, 257, 400, 512, 513])
-@pytest.mark.parametrize("vocab,width,top,dtype", [(999, 64, 5, "bf16"), (4099, 72, 20, "f16"), (9000, 64, 64, "bf16"), (700, 33, 9, "f32")])
+@pytest.mark.parametrize("vocab,width,top,dtype", [(999, 64, 5, "bf16"), (4099, 72, 20, "f16"), (9000, 64, 64, "bf16"),
+                                                   (700, 33, 9, "f32")])
 def test_alternatives(comms, n, vocab, width, top, dtype):  # noqa: F811
     check_top(comms, n, vocab, width, dtype, top)
