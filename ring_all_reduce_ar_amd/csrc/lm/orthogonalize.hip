@@ -15,7 +15,7 @@
 // steps costs m^2 (n + (4k - 3) m + 2n) products (of half of a symmetric result)
 // where steps by themselves take k m^2 (3n + m). Errors of A for small singular
 // values grow with a^2 a step there, in X with a, which bounds a segment's length
-// (segment_size): the default's five steps go as three and two.
+// (segment_size): the default's five steps mostly go as three and two.
 //
 // Small singular values grow by a factor of a in each step (485 in five of them),
 // and what a rounding adds to X grows alike: in bf16, results are off by 4-30%, in
@@ -274,7 +274,7 @@ struct UpdateEpilogue {
 constexpr uint32_t kCUs = 256;
 constexpr int kSegment = 3;  // steps
 constexpr double kMostTop = 4.0;
-constexpr double kMostGrowth = 144.0, kLateGrowth = 16.0;  // of errors of A in one
+constexpr double kLateGrowth = 16.0, kAnyGrowth = 4.0;  // of errors of A in one
 
 // How a product goes through its tiles: of which size, and in how many parts
 // those behind the last full round of workgroups are split.
@@ -590,14 +590,17 @@ struct Group {
     // The steps of the segment that starts with step k, up to three. In a segment an
     // error of A grows with a^2 a step but for the last, whose bracket takes it over.
     // The rounding of X at the segment's start, which steps by themselves have too,
-    // grows with a in every step to come: the former may grow no more than that, nor
-    // by more than kMostGrowth, or kLateGrowth behind the first segment, where A has the
-    // size 1 whatever the matrix was and much of it has yet to grow. Largest errors of
-    // 30 kinds of singular values as multiples of those of fp32 products (where either
-    // is above 1e-6 of the result), 5 of 770 x 3000, in segments of three whatever the
-    // growth / so / by steps: 3 steps of the default 9.8 / 2.8 / 2.6, 4 steps 8.0 / 4.1 /
-    // 1.7, 5 steps 2.1 / 2.1 / 1.6, 8 steps 24 / 1.6 / 1.6, 5 steps of (8.3, -24, 17), (4.1,
-    // -2.9, 0.5) .. 17 / 2.4 / 1.6, the first 3 of them 53 / 4.0 / 2.7.
+    // grows with a in every step to come: the former may grow no more than that. In the
+    // first segment A is known to little more than its largest singular values' part,
+    // whose rounding weighs the more the fewer rows there are: growth up to m / 2. In
+    // later ones A has the size 1 whatever the matrix was: up to kLateGrowth, and half
+    // of what singular values have grown so far. (Up to kAnyGrowth is no matter.)
+    // Largest errors of 30 kinds of singular values as multiples of those of fp32
+    // products (where either is above 1e-6 of the result), 5 of 770 x 3000, in segments
+    // of three whatever the growth / so / by steps: 3 steps of the default 9.8 / 2.8 / 2.6, 4
+    // steps 8.0 / 4.1 / 1.7, 5 steps 2.1 / 2.1 / 1.6, 8 steps 24 / 1.6 / 1.6, 5 steps of (8.3,
+    // -24, 17), (4.1, -2.9, 0.5) .. 17 / 2.4 / 1.6, the first 3 of them 53 / 4.0 / 2.7; 5
+    // steps of the default of 40 x 883, simulated, 21 / 1.5 / 2.0.
     // The brackets' product is held at a scale for the largest singular values that
     // there may be; where these would pass kMostTop, which those of the matrix need not,
     // steps go by themselves.
@@ -609,7 +612,8 @@ struct Group {
             return g;
         };
         const double all = growth(k, a.steps) * 1.001;  // (equal products, in whatever order, are not more)
-        const double most = std::min(all, k ? kLateGrowth : kMostGrowth);
+        const double own = k ? std::min(growth(0, k) / 2, kLateGrowth) : static_cast<double>(l.m) / 2;
+        const double most = std::min(all, std::max(own, kAnyGrowth));
         int size = std::min(a.steps - k, kSegment);
         while (size > 1 && (std::pow(growth(k, k + size - 1), 2) > most || bounds[k + size - 1].top > kMostTop)) --size;
         return size;

@@ -153,3 +153,17 @@ def test_coefficients_that_singular_values_of_one_would_not_bear(comms, rows, co
         zeros = [torch.zeros(rows, cols, device="cuda") for _ in range(count)]
         ar.ar_orthogonalize(comm, zeros, outs, rows, cols, "f32", steps=32, coefficients=co)
         assert all((y == 0).all() for y in outs)
+
+
+@pytest.mark.parametrize("steps", [4, 5, 6, 8])
+@pytest.mark.parametrize("rows,cols", [(40, 883), (72, 1100), (1222, 106), (1409, 49), (128, 2500), (256, 1024), (300, 2000)])
+def test_thin_matrices_with_one_large_singular_value(comms, rows, cols, steps):  # noqa: F811
+    """Few rows: a rounding of A weighs the more beside the others' part of it."""
+    comm = workspace(comms, 9, rows, cols)
+    g = gen(45)
+    ins = [normal(g, rows, rank) @ normal(g, rank, cols) + noise * normal(g, rows, cols)
+           for rank in (1, 4, 16) for noise in (1.0, 0.5, 0.3)]
+    outs = [nan_like(rows, cols, dtype="f32") for _ in ins]
+    ar.ar_orthogonalize(comm, ins, outs, rows, cols, "f32", steps=steps)
+    for x, y in zip(ins, outs):
+        check_as_fp32(x, y, "f32", steps)
