@@ -592,14 +592,15 @@ struct Group {
     // The rounding of X at the segment's start, which steps by themselves have too,
     // grows with a in every step to come: the former may grow no more than that. In the
     // first segment A is known to little more than its largest singular values' part,
-    // whose rounding weighs the more the fewer rows there are: growth up to m / 2. In
-    // later ones A has the size 1 whatever the matrix was: up to kLateGrowth, and half
-    // of what singular values have grown so far. (Up to kAnyGrowth is no matter.)
+    // whose rounding weighs the more the fewer rows there are: growth up to half of that
+    // and m / 2. In later ones A has the size 1 whatever the matrix was: up to
+    // kLateGrowth, and half of what singular values have grown so far. (Up to kAnyGrowth
+    // is no matter.)
     // Largest errors of 30 kinds of singular values as multiples of those of fp32
     // products (where either is above 1e-6 of the result), 5 of 770 x 3000, in segments
     // of three whatever the growth / so / by steps: 3 steps of the default 9.8 / 2.8 / 2.6, 4
-    // steps 8.0 / 4.1 / 1.7, 5 steps 2.1 / 2.1 / 1.6, 8 steps 24 / 1.6 / 1.6, 5 steps of (8.3,
-    // -24, 17), (4.1, -2.9, 0.5) .. 17 / 2.4 / 1.6, the first 3 of them 53 / 4.0 / 2.7; 5
+    // steps 8.0 / 1.4 / 1.7, 5 steps 2.1 / 2.1 / 1.6, 8 steps 24 / 1.6 / 1.6, 5 steps of (8.3,
+    // -24, 17), (4.1, -2.9, 0.5) .. 17 / 2.4 / 1.6, the first 3 of them 53 / 2.7 / 2.7; 5
     // steps of the default of 40 x 883, simulated, 21 / 1.5 / 2.0.
     // The brackets' product is held at a scale for the largest singular values that
     // there may be; where these would pass kMostTop, which those of the matrix need not,
@@ -612,8 +613,8 @@ struct Group {
             return g;
         };
         const double all = growth(k, a.steps) * 1.001;  // (equal products, in whatever order, are not more)
-        const double own = k ? std::min(growth(0, k) / 2, kLateGrowth) : static_cast<double>(l.m) / 2;
-        const double most = std::min(all, std::max(own, kAnyGrowth));
+        const double most = std::max(kAnyGrowth, k ? std::min({all, growth(0, k) / 2, kLateGrowth})
+                                                   : std::min(all, static_cast<double>(l.m)) / 2);
         int size = std::min(a.steps - k, kSegment);
         while (size > 1 && (std::pow(growth(k, k + size - 1), 2) > most || bounds[k + size - 1].top > kMostTop)) --size;
         return size;
